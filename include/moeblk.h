@@ -397,6 +397,173 @@ int moe_post_expert(const moe_proj_dims* dims, const float* partial, const void*
 int moe_topk(const moe_dims* dims, const float* logits, const float* bias, int32_t* topk_ids,
              float* topk_w, hipStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* FP8 weights: products with block-128 scales                               */
+/* ------------------------------------------------------------------------ */
+
+/* The same dense projections and expert FFNs on weights held as OCP e4m3 (8
+ * bits, largest value 448, no infinities) with one fp32 scale per 128 x 128
+ * block (weight = scale x value), times rows held as e4m3 with one scale per
+ * row and 128 columns.
+ * Sizes (elements). Supported ranges: 1 <= M <= 262144; 1 <= N <= 32768;
+ * 1 <= K <= 32768 (any of them odd); in_type, out_type in {MOE_BF16,
+ * MOE_FP32}. Kb = ceil(K / 128) and Nb = ceil(N / 128) are the numbers of
+ * blocks, Kp = 128 Kb. */
+#define MOE_BF16 0
+#define MOE_FP32 1
+typedef struct moe_fp8_dims {
+  int32_t M;        /* rows (tokens) */
+  int32_t N;        /* weight rows = outputs a token */
+  int32_t K;        /* input width */
+  int32_t in_type;  /* x of moe_fp8_quant and moe_fp8_proj */
+  int32_t out_type; /* out of moe_fp8_gemm and moe_fp8_proj */
+} moe_fp8_dims;
+
+/* Host-only check of `dims`: MOE_OK, MOE_ERR_NULL, _SHAPE or _UNSUPPORTED. */
+int moe_check_fp8_dims(const moe_fp8_dims* dims);
+
+/* Rows to e4m3 (reads dims->M, K, in_type; N and out_type must be in range).
+ *   x  [M, K] in_type;
+ *   xq [M, Kp] e4m3, written: column k of block j = k / 128 is e4m3(x / s),
+ *      rounded to nearest even; columns K .. Kp - 1 are zero;
+ *   xs [Kb, M] fp32, written: s = 2^e with the smallest integer e >= -126 such
+ *      that the block's largest |x| is at most 448 * 2^e (a zero block: 2^-126).
+ *      Division by a power of two is exact, so a value is rounded once. A block
+ *      that holds an infinity or a NaN gets s = NaN and NaN values. */
+int moe_fp8_quant(const moe_fp8_dims* dims, const void* x, void* xq, float* xs,
+                  hipStream_t stream);
+
+/* Packed size of an FP8 weight [N, K] (0 if `dims` is invalid) and its packing
+ * into the kernels' tile order:
+ *   q      [N, K] e4m3 bytes;  scales [Nb, Kb] fp32, any value;
+ *   packed [moe_packed_fp8_bytes(dims)], written. Opaque: only moe_fp8_gemm
+ *          and moe_fp8_proj read it. It depends on N and K alone. */
+size_t moe_packed_fp8_bytes(const moe_fp8_dims* dims);
+int moe_pack_fp8(const moe_fp8_dims* dims, const void* q, const float* scales, void* packed,
+                 hipStream_t stream);
+
+/* The product of quantised rows and a packed weight:
+ *   out[t][n] = sum over K blocks j of xs[j][t] * scales[n / 128][j] *
+ *               (sum over the block's k of xq[t][k] * q[n][k])
+ *   xq, xs   as moe_fp8_quant writes them; any fp32 scales are taken (rows
+ *            quantised elsewhere included), columns K .. Kp - 1 must be finite;
+ *   out      [M, N] out_type, written: fp32 accumulation in a fixed order
+ *            (deterministic), one rounding; NaNs and infinite scales propagate;
+ *   workspace device scratch of at least moe_fp8_gemm_workspace_bytes. It must
+ *            be zero-filled once before its first use; every call leaves it
+ *            ready for the next, with any dims of no larger workspace. Calls
+ *            sharing it must not overlap. */
+size_t moe_fp8_gemm_workspace_bytes(const moe_fp8_dims* dims);
+int moe_fp8_gemm(const moe_fp8_dims* dims, const void* xq, const float* xs, const void* w_packed,
+                 void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* moe_fp8_quant of x and moe_fp8_gemm in one call, with identical outputs (the
+ * quantised rows live in the workspace).
+ *   x [M, K] in_type; out [M, N] out_type; workspace: moe_fp8_gemm's rules. */
+size_t moe_fp8_proj_workspace_bytes(const moe_fp8_dims* dims);
+int moe_fp8_proj(const moe_fp8_dims* dims, const void* x, const void* w_packed, void* out,
+                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The expert FFNs on FP8 weights. Packing (once): `which` is MOE_W13 / MOE_W2
+ * (the n_local routed experts) or MOE_WS13 / MOE_WS2 (the shared expert, needs
+ * shared_I > 0):
+ *   q      [n, N, K] e4m3 bytes, scales [n, N / 128, K / 128] fp32, with n =
+ *          n_local or 1, and N, K as for MOE_W13 / MOE_W2 (rows [0, I) gate, then up);
+ *   packed [moe_packed_fp8_expert_bytes(dims, which)], written. Opaque: only
+ *          moe_fp8_expert_ffn reads it. */
+#define MOE_WS13 2 /* the shared expert's gate_up */
+#define MOE_WS2 3  /* the shared expert's down */
+size_t moe_packed_fp8_expert_bytes(const moe_dims* dims, int which);
+int moe_pack_fp8_expert(const moe_dims* dims, int which, const void* q, const float* scales,
+                        void* packed, hipStream_t stream);
+
+/* moe_expert_ffn on such weights: for every bucket row r of local expert el
+ * (token t = rows[r]), with Q the quantisation of moe_fp8_quant and the product
+ * of moe_fp8_gemm,
+ *   gu = Q(x[t]) . W13[el]^T          (fp32)
+ *   h  = silu(gu[0:I]) * gu[I:2I]     (fp32)
+ *   y[r] = bf16( Q(h) . W2[el]^T ),
+ * and, if shared_I > 0, the same chain on every token t with the shared weights
+ * into y[R_max + t]. Between x and y the values are rounded only where they are
+ * quantised (moe_expert_ffn rounds gu and h to bf16).
+ *   x, counts, offsets, rows, active, y: as for moe_expert_ffn (all four
+ *              moe_bucket outputs are read here), so that moe_bucket feeds this
+ *              call and moe_combine takes its y;
+ *   w13_packed .. ws2_packed: moe_pack_fp8_expert outputs (ws*: NULL when
+ *              shared_I == 0);
+ *   workspace  device scratch of at least moe_fp8_ffn_workspace_bytes(dims),
+ *              zero-filled once before its first use. A workspace used with
+ *              other dims must be zero-filled again. Calls sharing it must not
+ *              overlap. */
+size_t moe_fp8_ffn_workspace_bytes(const moe_dims* dims);
+int moe_fp8_expert_ffn(const moe_dims* dims, const void* x, const void* w13_packed,
+                       const void* w2_packed, const int32_t* counts, const int32_t* offsets,
+                       const int32_t* rows, const int32_t* active, const void* ws13_packed,
+                       const void* ws2_packed, void* y, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* the router's balance: per-expert counts, loss and gradient                */
+/* ------------------------------------------------------------------------ */
+
+/* T token rows, packed into n_seq sequences: sequence b is rows seq_starts[b] ..
+ * seq_starts[b + 1] - 1 (T_b of them; none is allowed). Rows outside every
+ * sequence (in front of the first, behind the last) are not looked at.
+ * Supported ranges: 1 <= T <= 2^22; 1 <= E <= 256; 1 <= topk <= 8, topk <= E;
+ * 1 <= n_seq <= 4096; coef finite. */
+#define MOE_SCORE_SIGMOID 0 /* p = sigmoid(l) / sum over E of sigmoid(l): moe_route's scores */
+#define MOE_SCORE_SOFTMAX 1 /* p = softmax(l) */
+typedef struct moe_balance_dims {
+  int32_t T;     /* token rows */
+  int32_t E;     /* experts routed over */
+  int32_t topk;  /* picks per token */
+  int32_t n_seq; /* sequences */
+  int32_t score; /* MOE_SCORE_SIGMOID or MOE_SCORE_SOFTMAX */
+  float coef;    /* factor of the loss */
+} moe_balance_dims;
+
+/* Host-only check of `dims`: MOE_OK, MOE_ERR_NULL, _SHAPE or _UNSUPPORTED. */
+int moe_check_balance_dims(const moe_balance_dims* dims);
+
+/* Scratch of moe_expert_counts and moe_balance_loss (0 if `dims` is invalid):
+ * zero-filled once before its first use; every call leaves it ready for the
+ * next, with any dims of no larger workspace. Calls sharing it must not overlap. */
+size_t moe_balance_workspace_bytes(const moe_balance_dims* dims);
+
+/* Picks per expert of every sequence, over all E experts (moe_bucket counts the
+ * local ones of one step).
+ *   topk_ids   [T, topk] int32 (moe_route, moe_topk); an id outside [0, E) is
+ *              not counted (a padded pick), an id twice in a row counts twice;
+ *   seq_starts [n_seq + 1] int32, ascending, within 0 .. T (values outside are
+ *              taken as the nearer end), or NULL when n_seq == 1: all T rows;
+ *   counts     [n_seq, E] int32, written. */
+int moe_expert_counts(const moe_balance_dims* dims, const int32_t* topk_ids,
+                      const int32_t* seq_starts, int32_t* counts, void* workspace,
+                      size_t workspace_bytes, hipStream_t stream);
+
+/* The balance loss: with p[t] the normalised scores of row t and c the counts,
+ *   probs[b][e] = mean of p[t][e] over the sequence's rows (0 without rows),
+ *   loss = coef / n_seq * sum_b sum_e E / (topk T_b) * c[b][e] * probs[b][e].
+ *   logits [T, E] fp32 (moe_route's or moe_pre_expert's); -inf leaves an expert
+ *          out (p = 0), a row whose logits are all -inf adds nothing to probs;
+ *   counts [n_seq, E] int32, probs [n_seq, E] fp32, loss [1] fp32, written.
+ * Sums run in a fixed order, across rows in fp64 beyond 64 of them. */
+int moe_balance_loss(const moe_balance_dims* dims, const float* logits, const int32_t* topk_ids,
+                     const int32_t* seq_starts, int32_t* counts, float* probs, float* loss,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Its gradient with respect to the logits, the counts held constant: with
+ * a[e] = dloss coef / n_seq * E / (topk T_b^2) * counts[b][e],
+ *   dlogits[t][j] = p_j (1 - sigmoid(l_j)) (a_j - sum_e a_e p_e)   (sigmoid)
+ *   dlogits[t][j] = p_j (a_j - sum_e a_e p_e)                      (softmax).
+ *   counts  moe_balance_loss's (or moe_expert_counts');
+ *   dloss   [1] fp32, the gradient of the loss, or NULL for 1;
+ *   dlogits [T, E] fp32, written for the rows of a sequence; other rows are
+ *           left as they were. */
+int moe_balance_backward(const moe_balance_dims* dims, const float* logits, const int32_t* counts,
+                         const int32_t* seq_starts, const float* dloss, float* dlogits,
+                         hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

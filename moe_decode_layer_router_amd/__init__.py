@@ -49,6 +49,33 @@ __all__ = [
     "moe_topk",
     "MOE_W13",
     "MOE_W2",
+    "MoeFp8Dims",
+    "fp8_dims_from",
+    "moe_check_fp8_dims",
+    "moe_fp8_quant",
+    "moe_packed_fp8_bytes",
+    "moe_pack_fp8",
+    "moe_fp8_gemm_workspace_bytes",
+    "moe_fp8_gemm",
+    "moe_fp8_proj_workspace_bytes",
+    "moe_fp8_proj",
+    "moe_packed_fp8_expert_bytes",
+    "moe_pack_fp8_expert",
+    "moe_fp8_ffn_workspace_bytes",
+    "moe_fp8_expert_ffn",
+    "MOE_WS13",
+    "MOE_WS2",
+    "MOE_BF16",
+    "MOE_FP32",
+    "MoeBalanceDims",
+    "balance_dims_from",
+    "moe_check_balance_dims",
+    "moe_balance_workspace_bytes",
+    "moe_expert_counts",
+    "moe_balance_loss",
+    "moe_balance_backward",
+    "MOE_SCORE_SIGMOID",
+    "MOE_SCORE_SOFTMAX",
 ]
 
 MOE_OK = 0
@@ -60,6 +87,12 @@ MOE_ERR_WORKSPACE = -5
 MOE_ERR_HIP = -6
 MOE_W13 = 0
 MOE_W2 = 1
+MOE_WS13 = 2
+MOE_WS2 = 3
+MOE_BF16 = 0
+MOE_FP32 = 1
+MOE_SCORE_SIGMOID = 0
+MOE_SCORE_SOFTMAX = 1
 MOE_STATIC_SCRATCH_BYTES = 16 << 20  # moe_forward_static's static scratch a GPU
 
 
@@ -95,6 +128,27 @@ class MoeProjDims(ctypes.Structure):
         ("E", ctypes.c_int32),
         ("bias_mode", ctypes.c_int32),
         ("eps", ctypes.c_float),
+    ]
+
+
+class MoeFp8Dims(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("in_type", ctypes.c_int32),
+        ("out_type", ctypes.c_int32),
+    ]
+
+
+class MoeBalanceDims(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32),
+        ("E", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("n_seq", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("coef", ctypes.c_float),
     ]
 
 
@@ -157,6 +211,31 @@ def lib() -> ctypes.CDLL:
         L.moe_latent_norm.argtypes = [_PD, _P, _P, _P, _P]
         L.moe_post_expert.argtypes = [_PD] + [_P] * 4 + [ctypes.c_size_t, _P]
         L.moe_topk.argtypes = [_DP, _P, _P, _P, _P, _P]
+        _FD, _BD, _Z = ctypes.POINTER(MoeFp8Dims), ctypes.POINTER(MoeBalanceDims), ctypes.c_size_t
+        for f, dims in (
+            ("moe_packed_fp8_bytes", _FD), ("moe_fp8_gemm_workspace_bytes", _FD),
+            ("moe_fp8_proj_workspace_bytes", _FD), ("moe_fp8_ffn_workspace_bytes", _DP),
+            ("moe_balance_workspace_bytes", _BD),
+        ):
+            getattr(L, f).argtypes = [dims]
+            getattr(L, f).restype = _Z
+        L.moe_packed_fp8_expert_bytes.argtypes = [_DP, ctypes.c_int]
+        L.moe_packed_fp8_expert_bytes.restype = _Z
+        for f, args in (
+            ("moe_check_fp8_dims", [_FD]),
+            ("moe_fp8_quant", [_FD] + [_P] * 4),
+            ("moe_pack_fp8", [_FD] + [_P] * 4),
+            ("moe_fp8_gemm", [_FD] + [_P] * 5 + [_Z, _P]),
+            ("moe_fp8_proj", [_FD] + [_P] * 4 + [_Z, _P]),
+            ("moe_pack_fp8_expert", [_DP, ctypes.c_int] + [_P] * 4),
+            ("moe_fp8_expert_ffn", [_DP] + [_P] * 11 + [_Z, _P]),
+            ("moe_check_balance_dims", [_BD]),
+            ("moe_expert_counts", [_BD] + [_P] * 4 + [_Z, _P]),
+            ("moe_balance_loss", [_BD] + [_P] * 7 + [_Z, _P]),
+            ("moe_balance_backward", [_BD] + [_P] * 6),
+        ):
+            getattr(L, f).argtypes = args
+            getattr(L, f).restype = ctypes.c_int
         for f in (
             "moe_pack_mxfp4", "moe_pack_bf16", "moe_route", "moe_bucket", "moe_expert_ffn", "moe_combine",
             "moe_forward", "moe_forward_static", "moe_forward_one_launch", "moe_check_proj_dims", "moe_pack_dense", "moe_pre_expert", "moe_latent_norm",
@@ -385,4 +464,220 @@ def moe_topk(dims, logits, bias, topk_ids, topk_w, stream=None) -> None:
     _call(
         "moe_topk", ctypes.byref(_d(dims)), _ptr(logits), _ptr(bias), _ptr(topk_ids), _ptr(topk_w),
         _stream(stream),
+    )
+
+
+# ---------------------------------------------------------------- FP8 weights
+
+
+def _buf(t, name: str, n: int, kinds: tuple[str, ...], device: int):
+    """The pointer of a tensor of ``n`` elements or more (None -> NULL) on GPU
+    ``device``: the calls below launch on the current device's stream."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name}: tensor is not on the current GPU device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor is not contiguous")
+    if str(t.dtype) not in kinds:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {', '.join(kinds)}")
+    if t.numel() < n:
+        raise ValueError(f"{name}: {t.numel()} elements, {n} are needed")
+    return t.data_ptr()
+
+
+_F32 = ("torch.float32",)
+_I32 = ("torch.int32",)
+_BF16 = ("torch.bfloat16",)
+_E4M3 = ("torch.float8_e4m3fn", "torch.uint8")
+_BYTES = ("torch.uint8",)
+_ROWS = (_BF16, _F32)  # by MOE_BF16 / MOE_FP32
+
+
+def _device() -> int:
+    import torch
+
+    return torch.cuda.current_device()
+
+
+def _workspace(ws, workspace_bytes, device: int):
+    ptr = _buf(ws, "workspace", 0, _BYTES, device)
+    return ptr, ctypes.c_size_t(ws.numel() if workspace_bytes is None and ws is not None else workspace_bytes or 0)
+
+
+def _refuse(fn: str, code: int) -> None:
+    if code != MOE_OK:
+        raise MoeError(fn, code)
+
+
+def fp8_dims_from(cfg) -> MoeFp8Dims:
+    """MoeFp8Dims from an object or dict with the moe_fp8_dims field names."""
+    get = cfg.get if isinstance(cfg, dict) else (lambda k, dflt=None: getattr(cfg, k, dflt))
+    return MoeFp8Dims(
+        M=get("M"), N=get("N", 1), K=get("K"), in_type=get("in_type", MOE_BF16), out_type=get("out_type", MOE_BF16),
+    )
+
+
+def _fd(dims) -> MoeFp8Dims:
+    return dims if isinstance(dims, MoeFp8Dims) else fp8_dims_from(dims)
+
+
+def moe_check_fp8_dims(dims) -> int:
+    return lib().moe_check_fp8_dims(ctypes.byref(_fd(dims)))
+
+
+def moe_packed_fp8_bytes(dims) -> int:
+    return lib().moe_packed_fp8_bytes(ctypes.byref(_fd(dims)))
+
+
+def moe_fp8_gemm_workspace_bytes(dims) -> int:
+    return lib().moe_fp8_gemm_workspace_bytes(ctypes.byref(_fd(dims)))
+
+
+def moe_fp8_proj_workspace_bytes(dims) -> int:
+    return lib().moe_fp8_proj_workspace_bytes(ctypes.byref(_fd(dims)))
+
+
+def moe_fp8_quant(dims, x, xq, xs, stream=None) -> None:
+    """x [M, K] -> xq [M, Kp] e4m3 (torch.float8_e4m3fn or uint8), xs [Kb, M] fp32."""
+    d, dev = _fd(dims), _device()
+    _refuse("moe_fp8_quant", moe_check_fp8_dims(d))
+    kb = -(-d.K // 128)
+    _call(
+        "moe_fp8_quant", ctypes.byref(d), _buf(x, "x", d.M * d.K, _ROWS[d.in_type], dev),
+        _buf(xq, "xq", d.M * kb * 128, _E4M3, dev), _buf(xs, "xs", d.M * kb, _F32, dev), _stream(stream),
+    )
+
+
+def moe_pack_fp8(dims, q, scales, packed, stream=None) -> None:
+    d, dev = _fd(dims), _device()
+    _refuse("moe_pack_fp8", moe_check_fp8_dims(d))
+    _call(
+        "moe_pack_fp8", ctypes.byref(d), _buf(q, "q", d.N * d.K, _E4M3, dev),
+        _buf(scales, "scales", -(-d.N // 128) * -(-d.K // 128), _F32, dev),
+        _buf(packed, "packed", moe_packed_fp8_bytes(d), _BYTES, dev), _stream(stream),
+    )
+
+
+def moe_fp8_gemm(dims, xq, xs, w_packed, out, workspace, workspace_bytes=None, stream=None) -> None:
+    d, dev = _fd(dims), _device()
+    _refuse("moe_fp8_gemm", moe_check_fp8_dims(d))
+    kb = -(-d.K // 128)
+    ws, n = _workspace(workspace, workspace_bytes, dev)
+    _call(
+        "moe_fp8_gemm", ctypes.byref(d), _buf(xq, "xq", d.M * kb * 128, _E4M3, dev),
+        _buf(xs, "xs", d.M * kb, _F32, dev), _buf(w_packed, "w_packed", d.N * d.K, _BYTES, dev),
+        _buf(out, "out", d.M * d.N, _ROWS[d.out_type], dev), ws, n, _stream(stream),
+    )
+
+
+def moe_fp8_proj(dims, x, w_packed, out, workspace, workspace_bytes=None, stream=None) -> None:
+    """moe_fp8_quant of x and moe_fp8_gemm in one call."""
+    d, dev = _fd(dims), _device()
+    _refuse("moe_fp8_proj", moe_check_fp8_dims(d))
+    ws, n = _workspace(workspace, workspace_bytes, dev)
+    _call(
+        "moe_fp8_proj", ctypes.byref(d), _buf(x, "x", d.M * d.K, _ROWS[d.in_type], dev),
+        _buf(w_packed, "w_packed", d.N * d.K, _BYTES, dev), _buf(out, "out", d.M * d.N, _ROWS[d.out_type], dev),
+        ws, n, _stream(stream),
+    )
+
+
+def moe_packed_fp8_expert_bytes(dims, which: int) -> int:
+    return lib().moe_packed_fp8_expert_bytes(ctypes.byref(_d(dims)), int(which))
+
+
+def moe_pack_fp8_expert(dims, which, q, scales, packed, stream=None) -> None:
+    d, dev = _d(dims), _device()
+    _refuse("moe_pack_fp8_expert", moe_check_dims(d))
+    need = moe_packed_fp8_expert_bytes(d, which)
+    if need == 0:  # a selector the dims do not have
+        raise MoeError("moe_pack_fp8_expert", MOE_ERR_UNSUPPORTED)
+    n = d.n_local if which in (MOE_W13, MOE_W2) else 1
+    size = d.d * (d.I if which in (MOE_W13, MOE_W2) else d.shared_I) * n * (2 if which in (MOE_W13, MOE_WS13) else 1)
+    _call(
+        "moe_pack_fp8_expert", ctypes.byref(d), int(which), _buf(q, "q", size, _E4M3, dev),
+        _buf(scales, "scales", size // 16384, _F32, dev), _buf(packed, "packed", need, _BYTES, dev), _stream(stream),
+    )
+
+
+def moe_fp8_ffn_workspace_bytes(dims) -> int:
+    return lib().moe_fp8_ffn_workspace_bytes(ctypes.byref(_d(dims)))
+
+
+def moe_fp8_expert_ffn(dims, x, w13_packed, w2_packed, counts, offsets, rows, active, ws13_packed, ws2_packed, y,
+                       workspace, workspace_bytes=None, stream=None) -> None:
+    """moe_expert_ffn on FP8 weights (moe_pack_fp8_expert)."""
+    d, dev = _d(dims), _device()
+    _refuse("moe_fp8_expert_ffn", moe_check_dims(d))
+    r_max, wide = d.r_max, d.d * d.I
+    ws, nb = _workspace(workspace, workspace_bytes, dev)
+    _call(
+        "moe_fp8_expert_ffn", ctypes.byref(d), _buf(x, "x", d.S * d.d, _BF16, dev),
+        _buf(w13_packed, "w13_packed", 2 * d.n_local * wide, _BYTES, dev),
+        _buf(w2_packed, "w2_packed", d.n_local * wide, _BYTES, dev),
+        _buf(counts, "counts", d.n_local, _I32, dev), _buf(offsets, "offsets", d.n_local + 1, _I32, dev),
+        _buf(rows, "rows", r_max, _I32, dev), _buf(active, "active", d.n_local + 1, _I32, dev),
+        _buf(ws13_packed, "ws13_packed", 2 * d.d * d.shared_I, _BYTES, dev),
+        _buf(ws2_packed, "ws2_packed", d.d * d.shared_I, _BYTES, dev),
+        _buf(y, "y", (r_max + (d.S if d.shared_I else 0)) * d.d, _BF16, dev), ws, nb, _stream(stream),
+    )
+
+
+# ---------------------------------------------------------------- the router's balance
+
+
+def balance_dims_from(cfg) -> MoeBalanceDims:
+    """MoeBalanceDims from an object or dict with the moe_balance_dims field names."""
+    get = cfg.get if isinstance(cfg, dict) else (lambda k, dflt=None: getattr(cfg, k, dflt))
+    return MoeBalanceDims(
+        T=get("T"), E=get("E"), topk=get("topk"), n_seq=get("n_seq", 1), score=get("score", MOE_SCORE_SIGMOID),
+        coef=get("coef", 1.0),
+    )
+
+
+def _bd(dims) -> MoeBalanceDims:
+    return dims if isinstance(dims, MoeBalanceDims) else balance_dims_from(dims)
+
+
+def moe_check_balance_dims(dims) -> int:
+    return lib().moe_check_balance_dims(ctypes.byref(_bd(dims)))
+
+
+def moe_balance_workspace_bytes(dims) -> int:
+    return lib().moe_balance_workspace_bytes(ctypes.byref(_bd(dims)))
+
+
+def moe_expert_counts(dims, topk_ids, seq_starts, counts, workspace, workspace_bytes=None, stream=None) -> None:
+    d, dev = _bd(dims), _device()
+    _refuse("moe_expert_counts", moe_check_balance_dims(d))
+    ws, n = _workspace(workspace, workspace_bytes, dev)
+    _call(
+        "moe_expert_counts", ctypes.byref(d), _buf(topk_ids, "topk_ids", d.T * d.topk, _I32, dev),
+        _buf(seq_starts, "seq_starts", d.n_seq + 1, _I32, dev), _buf(counts, "counts", d.n_seq * d.E, _I32, dev),
+        ws, n, _stream(stream),
+    )
+
+
+def moe_balance_loss(dims, logits, topk_ids, seq_starts, counts, probs, loss, workspace, workspace_bytes=None,
+                     stream=None) -> None:
+    d, dev = _bd(dims), _device()
+    _refuse("moe_balance_loss", moe_check_balance_dims(d))
+    ws, n = _workspace(workspace, workspace_bytes, dev)
+    _call(
+        "moe_balance_loss", ctypes.byref(d), _buf(logits, "logits", d.T * d.E, _F32, dev),
+        _buf(topk_ids, "topk_ids", d.T * d.topk, _I32, dev), _buf(seq_starts, "seq_starts", d.n_seq + 1, _I32, dev),
+        _buf(counts, "counts", d.n_seq * d.E, _I32, dev), _buf(probs, "probs", d.n_seq * d.E, _F32, dev),
+        _buf(loss, "loss", 1, _F32, dev), ws, n, _stream(stream),
+    )
+
+
+def moe_balance_backward(dims, logits, counts, seq_starts, dloss, dlogits, stream=None) -> None:
+    """``dloss``: a one-element device tensor, or None for 1."""
+    d, dev = _bd(dims), _device()
+    _refuse("moe_balance_backward", moe_check_balance_dims(d))
+    _call(
+        "moe_balance_backward", ctypes.byref(d), _buf(logits, "logits", d.T * d.E, _F32, dev),
+        _buf(counts, "counts", d.n_seq * d.E, _I32, dev), _buf(seq_starts, "seq_starts", d.n_seq + 1, _I32, dev),
+        _buf(dloss, "dloss", 1, _F32, dev), _buf(dlogits, "dlogits", d.T * d.E, _F32, dev), _stream(stream),
     )

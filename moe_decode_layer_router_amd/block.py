@@ -167,6 +167,72 @@ class MoeBlock:
         return self._error_word(self.fws)
 
 
+class Fp8Block:
+    """The block with FP8 experts, from ``synth.make_fp8_inputs``: route ->
+    bucket -> moe_fp8_expert_ffn -> combine on the current stream. Allocates
+    only in the constructor."""
+
+    def __init__(self, inp: dict, device="cuda"):
+        from . import MOE_WS2, MOE_WS13, moe_fp8_ffn_workspace_bytes, moe_pack_fp8_expert, moe_packed_fp8_expert_bytes
+
+        cfg = inp["cfg"]
+        self.cfg = cfg
+        self.dims: MoeDims = dims_from(cfg)
+        dv = torch.device(device)
+        S, d, E, k, n = cfg.S, cfg.d, cfg.E, cfg.topk, cfg.n_local
+        R = self.dims.r_max
+        self.x = bf16_tensor(inp["x"], dv)
+        self.gamma = bf16_tensor(inp.get("gamma"), dv)
+        self.wr = _dev(inp["wr"], dv)
+        self.bias = _dev(inp.get("bias"), dv)
+        self.packed = {}
+        for key, which in (("w13", MOE_W13), ("w2", MOE_W2), ("ws13", MOE_WS13), ("ws2", MOE_WS2)):
+            self.packed[key] = None
+            if inp[key] is not None:
+                q, scales = inp[key]
+                buf = torch.empty(moe_packed_fp8_expert_bytes(self.dims, which), dtype=torch.uint8, device=dv)
+                moe_pack_fp8_expert(self.dims, which, _dev(q, dv), _dev(scales, dv), buf)
+                self.packed[key] = buf
+        i32 = dict(dtype=torch.int32, device=dv)
+        self.logits = torch.empty((S, E), dtype=torch.float32, device=dv)
+        self.ids = torch.empty((S, k), **i32)
+        self.w = torch.empty((S, k), dtype=torch.float32, device=dv)
+        self.counts = torch.empty(n, **i32)
+        self.offsets = torch.empty(n + 1, **i32)
+        self.rows = torch.empty(max(R, 1), **i32)
+        self.pick_pos = torch.empty((S, k), **i32)
+        self.active = torch.empty(n + 1, **i32)
+        self.y = torch.zeros((R + (S if cfg.shared_I else 0), d), dtype=torch.bfloat16, device=dv)
+        self.out = torch.empty((S, d), dtype=torch.float32, device=dv)
+        self.ws = torch.zeros(moe_fp8_ffn_workspace_bytes(self.dims), dtype=torch.uint8, device=dv)
+        rw = moe_route_workspace_bytes(self.dims)
+        self.rws = torch.empty(rw, dtype=torch.uint8, device=dv) if rw else None
+
+    def route(self):
+        moe_route(self.dims, self.x, self.wr, self.bias, self.logits, self.ids, self.w, self.rws)
+
+    def bucket(self):
+        moe_bucket(self.dims, self.ids, self.counts, self.offsets, self.rows, self.pick_pos, self.active)
+
+    def expert_ffn(self):
+        from . import moe_fp8_expert_ffn
+
+        p = self.packed
+        moe_fp8_expert_ffn(
+            self.dims, self.x, p["w13"], p["w2"], self.counts, self.offsets, self.rows, self.active, p["ws13"],
+            p["ws2"], self.y, self.ws,
+        )
+
+    def combine(self):
+        moe_combine(self.dims, self.y, self.w, self.pick_pos, self.gamma, self.out)
+
+    def step(self):
+        self.route()
+        self.bucket()
+        self.expert_ffn()
+        self.combine()
+
+
 class ProjSteps:
     """Device buffers of the steps around the block for inputs from
     ``synth.make_proj_inputs``: the pre-expert step (router + pre projection

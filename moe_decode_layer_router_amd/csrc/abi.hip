@@ -34,6 +34,16 @@ int check_proj_dims(const moe_proj_dims* d) {
   return MOE_OK;
 }
 
+int check_fp8_dims(const moe_fp8_dims* d) {
+  MOE_REQUIRE(d != nullptr, MOE_ERR_NULL);
+  MOE_REQUIRE(d->M >= 1 && d->M <= 262144, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->N >= 1 && d->N <= 32768, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->K >= 1 && d->K <= 32768, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->in_type == MOE_BF16 || d->in_type == MOE_FP32, MOE_ERR_UNSUPPORTED);
+  MOE_REQUIRE(d->out_type == MOE_BF16 || d->out_type == MOE_FP32, MOE_ERR_UNSUPPORTED);
+  return MOE_OK;
+}
+
 int launch_status() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 }  // namespace moeblk

@@ -13,6 +13,7 @@ inline int r_max(const moe_dims& d) { return d.S * (d.topk < d.n_local ? d.topk 
 
 int check_dims(const moe_dims* d);  // MOE_OK or an error code
 int check_proj_dims(const moe_proj_dims* d);
+int check_fp8_dims(const moe_fp8_dims* d);
 
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 

@@ -48,6 +48,11 @@ _STREAM = {
     "h_raw": 14,
     "partial": 15,
     "w_post": 16,
+    "fp8_w13": 17,
+    "fp8_w2": 18,
+    "fp8_ws13": 19,
+    "fp8_ws2": 20,
+    "fp8_w": 21,
 }
 
 
@@ -203,4 +208,34 @@ def make_proj_inputs(pc: ProjConfig, seed: int = 0, *, gamma: str = "random") ->
     out["w_post"] = f32_to_bf16_bits(
         _rng(seed, "w_post").standard_normal((pc.n_post, L), dtype=np.float32) * pc.w_std
     )
+    return out
+
+
+def make_fp8_weight(shape, seed: int, stream: str = "fp8_w", std: float = 0.02):
+    """An FP8 weight [..., N, K]: e4m3 bytes (uint8, normal values that reach
+    about 448 in every block) and fp32 scales [..., ceil(N / 128), ceil(K / 128)],
+    so that the weights' standard deviation is about ``std``."""
+    r = _rng(seed, stream)
+    v = np.clip(np.abs(r.standard_normal(shape, dtype=np.float32)) * 110.0, 0.0, 448.0)
+    # magnitude -> nearest e4m3 code through its fp32 bits: 3 mantissa bits, bias 7
+    v = np.maximum(v, 2.0**-6).astype(np.float32)
+    u = v.view(np.uint32).astype(np.uint64)
+    u = (u + 0x7FFFF + ((u >> 20) & 1)) >> 20
+    q = (u - ((127 - 7) << 3)).astype(np.uint8)
+    q |= (r.random(shape) < 0.5).astype(np.uint8) << 7
+    blocks = (*shape[:-2], -(-shape[-2] // 128), -(-shape[-1] // 128))
+    scales = (std / 110.0 * r.uniform(0.7, 1.3, blocks)).astype(np.float32)
+    return q, scales
+
+
+def make_fp8_inputs(cfg: MoeConfig, seed: int = 0, *, gamma: str = "ones") -> dict:
+    """Inputs of the block with FP8 experts: ``make_inputs``' rows, router and
+    norm weight, and w13 [n_local, 2 I, d], w2 [n_local, d, I], ws13 [2 I_s, d],
+    ws2 [d, I_s] (or None) as (e4m3 bytes, scales) pairs."""
+    out = make_inputs(cfg, seed, gamma=gamma, parts=("x", "wr", "bias", "gamma"))
+    n, d, I, Is = cfg.n_local, cfg.d, cfg.I, cfg.shared_I  # noqa: E741
+    out["w13"] = make_fp8_weight((n, 2 * I, d), seed, "fp8_w13")
+    out["w2"] = make_fp8_weight((n, d, I), seed, "fp8_w2")
+    out["ws13"] = make_fp8_weight((2 * Is, d), seed, "fp8_ws13", cfg.ws_std) if Is else None
+    out["ws2"] = make_fp8_weight((d, Is), seed, "fp8_ws2", cfg.ws_std) if Is else None
     return out
