@@ -470,44 +470,67 @@ def moe_topk(dims, logits, bias, topk_ids, topk_w, stream=None) -> None:
 # ---------------------------------------------------------------- FP8 weights
 
 
-def _buf(t, name: str, n: int, kinds: tuple[str, ...], device: int):
-    """The pointer of a tensor of ``n`` elements or more (None -> NULL) on GPU
-    ``device``: the calls below launch on the current device's stream."""
+class _Torch:
+    """What the calls below ask of torch on every call, looked up once (these
+    calls take a few microseconds on the GPU, so the marshalling counts)."""
+
+    def __init__(self):
+        import torch
+
+        self.device = torch.cuda.current_device
+        self.raw_stream = torch._C._cuda_getCurrentRawStream  # of a device, as an int
+        self.f32, self.bf16, self.i32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
+        self.bytes = (torch.uint8,)
+        self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
+        self.rows = {MOE_BF16: self.bf16, MOE_FP32: self.f32}
+
+
+_torch = None
+
+
+def _t() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _buf(t, name: str, n: int, kinds, device: int):
+    """The pointer of a tensor of ``n`` elements or more (None -> NULL) of one
+    of the dtypes ``kinds`` (None: dims the library refuses) on GPU ``device``:
+    the calls below launch on the current device."""
     if t is None:
         return None
-    if not t.is_cuda or t.get_device() != device:
+    if t.get_device() != device:
         raise ValueError(f"{name}: tensor is not on the current GPU device")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor is not contiguous")
-    if str(t.dtype) not in kinds:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {', '.join(kinds)}")
+    if kinds is not None and t.dtype not in kinds:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {kinds}")
     if t.numel() < n:
         raise ValueError(f"{name}: {t.numel()} elements, {n} are needed")
     return t.data_ptr()
 
 
-_F32 = ("torch.float32",)
-_I32 = ("torch.int32",)
-_BF16 = ("torch.bfloat16",)
-_E4M3 = ("torch.float8_e4m3fn", "torch.uint8")
-_BYTES = ("torch.uint8",)
-_ROWS = (_BF16, _F32)  # by MOE_BF16 / MOE_FP32
+def _on(stream, T: _Torch, device: int) -> int:
+    if stream is None:
+        return T.raw_stream(device)
+    if not isinstance(stream, int) and stream.device_index != device:
+        raise ValueError("stream: not on the current GPU device")
+    return _stream(stream)
 
 
-def _device() -> int:
-    import torch
-
-    return torch.cuda.current_device()
-
-
-def _workspace(ws, workspace_bytes, device: int):
-    ptr = _buf(ws, "workspace", 0, _BYTES, device)
-    return ptr, ctypes.c_size_t(ws.numel() if workspace_bytes is None and ws is not None else workspace_bytes or 0)
+def _fp8_bytes(N: int, K: int) -> int:
+    """Packed bytes of one [N, K] matrix: whole 64 x 128 blocks, then the scales."""
+    kb = -(-K // 128)
+    return -(-N // 64) * 64 * kb * 128 + -(-(-(-N // 128) * kb) // 4) * 16
 
 
-def _refuse(fn: str, code: int) -> None:
-    if code != MOE_OK:
-        raise MoeError(fn, code)
+def _workspace(ws, workspace_bytes, T: _Torch, device: int):
+    """The workspace's pointer and bytes (``workspace_bytes`` may state fewer
+    than the tensor has)."""
+    ptr = _buf(ws, "workspace", workspace_bytes or 0, T.bytes, device)
+    return ptr, workspace_bytes if workspace_bytes is not None or ws is None else ws.numel()
 
 
 def fp8_dims_from(cfg) -> MoeFp8Dims:
@@ -540,46 +563,46 @@ def moe_fp8_proj_workspace_bytes(dims) -> int:
 
 def moe_fp8_quant(dims, x, xq, xs, stream=None) -> None:
     """x [M, K] -> xq [M, Kp] e4m3 (torch.float8_e4m3fn or uint8), xs [Kb, M] fp32."""
-    d, dev = _fd(dims), _device()
-    _refuse("moe_fp8_quant", moe_check_fp8_dims(d))
+    d, T = _fd(dims), _t()
+    dev = T.device()
     kb = -(-d.K // 128)
     _call(
-        "moe_fp8_quant", ctypes.byref(d), _buf(x, "x", d.M * d.K, _ROWS[d.in_type], dev),
-        _buf(xq, "xq", d.M * kb * 128, _E4M3, dev), _buf(xs, "xs", d.M * kb, _F32, dev), _stream(stream),
+        "moe_fp8_quant", ctypes.byref(d), _buf(x, "x", d.M * d.K, T.rows.get(d.in_type), dev),
+        _buf(xq, "xq", d.M * kb * 128, T.e4m3, dev), _buf(xs, "xs", d.M * kb, T.f32, dev), _on(stream, T, dev),
     )
 
 
 def moe_pack_fp8(dims, q, scales, packed, stream=None) -> None:
-    d, dev = _fd(dims), _device()
-    _refuse("moe_pack_fp8", moe_check_fp8_dims(d))
+    d, T = _fd(dims), _t()
+    dev = T.device()
     _call(
-        "moe_pack_fp8", ctypes.byref(d), _buf(q, "q", d.N * d.K, _E4M3, dev),
-        _buf(scales, "scales", -(-d.N // 128) * -(-d.K // 128), _F32, dev),
-        _buf(packed, "packed", moe_packed_fp8_bytes(d), _BYTES, dev), _stream(stream),
+        "moe_pack_fp8", ctypes.byref(d), _buf(q, "q", d.N * d.K, T.e4m3, dev),
+        _buf(scales, "scales", -(-d.N // 128) * -(-d.K // 128), T.f32, dev),
+        _buf(packed, "packed", moe_packed_fp8_bytes(d), T.bytes, dev), _on(stream, T, dev),
     )
 
 
 def moe_fp8_gemm(dims, xq, xs, w_packed, out, workspace, workspace_bytes=None, stream=None) -> None:
-    d, dev = _fd(dims), _device()
-    _refuse("moe_fp8_gemm", moe_check_fp8_dims(d))
+    d, T = _fd(dims), _t()
+    dev = T.device()
     kb = -(-d.K // 128)
-    ws, n = _workspace(workspace, workspace_bytes, dev)
+    ws, n = _workspace(workspace, workspace_bytes, T, dev)
     _call(
-        "moe_fp8_gemm", ctypes.byref(d), _buf(xq, "xq", d.M * kb * 128, _E4M3, dev),
-        _buf(xs, "xs", d.M * kb, _F32, dev), _buf(w_packed, "w_packed", d.N * d.K, _BYTES, dev),
-        _buf(out, "out", d.M * d.N, _ROWS[d.out_type], dev), ws, n, _stream(stream),
+        "moe_fp8_gemm", ctypes.byref(d), _buf(xq, "xq", d.M * kb * 128, T.e4m3, dev),
+        _buf(xs, "xs", d.M * kb, T.f32, dev), _buf(w_packed, "w_packed", _fp8_bytes(d.N, d.K), T.bytes, dev),
+        _buf(out, "out", d.M * d.N, T.rows.get(d.out_type), dev), ws, n, _on(stream, T, dev),
     )
 
 
 def moe_fp8_proj(dims, x, w_packed, out, workspace, workspace_bytes=None, stream=None) -> None:
     """moe_fp8_quant of x and moe_fp8_gemm in one call."""
-    d, dev = _fd(dims), _device()
-    _refuse("moe_fp8_proj", moe_check_fp8_dims(d))
-    ws, n = _workspace(workspace, workspace_bytes, dev)
+    d, T = _fd(dims), _t()
+    dev = T.device()
+    ws, n = _workspace(workspace, workspace_bytes, T, dev)
     _call(
-        "moe_fp8_proj", ctypes.byref(d), _buf(x, "x", d.M * d.K, _ROWS[d.in_type], dev),
-        _buf(w_packed, "w_packed", d.N * d.K, _BYTES, dev), _buf(out, "out", d.M * d.N, _ROWS[d.out_type], dev),
-        ws, n, _stream(stream),
+        "moe_fp8_proj", ctypes.byref(d), _buf(x, "x", d.M * d.K, T.rows.get(d.in_type), dev),
+        _buf(w_packed, "w_packed", _fp8_bytes(d.N, d.K), T.bytes, dev), _buf(out, "out", d.M * d.N, T.rows.get(d.out_type), dev),
+        ws, n, _on(stream, T, dev),
     )
 
 
@@ -588,16 +611,16 @@ def moe_packed_fp8_expert_bytes(dims, which: int) -> int:
 
 
 def moe_pack_fp8_expert(dims, which, q, scales, packed, stream=None) -> None:
-    d, dev = _d(dims), _device()
-    _refuse("moe_pack_fp8_expert", moe_check_dims(d))
+    d, T = _d(dims), _t()
+    dev = T.device()
     need = moe_packed_fp8_expert_bytes(d, which)
-    if need == 0:  # a selector the dims do not have
-        raise MoeError("moe_pack_fp8_expert", MOE_ERR_UNSUPPORTED)
+    if need == 0:  # invalid dims, or a selector they do not have
+        raise MoeError("moe_pack_fp8_expert", moe_check_dims(d) or MOE_ERR_UNSUPPORTED)
     n = d.n_local if which in (MOE_W13, MOE_W2) else 1
     size = d.d * (d.I if which in (MOE_W13, MOE_W2) else d.shared_I) * n * (2 if which in (MOE_W13, MOE_WS13) else 1)
     _call(
-        "moe_pack_fp8_expert", ctypes.byref(d), int(which), _buf(q, "q", size, _E4M3, dev),
-        _buf(scales, "scales", size // 16384, _F32, dev), _buf(packed, "packed", need, _BYTES, dev), _stream(stream),
+        "moe_pack_fp8_expert", ctypes.byref(d), int(which), _buf(q, "q", size, T.e4m3, dev),
+        _buf(scales, "scales", size // 16384, T.f32, dev), _buf(packed, "packed", need, T.bytes, dev), _on(stream, T, dev),
     )
 
 
@@ -608,19 +631,20 @@ def moe_fp8_ffn_workspace_bytes(dims) -> int:
 def moe_fp8_expert_ffn(dims, x, w13_packed, w2_packed, counts, offsets, rows, active, ws13_packed, ws2_packed, y,
                        workspace, workspace_bytes=None, stream=None) -> None:
     """moe_expert_ffn on FP8 weights (moe_pack_fp8_expert)."""
-    d, dev = _d(dims), _device()
-    _refuse("moe_fp8_expert_ffn", moe_check_dims(d))
-    r_max, wide = d.r_max, d.d * d.I
-    ws, nb = _workspace(workspace, workspace_bytes, dev)
+    d, T = _d(dims), _t()
+    dev = T.device()
+    S, dd, I, Is, n_loc = d.S, d.d, d.I, d.shared_I, d.n_local  # noqa: E741
+    r_max = d.r_max
+    ws, nb = _workspace(workspace, workspace_bytes, T, dev)
     _call(
-        "moe_fp8_expert_ffn", ctypes.byref(d), _buf(x, "x", d.S * d.d, _BF16, dev),
-        _buf(w13_packed, "w13_packed", 2 * d.n_local * wide, _BYTES, dev),
-        _buf(w2_packed, "w2_packed", d.n_local * wide, _BYTES, dev),
-        _buf(counts, "counts", d.n_local, _I32, dev), _buf(offsets, "offsets", d.n_local + 1, _I32, dev),
-        _buf(rows, "rows", r_max, _I32, dev), _buf(active, "active", d.n_local + 1, _I32, dev),
-        _buf(ws13_packed, "ws13_packed", 2 * d.d * d.shared_I, _BYTES, dev),
-        _buf(ws2_packed, "ws2_packed", d.d * d.shared_I, _BYTES, dev),
-        _buf(y, "y", (r_max + (d.S if d.shared_I else 0)) * d.d, _BF16, dev), ws, nb, _stream(stream),
+        "moe_fp8_expert_ffn", ctypes.byref(d), _buf(x, "x", S * dd, T.bf16, dev),
+        _buf(w13_packed, "w13_packed", n_loc * _fp8_bytes(2 * I, dd), T.bytes, dev),
+        _buf(w2_packed, "w2_packed", n_loc * _fp8_bytes(dd, I), T.bytes, dev),
+        _buf(counts, "counts", n_loc, T.i32, dev), _buf(offsets, "offsets", n_loc + 1, T.i32, dev),
+        _buf(rows, "rows", r_max, T.i32, dev), _buf(active, "active", n_loc + 1, T.i32, dev),
+        _buf(ws13_packed, "ws13_packed", _fp8_bytes(2 * Is, dd), T.bytes, dev),
+        _buf(ws2_packed, "ws2_packed", _fp8_bytes(dd, Is), T.bytes, dev),
+        _buf(y, "y", (r_max + (S if Is else 0)) * dd, T.bf16, dev), ws, nb, _on(stream, T, dev),
     )
 
 
@@ -649,35 +673,35 @@ def moe_balance_workspace_bytes(dims) -> int:
 
 
 def moe_expert_counts(dims, topk_ids, seq_starts, counts, workspace, workspace_bytes=None, stream=None) -> None:
-    d, dev = _bd(dims), _device()
-    _refuse("moe_expert_counts", moe_check_balance_dims(d))
-    ws, n = _workspace(workspace, workspace_bytes, dev)
+    d, T = _bd(dims), _t()
+    dev = T.device()
+    ws, n = _workspace(workspace, workspace_bytes, T, dev)
     _call(
-        "moe_expert_counts", ctypes.byref(d), _buf(topk_ids, "topk_ids", d.T * d.topk, _I32, dev),
-        _buf(seq_starts, "seq_starts", d.n_seq + 1, _I32, dev), _buf(counts, "counts", d.n_seq * d.E, _I32, dev),
-        ws, n, _stream(stream),
+        "moe_expert_counts", ctypes.byref(d), _buf(topk_ids, "topk_ids", d.T * d.topk, T.i32, dev),
+        _buf(seq_starts, "seq_starts", d.n_seq + 1, T.i32, dev), _buf(counts, "counts", d.n_seq * d.E, T.i32, dev),
+        ws, n, _on(stream, T, dev),
     )
 
 
 def moe_balance_loss(dims, logits, topk_ids, seq_starts, counts, probs, loss, workspace, workspace_bytes=None,
                      stream=None) -> None:
-    d, dev = _bd(dims), _device()
-    _refuse("moe_balance_loss", moe_check_balance_dims(d))
-    ws, n = _workspace(workspace, workspace_bytes, dev)
+    d, T = _bd(dims), _t()
+    dev = T.device()
+    ws, n = _workspace(workspace, workspace_bytes, T, dev)
     _call(
-        "moe_balance_loss", ctypes.byref(d), _buf(logits, "logits", d.T * d.E, _F32, dev),
-        _buf(topk_ids, "topk_ids", d.T * d.topk, _I32, dev), _buf(seq_starts, "seq_starts", d.n_seq + 1, _I32, dev),
-        _buf(counts, "counts", d.n_seq * d.E, _I32, dev), _buf(probs, "probs", d.n_seq * d.E, _F32, dev),
-        _buf(loss, "loss", 1, _F32, dev), ws, n, _stream(stream),
+        "moe_balance_loss", ctypes.byref(d), _buf(logits, "logits", d.T * d.E, T.f32, dev),
+        _buf(topk_ids, "topk_ids", d.T * d.topk, T.i32, dev), _buf(seq_starts, "seq_starts", d.n_seq + 1, T.i32, dev),
+        _buf(counts, "counts", d.n_seq * d.E, T.i32, dev), _buf(probs, "probs", d.n_seq * d.E, T.f32, dev),
+        _buf(loss, "loss", 1, T.f32, dev), ws, n, _on(stream, T, dev),
     )
 
 
 def moe_balance_backward(dims, logits, counts, seq_starts, dloss, dlogits, stream=None) -> None:
     """``dloss``: a one-element device tensor, or None for 1."""
-    d, dev = _bd(dims), _device()
-    _refuse("moe_balance_backward", moe_check_balance_dims(d))
+    d, T = _bd(dims), _t()
+    dev = T.device()
     _call(
-        "moe_balance_backward", ctypes.byref(d), _buf(logits, "logits", d.T * d.E, _F32, dev),
-        _buf(counts, "counts", d.n_seq * d.E, _I32, dev), _buf(seq_starts, "seq_starts", d.n_seq + 1, _I32, dev),
-        _buf(dloss, "dloss", 1, _F32, dev), _buf(dlogits, "dlogits", d.T * d.E, _F32, dev), _stream(stream),
+        "moe_balance_backward", ctypes.byref(d), _buf(logits, "logits", d.T * d.E, T.f32, dev),
+        _buf(counts, "counts", d.n_seq * d.E, T.i32, dev), _buf(seq_starts, "seq_starts", d.n_seq + 1, T.i32, dev),
+        _buf(dloss, "dloss", 1, T.f32, dev), _buf(dlogits, "dlogits", d.T * d.E, T.f32, dev), _on(stream, T, dev),
     )
