@@ -3,6 +3,7 @@
 // moe_fp8_proj).
 #include "fp8_dev.h"
 #include "fp8_launch.h"
+#include "fp8_tile.h"
 #include "host.h"
 
 namespace moeblk {
@@ -230,14 +231,35 @@ void launch_fp8_pack(const void* q, const void* scales, void* packed, int n, int
 
 namespace {
 
+template <int kRT, int kTT, int kWN, int kWM>
+void launch_tiles(Fp8TileArgs a, hipStream_t stream) {
+  constexpr int BN = 16 * kRT * kWN, BM = 16 * kTT * kWM;
+  a.tiles_n = (a.N + BN - 1) / BN;
+  a.tiles_m = (a.M + BM - 1) / BM;
+  const unsigned grid = static_cast<unsigned>(a.tiles_n) * a.tiles_m;
+  if (a.out_bf16)
+    fp8_tile_kernel<kRT, kTT, kWN, kWM, false><<<grid, 64 * kWN * kWM, 0, stream>>>(a);
+  else
+    fp8_tile_kernel<kRT, kTT, kWN, kWM, true><<<grid, 64 * kWN * kWM, 0, stream>>>(a);
+}
+
 void launch_fp8_gemm(const moe_fp8_dims& m, const void* xq, const float* xs, const void* packed,
                      void* out, hipStream_t stream) {
   const int Kb = fp8_kb(m.K);
   const uint8_t* q = static_cast<const uint8_t*>(xq);
   const uint8_t* w = static_cast<const uint8_t*>(packed);
   const float* ws = reinterpret_cast<const float*>(w + fp8_tile_bytes(m.N, m.K));
-  const int rbs = (m.N + 63) / 64;
   const bool bf = m.out_type == MOE_BF16;
+  if (m.M > 128) {
+    const Fp8TileArgs a = {q, xs, w, ws, out, m.M, m.N, Kb, bf, 0, 0};
+    const size_t big = static_cast<size_t>((m.N + 255) / 256) * ((m.M + 255) / 256);
+    if (big >= 128)
+      launch_tiles<8, 4, 2, 4>(a, stream);
+    else
+      launch_tiles<4, 4, 2, 2>(a, stream);
+    return;
+  }
+  const int rbs = (m.N + 63) / 64;
   const int tgs = m.M <= 16 ? 1 : (m.M + 63) / 64;
   const dim3 grid(static_cast<unsigned>(rbs) * tgs);
   if (m.M <= 16)
