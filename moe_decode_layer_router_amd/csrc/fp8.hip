@@ -231,16 +231,13 @@ void launch_fp8_pack(const void* q, const void* scales, void* packed, int n, int
 
 namespace {
 
-template <int kRT, int kTT, int kWN, int kWM>
+template <int kRT, int kTT, int kWN, int kWM, bool kExact>
 void launch_tiles(Fp8TileArgs a, hipStream_t stream) {
   constexpr int BN = 16 * kRT * kWN, BM = 16 * kTT * kWM;
   a.tiles_n = (a.N + BN - 1) / BN;
   a.tiles_m = (a.M + BM - 1) / BM;
   const unsigned grid = static_cast<unsigned>(a.tiles_n) * a.tiles_m;
-  if (a.out_bf16)
-    fp8_tile_kernel<kRT, kTT, kWN, kWM, false><<<grid, 64 * kWN * kWM, 0, stream>>>(a);
-  else
-    fp8_tile_kernel<kRT, kTT, kWN, kWM, true><<<grid, 64 * kWN * kWM, 0, stream>>>(a);
+  fp8_tile_kernel<kRT, kTT, kWN, kWM, kExact><<<grid, 64 * kWN * kWM, 0, stream>>>(a);
 }
 
 void launch_fp8_gemm(const moe_fp8_dims& m, const void* xq, const float* xs, const void* packed,
@@ -253,10 +250,12 @@ void launch_fp8_gemm(const moe_fp8_dims& m, const void* xq, const float* xs, con
   if (m.M > 128) {
     const Fp8TileArgs a = {q, xs, w, ws, out, m.M, m.N, Kb, bf, 0, 0};
     const size_t big = static_cast<size_t>((m.N + 255) / 256) * ((m.M + 255) / 256);
-    if (big >= 128)
-      launch_tiles<8, 4, 2, 4>(a, stream);
+    if (!bf)
+      launch_tiles<4, 4, 2, 2, true>(a, stream);
+    else if (big >= 128)
+      launch_tiles<8, 4, 2, 4, false>(a, stream);
     else
-      launch_tiles<4, 4, 2, 2>(a, stream);
+      launch_tiles<4, 4, 2, 2, false>(a, stream);
     return;
   }
   const int rbs = (m.N + 63) / 64;

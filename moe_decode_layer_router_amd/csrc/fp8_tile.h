@@ -131,22 +131,45 @@ __global__ __launch_bounds__(64 * kWN * kWM) void fp8_tile_kernel(Fp8TileArgs a)
 #pragma unroll
       for (int t = 0; t < kTT; ++t) be[t] = e4m3_to_bf16(b[t]);
     }
+    // Row tile r's MFMAs are issued while row tile r - 1's results are added: an
+    // MFMA's result cannot be read for some 40 cycles, which the additions fill.
+    // The scheduling groups keep one MFMA to the 4 additions it hides.
+    const auto row_tile = [&](int r) {
+      return join8(*reinterpret_cast<const u32x4_t*>(lw + r * kFp8TileBytes),
+                   *reinterpret_cast<const u32x4_t*>(lw + r * kFp8TileBytes + 1024));
+    };
+    i32x8_t w_next = row_tile(0);
+    f32x4_t d[kTT];
 #pragma unroll
-    for (int r = 0; r < kRT; ++r) {
-      const i32x8_t w8 = join8(*reinterpret_cast<const u32x4_t*>(lw + r * kFp8TileBytes),
-                               *reinterpret_cast<const u32x4_t*>(lw + r * kFp8TileBytes + 1024));
+    for (int r = 0; r <= kRT; ++r) {
+      const i32x8_t w8 = w_next;
+      if (r + 1 < kRT) w_next = row_tile(r + 1);
       Bf16Frag we;
       if constexpr (kExact) we = e4m3_to_bf16(w8);
 #pragma unroll
       for (int t = 0; t < kTT; ++t) {
-        f32x4_t d;
-        if constexpr (kExact)
-          d = mfma_exact_block(we, be[t]);
-        else
-          d = mfma_fp8_block(w8, b[t]);
+        const f32x4_t old = d[t];
+        if (r < kRT) {
+          if constexpr (kExact)
+            d[t] = mfma_exact_block(we, be[t]);
+          else
+            d[t] = mfma_fp8_block(w8, b[t]);
+        }
+        if (r > 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(d[i], s[t], acc[r][t][i]);
+          for (int i = 0; i < 4; ++i)
+            acc[r - 1][t][i] = __builtin_fmaf(old[i], s[t], acc[r - 1][t][i]);
+        }
       }
+      if constexpr (!kExact) {
+        if (r + 1 < kRT) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+#pragma unroll
+        for (int t = 0; t < kTT; ++t) {
+          if (r < kRT) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+          if (r > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);    // vector ALU
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);  // nothing moves into another row tile's step
     }
   }
 
