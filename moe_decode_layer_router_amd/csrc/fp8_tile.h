@@ -1,22 +1,35 @@
 // fp8_tile.h -- the FP8 product of many rows, tiled through LDS (device code).
 //
 // A workgroup of kWN x kWM waves takes 16 kRT kWN weight rows x 16 kTT kWM
-// tokens and steps through the 128-K blocks: one block of both operands is
-// copied to LDS with direct loads (no registers) while the block before it is
-// multiplied, one barrier a block. A wave holds kRT x kTT accumulator tiles; per
-// block it multiplies from zero and adds into them with the fp32 factor (token
-// scale x weight scale), which costs 4 vector fmas beside each 32-cycle MFMA.
+// tokens and steps through the 128-K blocks. Both operands are copied to LDS by
+// direct loads (no registers). A wave holds kRT x kTT accumulator tiles; a block
+// is multiplied from zero and added into them with the fp32 factor (token scale
+// x weight scale): 4 vector fmas beside each 32-cycle MFMA (on MI355X 4 fmas an
+// MFMA cost 18% over the MFMAs alone, 8 cost 63%).
+//
+// Step k's work on row tile r, token tile t is one unit: the additions of the
+// result d[t] that the row tile before left, then the MFMA that replaces it, so
+// an MFMA's latency is covered by the units in between (the last row tile's
+// additions fall into the next step). One barrier a step, in front of the last
+// row tile but one: each wave has waited for its own copies of step k + 1, so
+// behind it all of them have landed, and every wave is done with step k - 1's
+// buffers and with step k's token rows (held in registers). The copies of step
+// k + 2 start there (weights: 3 buffers, token rows: 2), a full step before they
+// are needed, and the first operands of step k + 1 are read during the last row
+// tile, so no wave waits for LDS at the start of a step.
+//
 // Weights are copied as packed (a 1 KiB piece is one operand half, read back
 // contiguously). Token rows are copied as whole 128-byte lines, the 16-byte
 // chunks of row r permuted by chunk ^ (r % 8), so that the reads of 8 rows at
 // one chunk fall on different banks.
 #pragma once
 
+#include <type_traits>
+
 #include "fp8_dev.h"
 
 namespace moeblk {
 
-typedef const __attribute__((address_space(1))) void* fp8_gptr_t;
 typedef __attribute__((address_space(3))) void* fp8_lptr_t;
 
 struct Fp8TileArgs {
@@ -44,14 +57,43 @@ __device__ __forceinline__ void fp8_tile_of(int b, int tiles_n, int tiles_m, int
   tn = in / gm;
 }
 
+// four outputs of a row at element `at`, `left` of them inside the row; quad: rows
+// start at multiples of 4
+template <bool kExact>
+__device__ __forceinline__ void store4(void* out, size_t at, int left, bool quad, f32x4_t v,
+                                       bool bf16) {
+  if (left <= 0) return;
+  if (!kExact || bf16) {
+    uint16_t* o = static_cast<uint16_t*>(out) + at;
+    const u32x2_t p = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    if (quad) {
+      *reinterpret_cast<u32x2_t*>(o) = p;
+    } else {
+      o[0] = static_cast<uint16_t>(p[0]);
+      if (left > 1) o[1] = static_cast<uint16_t>(p[0] >> 16);
+      if (left > 2) o[2] = static_cast<uint16_t>(p[1]);
+      if (left > 3) o[3] = static_cast<uint16_t>(p[1] >> 16);
+    }
+  } else {
+    float* o = static_cast<float*>(out) + at;
+    if (quad) {
+      *reinterpret_cast<f32x4_t*>(o) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) o[i] = v[i];
+    }
+  }
+}
+
 template <int kRT, int kTT, int kWN, int kWM, bool kExact>
-__global__ __launch_bounds__(64 * kWN * kWM) void fp8_tile_kernel(Fp8TileArgs a) {
+__device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
   constexpr int kWaves = kWN * kWM;
   constexpr int BN = 16 * kRT * kWN, BM = 16 * kTT * kWM;
   constexpr int kWPieces = BN / 8, kXPieces = BM / 8;  // 1 KiB wave loads a block
   static_assert(kWPieces % kWaves == 0 && kXPieces % kWaves == 0, "whole pieces a wave");
   static_assert(kRT * 16 <= 128, "a wave's weight rows share one scale block");
-  __shared__ __attribute__((aligned(128))) uint8_t lds[2][(BN + BM) * 128];
+  constexpr int kWBuf = BN * 128, kXBuf = BM * 128;  // LDS bytes of one step's operands
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int m16 = lane & 15, g = lane >> 4;
   const int wn = wave % kWN, wm = wave / kWN;
@@ -60,152 +102,185 @@ __global__ __launch_bounds__(64 * kWN * kWM) void fp8_tile_kernel(Fp8TileArgs a)
   const int Kb = a.Kb, M = a.M;
   const size_t Kp = static_cast<size_t>(Kb) * kFp8Block;
 
-  // this wave's pieces: global addresses at block 0 (rows and row tiles past the
-  // end are read as the last ones; their results are not stored)
-  const uint8_t* wsrc[kWPieces / kWaves];
-  const uint8_t* xsrc[kXPieces / kWaves];
+  // This wave's copies, pieces wave + i kWaves: bases that are the same for the
+  // whole wave and 32-bit lane offsets. Rows and row tiles past the end are read
+  // as the last ones; their results are not stored.
   const int last_rt = fp8_row_tiles(a.N) - 1;
+  const int uwave = __builtin_amdgcn_readfirstlane(wave);
+  const uint8_t* xbase = a.xq + static_cast<size_t>(tm) * BM * Kp;
+  constexpr int kXLoads = kXPieces / kWaves, kLoads = kWPieces / kWaves + kXLoads;
+  uint32_t xoff[kXLoads];
 #pragma unroll
-  for (int i = 0; i < kWPieces / kWaves; ++i) {
-    const int p = wave + i * kWaves;  // piece: row tile p / 2, half p % 2
-    const int rt = min(tn * (BN / 16) + (p >> 1), last_rt);
-    wsrc[i] = a.w + static_cast<size_t>(rt) * Kb * kFp8TileBytes + (p & 1) * 1024 + lane * 16;
+  for (int i = 0; i < kXLoads; ++i) {
+    const int row = min(8 * (uwave + i * kWaves) + (lane >> 3), M - 1 - tm * BM);  // piece: 8 rows
+    xoff[i] = static_cast<uint32_t>(row) * static_cast<uint32_t>(Kp) + ((lane & 7) ^ (lane >> 3)) * 16;
   }
-#pragma unroll
-  for (int i = 0; i < kXPieces / kWaves; ++i) {
-    const int p = wave + i * kWaves;  // piece: rows 8 p .. + 7
-    const int row = min(tm * BM + 8 * p + (lane >> 3), M - 1);
-    xsrc[i] = a.xq + row * Kp + ((lane & 7) ^ (lane >> 3)) * 16;
-  }
-  const auto load = [&](int kb, int buf) {
-#pragma unroll
-    for (int i = 0; i < kWPieces / kWaves; ++i)
-      __builtin_amdgcn_global_load_lds((fp8_gptr_t)(wsrc[i] + static_cast<size_t>(kb) * kFp8TileBytes),
-                                       (fp8_lptr_t)(&lds[buf][(wave + i * kWaves) * 1024]), 16, 0, 0);
-#pragma unroll
-    for (int i = 0; i < kXPieces / kWaves; ++i)
-      __builtin_amdgcn_global_load_lds((fp8_gptr_t)(xsrc[i] + static_cast<size_t>(kb) * kFp8Block),
-                                       (fp8_lptr_t)(&lds[buf][BN * 128 + (wave + i * kWaves) * 1024]),
-                                       16, 0, 0);
+  const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(xbase), 0, static_cast<int>(min(BM, M - tm * BM) * Kp), 0x00020000);
+  const int rt0 = tn * (BN / 16), n_rt = min(BN / 16, last_rt + 1 - rt0);
+  const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(a.w) + static_cast<size_t>(rt0) * Kb * kFp8TileBytes, 0,
+      static_cast<int>(n_rt * Kb * kFp8TileBytes), 0x00020000);
+  // copy i < kLoads of step kb into weight buffer wb, token buffer xb
+  const auto copy = [&](int i, int kb, int wb, int xb) {
+    if (i < kXLoads) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          xr, (fp8_lptr_t)(lds + 3 * kWBuf + xb * kXBuf + (uwave + i * kWaves) * 1024), 16, xoff[i],
+          kb * kFp8Block, 0, 0);
+    } else {
+      const int p = uwave + (i - kXLoads) * kWaves;  // piece: row tile p / 2, half p % 2
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          wr, (fp8_lptr_t)(lds + wb * kWBuf + p * 1024), 16, lane * 16,
+          (min(p >> 1, n_rt - 1) * Kb + kb) * kFp8TileBytes + (p & 1) * 1024, 0, 0);
+    }
   };
 
-  int tok[kTT];
-  f32x4_t acc[kRT][kTT];
+  // operand reads
+  const uint8_t* lw = lds + wn * kRT * kFp8TileBytes + lane * 16;
+  const uint8_t* lx = lds + 3 * kWBuf + (wm * kTT * 16 + m16) * 128;
+  const int c0 = ((2 * g) ^ (m16 & 7)) * 16, c1 = ((2 * g + 1) ^ (m16 & 7)) * 16;
+  const auto read_w = [&](int wb, int r) {
+    const uint8_t* p = lw + wb * kWBuf + r * kFp8TileBytes;
+    return join8(*reinterpret_cast<const u32x4_t*>(p), *reinterpret_cast<const u32x4_t*>(p + 1024));
+  };
+  const auto read_x = [&](int xb, int t) {
+    const uint8_t* p = lx + xb * kXBuf + t * 2048;
+    return join8(*reinterpret_cast<const u32x4_t*>(p + c0), *reinterpret_cast<const u32x4_t*>(p + c1));
+  };
+
+  uint32_t tok4[kTT];  // byte offset of the lane's token in a row of scales
+  f32x4_t acc[kRT][kTT], d[kTT];
+  float s[kTT], s_next[kTT], xs_raw[kTT], ws_raw;
 #pragma unroll
   for (int t = 0; t < kTT; ++t) {
-    tok[t] = min(tm * BM + (wm * kTT + t) * 16 + m16, M - 1);
+    tok4[t] = 4u * static_cast<uint32_t>(min(tm * BM + (wm * kTT + t) * 16 + m16, M - 1));
+    d[t] = f32x4_t{0, 0, 0, 0};
+    s[t] = 0.0f;
 #pragma unroll
     for (int r = 0; r < kRT; ++r) acc[r][t] = f32x4_t{0, 0, 0, 0};
   }
   const int nb = min((tn * BN + wn * kRT * 16) / 128, (a.N + 127) / 128 - 1);
   const float* wsr = a.ws + static_cast<size_t>(nb) * Kb;
-  float xs_next[kTT], ws_next;  // the next block's scales, multiplied once they are needed
-  const auto scales = [&](int kb) {
-    ws_next = wsr[kb];
+  const auto load_scales = [&](int kb) {
+    ws_raw = wsr[kb];
+    const char* xk = reinterpret_cast<const char*>(a.xs + static_cast<size_t>(kb) * M);
 #pragma unroll
-    for (int t = 0; t < kTT; ++t) xs_next[t] = a.xs[static_cast<size_t>(kb) * M + tok[t]];
+    for (int t = 0; t < kTT; ++t) xs_raw[t] = *reinterpret_cast<const float*>(xk + tok4[t]);
   };
-  scales(0);
-  load(0, 0);
-  for (int kb = 0; kb < Kb; ++kb) {
-    const int buf = kb & 1;
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's pieces have landed
-    float s[kTT];
+  const auto wait_all = [&]() {  // every wave's copies have landed, and the scales loaded before
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 #pragma unroll
-    for (int t = 0; t < kTT; ++t) s[t] = xs_next[t] * ws_next;
-    __syncthreads();                     // and everyone's; the other buffer is read out
-    if (kb + 1 < Kb) {
-      scales(kb + 1);
-      load(kb + 1, buf ^ 1);
+    for (int t = 0; t < kTT; ++t) {
+      asm volatile("" : "+v"(xs_raw[t]));  // used behind the wait, not before it
+      s_next[t] = xs_raw[t] * ws_raw;
     }
-    const uint8_t* lw = &lds[buf][wn * kRT * kFp8TileBytes + lane * 16];
-    const uint8_t* lx = &lds[buf][BN * 128 + (wm * kTT * 16 + m16) * 128];
-    const int c0 = ((2 * g) ^ (m16 & 7)) * 16, c1 = ((2 * g + 1) ^ (m16 & 7)) * 16;
-    i32x8_t b[kTT];
+  };
+
+  load_scales(0);
 #pragma unroll
-    for (int t = 0; t < kTT; ++t)
-      b[t] = join8(*reinterpret_cast<const u32x4_t*>(lx + t * 2048 + c0),
-                   *reinterpret_cast<const u32x4_t*>(lx + t * 2048 + c1));
+  for (int i = 0; i < kLoads; ++i) copy(i, 0, 0, 0);
+  if (Kb > 1) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) copy(i, 1, 1, 1);
+  }
+  wait_all();
+  i32x8_t w[2], b[kTT];
+  w[0] = read_w(0, 0);
+#pragma unroll
+  for (int t = 0; t < kTT; ++t) b[t] = read_x(0, t);
+
+  // one step; kCopy: there is a step kb + 2, kMore: there is a step kb + 1
+  const auto step = [&](int kb, int wb, int wb1, int wb2, auto copy_c, auto more_c) {
+    constexpr bool kCopy = decltype(copy_c)::value, kMore = decltype(more_c)::value;
+    const int xb = kb & 1;
+    float s_now[kTT];
+#pragma unroll
+    for (int t = 0; t < kTT; ++t) s_now[t] = s_next[t];
+    if constexpr (kMore) load_scales(kb + 1);
     Bf16Frag be[kExact ? kTT : 1];
     if constexpr (kExact) {
 #pragma unroll
       for (int t = 0; t < kTT; ++t) be[t] = e4m3_to_bf16(b[t]);
     }
-    // Row tile r's MFMAs are issued while row tile r - 1's results are added: an
-    // MFMA's result cannot be read for some 40 cycles, which the additions fill.
-    // The scheduling groups keep one MFMA to the 4 additions it hides.
-    const auto row_tile = [&](int r) {
-      return join8(*reinterpret_cast<const u32x4_t*>(lw + r * kFp8TileBytes),
-                   *reinterpret_cast<const u32x4_t*>(lw + r * kFp8TileBytes + 1024));
-    };
-    i32x8_t w_next = row_tile(0);
-    f32x4_t d[kTT];
 #pragma unroll
-    for (int r = 0; r <= kRT; ++r) {
-      const i32x8_t w8 = w_next;
-      if (r + 1 < kRT) w_next = row_tile(r + 1);
+    for (int r = 0; r < kRT; ++r) {
       Bf16Frag we;
-      if constexpr (kExact) we = e4m3_to_bf16(w8);
+      if constexpr (kExact) we = e4m3_to_bf16(w[r & 1]);
+      if constexpr (kMore)
+        if (r == kRT - 2) wait_all();
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int t = 0; t < kTT; ++t) {
-        const f32x4_t old = d[t];
-        if (r < kRT) {
-          if constexpr (kExact)
-            d[t] = mfma_exact_block(we, be[t]);
-          else
-            d[t] = mfma_fp8_block(w8, b[t]);
-        }
-        if (r > 0) {
+        f32x4_t& c = acc[r == 0 ? kRT - 1 : r - 1][t];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[r - 1][t][i] = __builtin_fmaf(old[i], s[t], acc[r - 1][t][i]);
+        for (int i = 0; i < 4; ++i) c[i] = __builtin_fmaf(d[t][i], s[t], c[i]);
+        if (r == 0) s[t] = s_now[t];  // d[t] is this step's from here on
+        if constexpr (kExact)
+          d[t] = mfma_exact_block(we, be[t]);
+        else
+          d[t] = mfma_fp8_block(w[r & 1], b[t]);
+        if (t == 0 && r + 1 < kRT) w[(r + 1) & 1] = read_w(wb, r + 1);
+        if constexpr (kMore) {
+          if (r == kRT - 1) {  // the next step's first operands
+            if (t == 0) w[0] = read_w(wb1, 0);
+            b[t] = read_x(xb ^ 1, t);
+          }
         }
-      }
-      if constexpr (!kExact) {
-        if (r + 1 < kRT) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+        if constexpr (kCopy) {
+          constexpr int kUnits = 2 * kTT;  // the last two row tiles
+          const int u = (r - (kRT - 2)) * kTT + t;
+          if (u >= 0) {
 #pragma unroll
-        for (int t = 0; t < kTT; ++t) {
-          if (r < kRT) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
-          if (r > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);    // vector ALU
+            for (int i = 0; i < kLoads; ++i)
+              if (i * kUnits / kLoads == u) copy(i, kb + 2, wb2, xb);
+          }
         }
+        __builtin_amdgcn_sched_barrier(0);  // units stay in order
       }
-      __builtin_amdgcn_sched_barrier(0);  // nothing moves into another row tile's step
     }
+  };
+  int kb = 0, wb = 0;
+  for (; kb + 2 < Kb; ++kb) {
+    const int wb1 = wb == 2 ? 0 : wb + 1, wb2 = wb1 == 2 ? 0 : wb1 + 1;
+    step(kb, wb, wb1, wb2, std::true_type{}, std::true_type{});
+    wb = wb1;
   }
+  if (kb + 1 < Kb) {
+    const int wb1 = wb == 2 ? 0 : wb + 1;
+    step(kb, wb, wb1, 0, std::false_type{}, std::true_type{});
+    wb = wb1;
+    ++kb;
+  }
+  step(kb, wb, 0, 0, std::false_type{}, std::false_type{});
+#pragma unroll
+  for (int t = 0; t < kTT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      acc[kRT - 1][t][i] = __builtin_fmaf(d[t][i], s[t], acc[kRT - 1][t][i]);
 
   // lane: token m16 of a token tile, outputs 4 g .. + 3 of a row tile
-  const bool quad = a.N % 4 == 0;
 #pragma unroll
   for (int t = 0; t < kTT; ++t) {
     const int token = tm * BM + (wm * kTT + t) * 16 + m16;
-    if (token >= M) continue;
     const size_t orow = static_cast<size_t>(token) * a.N;
 #pragma unroll
     for (int r = 0; r < kRT; ++r) {
       const int n0 = tn * BN + (wn * kRT + r) * 16 + 4 * g;
-      const f32x4_t v = acc[r][t];
-      if (quad) {
-        if (n0 < a.N) {
-          if (a.out_bf16) {
-            const u32x2_t p = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + orow + n0) = p;
-          } else {
-            *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + orow + n0) = v;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n0 + i < a.N) {
-            if (a.out_bf16)
-              static_cast<uint16_t*>(a.out)[orow + n0 + i] =
-                  static_cast<uint16_t>(f32_to_bf16_bits(v[i]));
-            else
-              static_cast<float*>(a.out)[orow + n0 + i] = v[i];
-          }
-      }
+      if (token < M) store4<kExact>(a.out, orow + n0, a.N - n0, a.N % 4 == 0, acc[r][t], a.out_bf16);
+      __builtin_amdgcn_sched_barrier(0);  // one tile's addresses at a time
     }
   }
+}
+
+template <int kRT, int kTT, int kWN, int kWM, bool kExact>
+__global__ __launch_bounds__(64 * kWN * kWM, kRT * kTT > 32 ? 1 : 2) void fp8_tile_kernel(Fp8TileArgs a) {
+  constexpr int kBytes = (3 * 16 * kRT * kWN + 2 * 16 * kTT * kWM) * 128;
+  static_assert(kBytes <= 160 * 1024, "LDS");
+  __shared__ __attribute__((aligned(128))) uint8_t lds[kBytes];
+  fp8_tile<kRT, kTT, kWN, kWM, kExact>(a, lds);
 }
 
 }  // namespace moeblk
