@@ -547,7 +547,8 @@ int moe_expert_counts(const moe_balance_dims* dims, const int32_t* topk_ids,
  *   logits [T, E] fp32 (moe_route's or moe_pre_expert's); -inf leaves an expert
  *          out (p = 0), a row whose logits are all -inf adds nothing to probs;
  *   counts [n_seq, E] int32, probs [n_seq, E] fp32, loss [1] fp32, written.
- * Sums run in a fixed order, across rows in fp64 beyond 64 of them. */
+ * Sums run in a fixed order, across rows in fp32 over at most 256 of them and in
+ * fp64 beyond. */
 int moe_balance_loss(const moe_balance_dims* dims, const float* logits, const int32_t* topk_ids,
                      const int32_t* seq_starts, int32_t* counts, float* probs, float* loss,
                      void* workspace, size_t workspace_bytes, hipStream_t stream);

@@ -9,11 +9,16 @@
 //   dL/dl_j = p_j (1 - s_j) (a_j - sum_e a_e p_e)   (sigmoid scores s)
 //   dL/dl_j = p_j (a_j - sum_e a_e p_e)             (softmax).
 // Forward is bound by reading the logits once, backward by reading and writing
-// them once. A workgroup of the forward takes kChunk rows; where a chunk c meets
-// a sequence b it leaves its sums in slot c + b (walking the rows, either index
+// them once. Sixteen lanes hold a row (four rows a wave): its maximum and sums
+// are four steps within a DPP row, no LDS.
+//
+// A workgroup of the forward takes a chunk of rows; where a chunk c meets a
+// sequence b it leaves its sums in slot c + b (walking the rows, either index
 // grows from one meeting to the next, so slots do not collide and there are at
 // most chunks + sequences of them). A second launch sums each sequence's slots
-// in chunk order in fp64: no result depends on an order of atomics.
+// in a fixed order in fp64: no result depends on an order of atomics. With few
+// slots (up to 16: T <= 240 in one sequence) the last workgroup of the first launch
+// does that instead, which saves a launch of about 3 us.
 #include <math.h>
 
 #include "common.h"
@@ -22,133 +27,167 @@
 namespace moeblk {
 namespace {
 
-constexpr int kChunk = 64;  // rows a forward workgroup takes
 constexpr int kMaxE = 256;
-constexpr int kPer = kMaxE / kWave;  // logits a lane holds: columns lane + 64 i
+constexpr int kPass = 16;      // rows a workgroup of 256 threads holds at a time
+constexpr int kOneSlots = 16;  // most slots the last workgroup of the first launch sums
+
+// Rows a workgroup takes: at least a pass, about 1024 (forward) or 2048 (backward:
+// no sums to hand over) workgroups, at most 256 rows (fp32 sums over a chunk).
+__host__ __device__ inline int chunk_rows(int T, int groups) {
+  const int per = (T + groups - 1) / groups;
+  const int r = (per + kPass - 1) / kPass * kPass;
+  return r > 256 ? 256 : r;
+}
+__host__ __device__ inline int forward_rows(int T) { return chunk_rows(T, 1024); }
+__host__ __device__ inline int backward_rows(int T) { return chunk_rows(T, 2048); }
 
 __device__ __forceinline__ int seq_start(const int32_t* starts, int b, int T) {
   if (!starts) return b == 0 ? 0 : T;
   return min(max(starts[b], 0), T);
 }
 
-// the last sequence that starts at or before `row` (0 if none does)
-__device__ __forceinline__ int find_seq(const int32_t* starts, int n_seq, int row, int T) {
-  if (!starts) return 0;
-  int lo = 0, hi = n_seq;  // invariant: start(lo) <= row (or lo = 0), start(hi) > row (or hi = n_seq)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (seq_start(starts, mid, T) <= row)
-      lo = mid;
-    else
-      hi = mid;
+// The starts as a wave sees them: up to 63 sequences lie in its lanes (one load,
+// no dependent search), more are searched in memory.
+struct Starts {
+  const int32_t* p;
+  int n_seq, T, mine;
+  __device__ Starts(const int32_t* starts, int n, int rows) : p(starts), n_seq(n), T(rows), mine(0) {
+    if (n < kWave) mine = seq_start(p, min(static_cast<int>(threadIdx.x & (kWave - 1)), n), T);
   }
-  return lo;
+  __device__ int at(int b) const {  // b: the same in all lanes
+    if (n_seq < kWave) return __builtin_amdgcn_readlane(mine, b);
+    return seq_start(p, b, T);
+  }
+  // the last sequence that starts at or before `row` (0 if none does)
+  __device__ int find(int row) const {
+    if (n_seq < kWave) {
+      const uint64_t m = __ballot(mine <= row && static_cast<int>(threadIdx.x & (kWave - 1)) < n_seq);
+      return m ? 63 - __builtin_clzll(m) : 0;
+    }
+    int lo = 0, hi = n_seq;  // start(lo) <= row (or lo = 0), start(hi) > row (or hi = n_seq)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (seq_start(p, mid, T) <= row)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return lo;
+  }
+};
+
+// butterfly over the 16 lanes of a DPP row: xor 1, xor 2, then the mirrors of 8 and
+// 16 lanes (whose halves agree by then); every lane gets the same bits
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp<0xb1>(v);
+  v += dpp<0x4e>(v);
+  v += dpp<0x141>(v);
+  return v + dpp<0x140>(v);
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp<0xb1>(v));
+  v = fmaxf(v, dpp<0x4e>(v));
+  v = fmaxf(v, dpp<0x141>(v));
+  return fmaxf(v, dpp<0x140>(v));
 }
 
-__device__ __forceinline__ float wave_max(float v) {
+// exp through the hardware's exp2: the argument's rounding is |x| 2^-24 relative
+// in the result, the instruction's own error 1 ulp
+__device__ __forceinline__ float exp_hw(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
+}
+
+// A lane's columns of a row: 64 i + 4 j + c with j = lane % 16, i < kNI, c < 4.
+template <int kNI>
+struct Row {
+  float v[4 * kNI];
+};
+
+template <int kNI>
+__device__ __forceinline__ void load_row(const float* logits, size_t row, int E, bool vec, int j,
+                                         Row<kNI>& l) {
+  const float* p = logits + row * E;
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, kWave));
-  return v;
+  for (int i = 0; i < kNI; ++i) {
+    const int e = 64 * i + 4 * j;
+    if (vec) {  // E % 4 == 0: whole groups of four, 16-byte aligned
+      f32x4_t q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (e < E) q = *reinterpret_cast<const f32x4_t*>(p + e);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) l.v[4 * i + c] = q[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) l.v[4 * i + c] = e + c < E ? p[e + c] : -INFINITY;
+    }
+  }
 }
 
-// One row's normalised scores p of this lane's columns, and slope = dp_j/dl_j's
-// factor p_j (1 - s_j) or p_j. Scores are taken relative to the row's largest
-// where that keeps them from vanishing: sigmoid(l) e^{-m} with m = min(max l, 0)
-// is exp(min(l, 0) - m) / (1 + exp(-|l|)). A row whose logits are all -inf has
+// One row's normalised scores p of this lane's columns, and slope = p_j (1 -
+// s_j) or p_j (kSlope). Scores are taken relative to the row's largest where
+// that keeps them from vanishing: sigmoid(l) e^{-m} with m = min(max l, 0) is
+// exp(min(l, 0) - m) / (1 + exp(-|l|)). A row whose logits are all -inf has
 // p = 0.
-__device__ __forceinline__ void row_scores(const float (&l)[kPer], int score, float (&p)[kPer],
-                                           float (&slope)[kPer]) {
-  float m = l[0];
+template <int kNI, bool kSlope>
+__device__ __forceinline__ void row_scores(const Row<kNI>& l, int score, Row<kNI>& p,
+                                           Row<kNI>& slope) {
+  constexpr int n = 4 * kNI;
+  float m = l.v[0];
 #pragma unroll
-  for (int i = 1; i < kPer; ++i) m = fmaxf(m, l[i]);
-  m = wave_max(m);
+  for (int i = 1; i < n; ++i) m = fmaxf(m, l.v[i]);
+  m = row_max(m);
   const bool none = m == -INFINITY;
   if (score == MOE_SCORE_SIGMOID) {
     m = none ? 0.0f : fminf(m, 0.0f);
+    const bool low = __any(m < 0.0f);  // a row of this wave has no logit above zero
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float e = expf(-fabsf(l[i]));
-      const float r = 1.0f / (1.0f + e);
-      const float num = m == 0.0f ? (l[i] >= 0.0f ? 1.0f : e) : expf(fminf(l[i], 0.0f) - m);
-      p[i] = num * r;
-      slope[i] = (l[i] >= 0.0f ? e : 1.0f) * r;  // 1 - sigmoid
+    for (int i = 0; i < n; ++i) {
+      const float x = l.v[i];
+      const float e = exp_hw(-fabsf(x));
+      const float r = __builtin_amdgcn_rcpf(1.0f + e);
+      float num = x >= 0.0f ? 1.0f : e;
+      if (low) num = m < 0.0f ? exp_hw(fminf(x, 0.0f) - m) : num;
+      p.v[i] = num * r;
+      if constexpr (kSlope) slope.v[i] = (x >= 0.0f ? e : 1.0f) * r;  // 1 - sigmoid
+      if (x != x) p.v[i] = x;
     }
   } else {
     m = none ? 0.0f : m;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      p[i] = expf(l[i] - m);
-      slope[i] = 1.0f;
+    for (int i = 0; i < n; ++i) {
+      p.v[i] = exp_hw(l.v[i] - m);
+      if constexpr (kSlope) slope.v[i] = 1.0f;
     }
   }
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) s += p[i];
-  s = wave_sum(s);
+  for (int i = 0; i < n; ++i) s += p.v[i];
+  s = row_sum(s);
   const float inv = none ? 0.0f : 1.0f / s;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    p[i] *= inv;
-    slope[i] *= p[i];
-  }
-}
-
-__device__ __forceinline__ void load_row(const float* logits, size_t row, int E, int lane,
-                                         float (&l)[kPer]) {
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane + kWave * i;
-    l[i] = e < E ? logits[row * E + e] : -INFINITY;
+  for (int i = 0; i < n; ++i) {
+    p.v[i] *= inv;
+    if constexpr (kSlope) slope.v[i] *= p.v[i];
   }
 }
 
 // ---------------------------------------------------------------- forward
 
-// logits NULL: counts only
-__global__ __launch_bounds__(256) void chunk_kernel(const float* __restrict__ logits,
-                                                    const int32_t* __restrict__ ids,
-                                                    const int32_t* __restrict__ starts,
-                                                    int32_t* __restrict__ slot_counts,
-                                                    float* __restrict__ slot_probs, int T, int E,
-                                                    int topk, int n_seq, int score) {
-  __shared__ int cnt[kMaxE];
-  __shared__ float sums[4][kMaxE];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int c = blockIdx.x;
-  const int lo = c * kChunk, hi = min(T, lo + kChunk);
-  int b = find_seq(starts, n_seq, lo, T);
-  for (; b < n_seq; ++b) {
-    const int s0 = max(lo, seq_start(starts, b, T)), s1 = min(hi, seq_start(starts, b + 1, T));
-    if (s0 >= hi) break;
-    if (s1 <= s0) continue;
-    __syncthreads();
-    cnt[threadIdx.x] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < (s1 - s0) * topk; i += 256) {
-      const int e = ids[static_cast<size_t>(s0) * topk + i];
-      if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
-    }
-    if (logits) {
-      float acc[kPer] = {};
-      for (int row = s0 + wave; row < s1; row += 4) {
-        float l[kPer], p[kPer], slope[kPer];
-        load_row(logits, row, E, lane, l);
-        row_scores(l, score, p, slope);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] += p[i];
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) sums[wave][lane + kWave * i] = acc[i];
-    }
-    __syncthreads();
-    const int e = threadIdx.x;
-    if (e < E) {
-      const size_t at = static_cast<size_t>(c + b) * E + e;
-      slot_counts[at] = cnt[e];
-      if (logits) slot_probs[at] = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
-    }
-  }
-}
+struct ForwardArgs {
+  const float* logits;  // NULL: counts only
+  const int32_t *ids, *starts;
+  int32_t* slot_counts;
+  float* slot_probs;
+  int32_t* counts;
+  float *probs, *loss;
+  double* terms;
+  int32_t* done;  // zero between calls
+  int T, E, topk, n_seq, score;
+  float coef;
+};
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
@@ -156,69 +195,220 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
   return v;
 }
 
-// workgroup (b, 64 experts): wave v sums the slots v, v + 4, ... of its
-// sequence's chunks. The last workgroup to finish adds the terms of the loss.
-__global__ __launch_bounds__(256) void reduce_kernel(const int32_t* __restrict__ slot_counts,
-                                                     const float* __restrict__ slot_probs,
-                                                     const int32_t* __restrict__ starts,
-                                                     int32_t* __restrict__ counts,
-                                                     float* __restrict__ probs,
-                                                     float* __restrict__ loss, double* terms,
-                                                     int32_t* done, int T, int E, int topk,
-                                                     int n_seq, float coef) {
-  __shared__ int cnt[4][kWave];
-  __shared__ double sums[4][kWave];
+template <typename T>
+__device__ __forceinline__ void store_through(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ T load_through(const T* p) {
+  return __hip_atomic_load(const_cast<T*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Counts this workgroup as done; true in all threads of the last one (which
+// sets the counter back). What the others stored through before is visible to its
+// load_through: each thread waits for its own stores first.
+__device__ __forceinline__ bool last_workgroup(int32_t* done) {
   __shared__ int last;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int groups = (E + kWave - 1) / kWave;
-  const int b = blockIdx.x / groups, e = (blockIdx.x % groups) * kWave + lane;
-  const int s0 = seq_start(starts, b, T), s1 = seq_start(starts, b + 1, T);
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = __hip_atomic_fetch_add(done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+           static_cast<int>(gridDim.x) - 1;
+    if (last) __hip_atomic_store(done, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return last;
+}
+
+// The sums of (b, 16 experts) over the sequence's slots by 256 threads: expert
+// tid % 16, slots tid / 16, + 16, ... Returns the 16 experts' loss term in
+// thread 0.
+__device__ __forceinline__ double reduce_group(const ForwardArgs& a, int b, int e0) {
+  __shared__ int cnt[16][17];
+  __shared__ double sums[16][17];
+  const int j = threadIdx.x & 15, k = threadIdx.x >> 4;
+  const int e = e0 + j;
+  const int rows = forward_rows(a.T);
+  const int s0 = seq_start(a.starts, b, a.T), s1 = seq_start(a.starts, b + 1, a.T);
   int n = 0;
   double p = 0.0;
-  if (s1 > s0 && e < E) {
-    for (int c = s0 / kChunk + wave; c <= (s1 - 1) / kChunk; c += 4) {
-      const size_t at = static_cast<size_t>(c + b) * E + e;
-      n += slot_counts[at];
-      if (loss) p += slot_probs[at];
+  if (s1 > s0 && e < a.E) {
+    const int last = (s1 - 1) / rows;
+#pragma unroll 8
+    for (int c = s0 / rows + k; c <= last; c += 16) {
+      const size_t at = static_cast<size_t>(c + b) * a.E + e;
+      n += a.slot_counts[at];
+      if (a.loss) p += a.slot_probs[at];
     }
   }
-  cnt[wave][lane] = n;
-  sums[wave][lane] = p;
+  __syncthreads();
+  cnt[k][j] = n;
+  sums[k][j] = p;
   __syncthreads();
   double term = 0.0;
-  if (wave == 0) {
-    n = cnt[0][lane] + cnt[1][lane] + cnt[2][lane] + cnt[3][lane];
-    p = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
-    const double rows = s1 > s0 ? s1 - s0 : 1;
-    p /= rows;
-    if (e < E) {
-      counts[static_cast<size_t>(b) * E + e] = n;
-      if (loss) probs[static_cast<size_t>(b) * E + e] = static_cast<float>(p);
-      term = static_cast<double>(E) / (topk * rows) * n * p;
+  if (k == 0) {
+    n = 0;
+    p = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      n += cnt[i][j];
+      p += sums[i][j];
     }
-    term = wave_sum_f64(term);
+    const double len = s1 > s0 ? s1 - s0 : 1;
+    p /= len;
+    if (e < a.E) {
+      a.counts[static_cast<size_t>(b) * a.E + e] = n;
+      if (a.loss) a.probs[static_cast<size_t>(b) * a.E + e] = static_cast<float>(p);
+      term = static_cast<double>(a.E) / (a.topk * len) * n * p;
+    }
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1) term += __shfl_xor(term, m, 16);
   }
-  if (!loss) return;
-  if (threadIdx.x == 0) {
-    __hip_atomic_store(&terms[blockIdx.x], term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __threadfence();
-    last = __hip_atomic_fetch_add(done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-           static_cast<int>(gridDim.x) - 1;
+  return term;
+}
+
+__device__ __forceinline__ void store_loss(const ForwardArgs& a, double sum) {
+  *a.loss = static_cast<float>(sum * static_cast<double>(a.coef) / a.n_seq);
+}
+
+template <int kNI, bool kOne>
+__global__ __launch_bounds__(256) void chunk_kernel(ForwardArgs a) {
+  __shared__ int cnt[kMaxE];
+  __shared__ float sums[kPass][kMaxE];
+  const int tid = threadIdx.x, j = tid & 15, group = tid >> 4;
+  const int c = blockIdx.x, rows = forward_rows(a.T), E = a.E;
+  const bool vec = E % 4 == 0;
+  const int lo = c * rows, hi = min(a.T, lo + rows);
+  // the chunk's first rows and its picks are on their way before the sequences are known
+  Row<kNI> next;
+  int have = lo + group;
+  if (a.logits && have < hi) load_row<kNI>(a.logits, have, E, vec, j, next);
+  int id[8];  // picks tid, tid + 256, ... of the chunk's at most 2048
+  const int picks = (hi - lo) * a.topk;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    id[i] = tid + 256 * i < picks ? a.ids[static_cast<size_t>(lo) * a.topk + tid + 256 * i] : -1;
+  const Starts seq(a.starts, a.n_seq, a.T);
+  for (int b = seq.find(lo); b < a.n_seq; ++b) {
+    const int s0 = max(lo, seq.at(b)), s1 = min(hi, seq.at(b + 1));
+    if (s0 >= hi) break;
+    if (s1 <= s0) continue;
+    __syncthreads();
+    cnt[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = tid + 256 * i;
+      if (at >= (s0 - lo) * a.topk && at < (s1 - lo) * a.topk && id[i] >= 0 && id[i] < E)
+        atomicAdd(&cnt[id[i]], 1);
+    }
+    if (a.logits) {
+      float acc[4 * kNI] = {};
+      int row = lo + (s0 - lo) / kPass * kPass + group;
+      if (row != have && row < s1) load_row<kNI>(a.logits, row, E, vec, j, next);
+      for (; row < s1; row += kPass) {
+        const Row<kNI> l = next;
+        if (row + kPass < s1) load_row<kNI>(a.logits, row + kPass, E, vec, j, next);
+        Row<kNI> p, unused;
+        row_scores<kNI, false>(l, a.score, p, unused);
+        if (row >= s0) {
+#pragma unroll
+          for (int i = 0; i < 4 * kNI; ++i) acc[i] += p.v[i];
+        }
+      }
+      have = -1;
+#pragma unroll
+      for (int i = 0; i < kNI; ++i)
+        *reinterpret_cast<f32x4_t*>(&sums[group][64 * i + 4 * j]) =
+            f32x4_t{acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]};
+    }
+    __syncthreads();
+    if (tid < E) {
+      const size_t at = static_cast<size_t>(c + b) * E + tid;
+      float t[kPass];
+      if (a.logits) {
+#pragma unroll
+        for (int i = 0; i < kPass; ++i) t[i] = sums[i][tid];
+#pragma unroll
+        for (int w = kPass / 2; w >= 1; w >>= 1)
+#pragma unroll
+          for (int i = 0; i < w; ++i) t[i] += t[i + w];
+      }
+      if constexpr (kOne) {
+        store_through(&a.slot_counts[at], cnt[tid]);
+        if (a.logits) store_through(&a.slot_probs[at], t[0]);
+      } else {
+        a.slot_counts[at] = cnt[tid];
+        if (a.logits) a.slot_probs[at] = t[0];
+      }
+    }
   }
-  __syncthreads();
-  if (!last || wave != 0) return;
+  if constexpr (kOne) {
+    if (!last_workgroup(a.done)) return;
+    // thread = expert; all slots at once (those no chunk met are not added)
+    int n[kOneSlots];
+    float p[kOneSlots];
+    const int slots = static_cast<int>(gridDim.x) + a.n_seq;
+#pragma unroll
+    for (int i = 0; i < kOneSlots; ++i) {
+      n[i] = 0;
+      p[i] = 0.0f;
+      if (i < slots && tid < E) {
+        n[i] = load_through(&a.slot_counts[i * E + tid]);
+        if (a.logits) p[i] = load_through(&a.slot_probs[i * E + tid]);
+      }
+    }
+    double sum = 0.0;
+    for (int b = 0; b < a.n_seq; ++b) {
+      const int s0 = seq.at(b), s1 = seq.at(b + 1);
+      const int first = s0 / rows + b, last = s1 > s0 ? (s1 - 1) / rows + b : -1;
+      int count = 0;
+      double prob = 0.0;
+#pragma unroll
+      for (int i = 0; i < kOneSlots; ++i) {
+        if (i >= first && i <= last) {
+          count += n[i];
+          prob += p[i];
+        }
+      }
+      const double len = s1 > s0 ? s1 - s0 : 1;
+      prob /= len;
+      if (tid < E) {
+        a.counts[static_cast<size_t>(b) * E + tid] = count;
+        if (a.loss) a.probs[static_cast<size_t>(b) * E + tid] = static_cast<float>(prob);
+        sum += static_cast<double>(E) / (a.topk * len) * count * prob;
+      }
+    }
+    if (!a.loss) return;
+    __shared__ double part[4];
+    sum = wave_sum_f64(sum);
+    if ((tid & 63) == 0) part[tid >> 6] = sum;
+    __syncthreads();
+    sum = (part[0] + part[1]) + (part[2] + part[3]);
+    if (tid == 0) store_loss(a, sum);
+  }
+}
+
+// workgroup (b, 16 experts); the last one to finish adds the terms of the loss
+__global__ __launch_bounds__(256) void reduce_kernel(ForwardArgs a) {
+  __shared__ double part[4];
+  const int groups = (a.E + 15) / 16;
+  const int b = blockIdx.x / groups, e0 = (blockIdx.x % groups) * 16;
+  const double term = reduce_group(a, b, e0);
+  if (!a.loss) return;
+  if (threadIdx.x == 0) store_through(&a.terms[blockIdx.x], term);
+  if (!last_workgroup(a.done)) return;
   double sum = 0.0;
-  for (unsigned i = lane; i < gridDim.x; i += kWave)
-    sum += __hip_atomic_load(&terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) sum += load_through(&a.terms[i]);
   sum = wave_sum_f64(sum);
-  if (lane == 0) {
-    *loss = static_cast<float>(sum * static_cast<double>(coef) / n_seq);
-    __hip_atomic_store(done, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) store_loss(a, (part[0] + part[1]) + (part[2] + part[3]));
 }
 
 // ---------------------------------------------------------------- backward
 
+template <int kNI>
 __global__ __launch_bounds__(256) void backward_kernel(const float* __restrict__ logits,
                                                        const int32_t* __restrict__ counts,
                                                        const int32_t* __restrict__ starts,
@@ -226,36 +416,56 @@ __global__ __launch_bounds__(256) void backward_kernel(const float* __restrict__
                                                        float* __restrict__ dlogits, int T, int E,
                                                        int topk, int n_seq, float coef,
                                                        int score) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int lo = blockIdx.x * kChunk, hi = min(T, lo + kChunk);
+  const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int rows = backward_rows(T);
+  const int lo = blockIdx.x * rows, hi = min(T, lo + rows);
+  const bool vec = E % 4 == 0;
+  Row<kNI> next;
+  int have = lo + group;
+  if (have < hi) load_row<kNI>(logits, have, E, vec, j, next);
   const float g = dloss ? *dloss : 1.0f;
-  int b = find_seq(starts, n_seq, lo, T);
-  for (; b < n_seq; ++b) {
-    const int q0 = seq_start(starts, b, T), q1 = seq_start(starts, b + 1, T);
+  const Starts seq(starts, n_seq, T);
+  for (int b = seq.find(lo); b < n_seq; ++b) {
+    const int q0 = seq.at(b), q1 = seq.at(b + 1);
     const int s0 = max(lo, q0), s1 = min(hi, q1);
     if (s0 >= hi) break;
     if (s1 <= s0) continue;
-    const double rows = q1 - q0;
-    const float f = static_cast<float>(static_cast<double>(g) * coef / n_seq * E /
-                                       (topk * rows * rows));
-    float a[kPer];
+    int row = lo + (s0 - lo) / kPass * kPass + group;
+    if (row != have && row < s1) load_row<kNI>(logits, row, E, vec, j, next);
+    have = -1;
+    const double len = q1 - q0;
+    const float f =
+        static_cast<float>(static_cast<double>(g) * coef / n_seq * E / (topk * len * len));
+    float a[4 * kNI];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane + kWave * i;
+    for (int i = 0; i < 4 * kNI; ++i) {
+      const int e = 64 * (i >> 2) + 4 * j + (i & 3);
       a[i] = e < E ? f * static_cast<float>(counts[static_cast<size_t>(b) * E + e]) : 0.0f;
     }
-    for (int row = s0 + wave; row < s1; row += 4) {
-      float l[kPer], p[kPer], slope[kPer];
-      load_row(logits, row, E, lane, l);
-      row_scores(l, score, p, slope);
+    for (; row < s1; row += kPass) {
+      const Row<kNI> l = next;
+      if (row + kPass < s1) load_row<kNI>(logits, row + kPass, E, vec, j, next);
+      Row<kNI> p, slope;
+      row_scores<kNI, true>(l, score, p, slope);
       float mean = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) mean = __builtin_fmaf(a[i], p[i], mean);
-      mean = wave_sum(mean);
+      for (int i = 0; i < 4 * kNI; ++i) mean = __builtin_fmaf(a[i], p.v[i], mean);
+      mean = row_sum(mean);
+      if (row < s0) continue;  // the sequence in front's
+      float* out = dlogits + static_cast<size_t>(row) * E;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = lane + kWave * i;
-        if (e < E) dlogits[static_cast<size_t>(row) * E + e] = slope[i] * (a[i] - mean);
+      for (int i = 0; i < kNI; ++i) {
+        const int e = 64 * i + 4 * j;
+        f32x4_t v;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = slope.v[4 * i + c] * (a[4 * i + c] - mean);
+        if (vec) {
+          if (e < E) *reinterpret_cast<f32x4_t*>(out + e) = v;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (e + c < E) out[e + c] = v[c];
+        }
       }
     }
   }
@@ -272,8 +482,10 @@ int check_balance_dims(const moe_balance_dims* d) {
   return MOE_OK;
 }
 
-inline int chunks(const moe_balance_dims& d) { return (d.T + kChunk - 1) / kChunk; }
-inline int reduce_groups(const moe_balance_dims& d) { return d.n_seq * ((d.E + 63) / 64); }
+inline int chunks(const moe_balance_dims& d) {
+  return (d.T + forward_rows(d.T) - 1) / forward_rows(d.T);
+}
+inline int reduce_groups(const moe_balance_dims& d) { return d.n_seq * ((d.E + 15) / 16); }
 
 // workspace: the done counter (zero between calls), the loss terms, the slots
 struct BalanceLayout {
@@ -290,6 +502,16 @@ BalanceLayout balance_layout(const moe_balance_dims& d) {
   return l;
 }
 
+template <int kNI>
+void launch_forward(const ForwardArgs& a, int n_chunks, int groups, hipStream_t stream) {
+  if (n_chunks + a.n_seq <= kOneSlots) {
+    chunk_kernel<kNI, true><<<n_chunks, 256, 0, stream>>>(a);
+    return;
+  }
+  chunk_kernel<kNI, false><<<n_chunks, 256, 0, stream>>>(a);
+  reduce_kernel<<<groups, 256, 0, stream>>>(a);
+}
+
 int forward(const moe_balance_dims* dims, const float* logits, const int32_t* topk_ids,
             const int32_t* seq_starts, int32_t* counts, float* probs, float* loss, void* workspace,
             size_t workspace_bytes, hipStream_t stream) {
@@ -301,13 +523,19 @@ int forward(const moe_balance_dims* dims, const float* logits, const int32_t* to
   const BalanceLayout l = balance_layout(m);
   MOE_REQUIRE(workspace_bytes >= l.total, MOE_ERR_WORKSPACE);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  int32_t* sc = reinterpret_cast<int32_t*>(ws + l.counts);
-  float* sp = reinterpret_cast<float*>(ws + l.probs);
-  chunk_kernel<<<chunks(m), 256, 0, stream>>>(logits, topk_ids, seq_starts, sc, sp, m.T, m.E,
-                                              m.topk, m.n_seq, m.score);
-  reduce_kernel<<<reduce_groups(m), 256, 0, stream>>>(
-      sc, sp, seq_starts, counts, probs, loss, reinterpret_cast<double*>(ws + l.terms),
-      reinterpret_cast<int32_t*>(ws), m.T, m.E, m.topk, m.n_seq, m.coef);
+  ForwardArgs a;
+  a.logits = logits, a.ids = topk_ids, a.starts = seq_starts;
+  a.slot_counts = reinterpret_cast<int32_t*>(ws + l.counts);
+  a.slot_probs = reinterpret_cast<float*>(ws + l.probs);
+  a.counts = counts, a.probs = probs, a.loss = loss;
+  a.terms = reinterpret_cast<double*>(ws + l.terms), a.done = reinterpret_cast<int32_t*>(ws);
+  a.T = m.T, a.E = m.E, a.topk = m.topk, a.n_seq = m.n_seq, a.score = m.score, a.coef = m.coef;
+  if (m.E <= 64)
+    launch_forward<1>(a, chunks(m), reduce_groups(m), stream);
+  else if (m.E <= 128)
+    launch_forward<2>(a, chunks(m), reduce_groups(m), stream);
+  else
+    launch_forward<4>(a, chunks(m), reduce_groups(m), stream);
   return launch_status();
 }
 
@@ -353,9 +581,18 @@ int moe_balance_backward(const moe_balance_dims* dims, const float* logits, cons
   MOE_REQUIRE(aligned16(logits) && aligned16(counts) && aligned16(seq_starts) &&
                   aligned16(dloss) && aligned16(dlogits),
               MOE_ERR_ALIGN);
-  backward_kernel<<<chunks(*dims), 256, 0, stream>>>(logits, counts, seq_starts, dloss, dlogits,
-                                                     dims->T, dims->E, dims->topk, dims->n_seq,
-                                                     dims->coef, dims->score);
+  const moe_balance_dims& m = *dims;
+  const unsigned grid = (m.T + backward_rows(m.T) - 1) / backward_rows(m.T);
+  const auto launch = [&](auto kernel) {
+    kernel<<<grid, 256, 0, stream>>>(logits, counts, seq_starts, dloss, dlogits, m.T, m.E, m.topk,
+                                     m.n_seq, m.coef, m.score);
+  };
+  if (m.E <= 64)
+    launch(backward_kernel<1>);
+  else if (m.E <= 128)
+    launch(backward_kernel<2>);
+  else
+    launch(backward_kernel<4>);
   return launch_status();
 }
 
