@@ -1,6 +1,8 @@
 // fp8.hip -- rows to e4m3 with a scale per 128 columns (moe_fp8_quant), FP8
 // weight packing, and the product with block scales (moe_fp8_gemm,
 // moe_fp8_proj).
+#include <type_traits>
+
 #include "fp8_dev.h"
 #include "fp8_launch.h"
 #include "fp8_tile.h"
@@ -12,44 +14,90 @@ namespace {
 // ---------------------------------------------------------------- quantise
 //
 // A (row, 128-column block) is 8 lanes of 16 columns: its magnitude maximum is
-// three butterfly steps, each lane stores 16 bytes. Division by the scale is an
-// exact multiplication (a power of two), so the only rounding is e4m3's.
+// three DPP steps, each lane stores 16 bytes. Division by the scale is part of
+// the converts and exact (a power of two), so the only rounding is e4m3's.
+// Magnitudes are compared as integers (non-negative floats order as their bit
+// patterns, infinity and NaN last), two bf16 at a time.
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+typedef int16_t i16x2_t __attribute__((ext_vector_type(2)));
+
+template <typename T>
+struct Raw16 {  // 16 columns of a row as loaded
+  uint32_t w[4 * sizeof(T)];
+};
+
 template <typename T, bool kVec>
-__device__ __forceinline__ void load16(const T* row, int c0, int K, float v[16]) {
-  if constexpr (kVec) {
-    if (c0 + 16 <= K) {
-      if constexpr (sizeof(T) == 2) {
+__device__ __forceinline__ void load16(const T* row, int c0, int K, Raw16<T>& v) {
+  if (kVec && c0 + 16 <= K) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const u32x4_t w = *reinterpret_cast<const u32x4_t*>(row + c0 + 8 * i);
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) {
+      const u32x4_t q = *reinterpret_cast<const u32x4_t*>(row + c0 + 16 / sizeof(T) * i);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[8 * i + 2 * j] = bf16_lo(w[j]);
-            v[8 * i + 2 * j + 1] = bf16_hi(w[j]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4_t w = *reinterpret_cast<const f32x4_t*>(row + c0 + 4 * i);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[4 * i + j] = w[j];
-        }
-      }
-      return;
+      for (int j = 0; j < 4; ++j) v.w[4 * i + j] = q[j];
     }
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(4 * sizeof(T)); ++i) v.w[i] = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    float f = 0.0f;
     if (c0 + i < K) {
       if constexpr (sizeof(T) == 2)
-        f = bf16_to_f32(row[c0 + i]);
+        v.w[i >> 1] |= static_cast<uint32_t>(row[c0 + i]) << (16 * (i & 1));
       else
-        f = row[c0 + i];
+        v.w[i] = __float_as_uint(row[c0 + i]);
     }
-    v[i] = f;
   }
+}
+
+template <int kCtrl>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
+  const uint32_t o = static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(v), kCtrl, 0xf, 0xf, false));
+  return v > o ? v : o;
+}
+
+// 16 columns of a block by one of 8 adjacent lanes: the e4m3 values, and the
+// block's scale (the same in all 8 lanes, which must all take part)
+template <typename T>
+__device__ __forceinline__ u32x4_t quant16(const Raw16<T>& v, float& scale) {
+  uint32_t m;
+  if constexpr (sizeof(T) == 2) {
+    u16x2_t p = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      p = __builtin_elementwise_max(p, __builtin_bit_cast(u16x2_t, v.w[i] & 0x7fff7fffu));
+    m = static_cast<uint32_t>(p[0] > p[1] ? p[0] : p[1]) << 16;
+  } else {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t a = v.w[i] & 0x7fffffffu;
+      m = m > a ? m : a;
+    }
+  }
+  m = max_dpp<0xb1>(m);   // lane ^ 1
+  m = max_dpp<0x4e>(m);   // lane ^ 2
+  m = max_dpp<0x141>(m);  // the mirror within 8 lanes: the other four
+  scale = fp8_block_scale(__uint_as_float(m));
+  u32x4_t q;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    i16x2_t r = {0, 0};
+    if constexpr (sizeof(T) == 2) {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, v.w[2 * i]),
+                                                    scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, v.w[2 * i + 1]),
+                                                    scale, true);
+    } else {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(v.w[4 * i]),
+                                                   __uint_as_float(v.w[4 * i + 1]), scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(v.w[4 * i + 2]),
+                                                   __uint_as_float(v.w[4 * i + 3]), scale, true);
+    }
+    q[i] = __builtin_bit_cast(uint32_t, r);
+  }
+  return q;
 }
 
 // nrows: rows to quantise, or NULL for all `M` (a device count, for bucket rows)
@@ -64,19 +112,10 @@ __global__ __launch_bounds__(256) void quant_kernel(const T* __restrict__ x,
   const int kb = static_cast<int>(item - row * Kb);
   const int n = nrows ? min(*nrows, M) : M;
   if (row >= static_cast<size_t>(n)) return;
-  float v[16];
+  Raw16<T> v;
+  float sc;
   load16<T, kVec>(x + row * K, kb * kFp8Block + l8 * 16, K, v);
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) m = max_mag(m, v[i]);
-#pragma unroll
-  for (int s = 1; s < 8; s <<= 1) m = max_mag(m, __shfl_xor(m, s, kWave));
-  float inv;
-  const float sc = fp8_block_scale(m, inv);
-  u32x4_t q;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q[i] = pack_e4m3x4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
+  const u32x4_t q = quant16(v, sc);
   *reinterpret_cast<u32x4_t*>(xq + row * (static_cast<size_t>(Kb) * kFp8Block) + kb * kFp8Block +
                               l8 * 16) = q;
   if (l8 == 0) xs[static_cast<size_t>(kb) * M + row] = sc;
@@ -119,82 +158,288 @@ __global__ __launch_bounds__(256) void pack_fp8_kernel(const uint8_t* __restrict
     reinterpret_cast<float*>(om + pieces * 16)[p] = sc[blockIdx.y * ns + p];
 }
 
-// ---------------------------------------------------------------- product
+// ---------------------------------------------------------------- product, few rows
+//
+// At most 16 rows: the weight is read once and its bytes bound the call. A
+// workgroup takes 16 kRT weight rows; its kNW waves take every kNW-th K block, a
+// ring of kRing blocks' loads in flight each, straight from the packed order into
+// registers (exact form, fp8_dev.h). The waves' sums are added in wave order.
+//
+// kSrc says where the rows come from. kRowsX: the rows themselves; every
+// workgroup quantises them into LDS while its first weight loads are in flight,
+// which costs less than a launch in front as long as they are few (rows x K
+// blocks up to kFusedItems). kRowsQ: quantised rows, read from memory.
+enum RowSource { kRowsBf16, kRowsFp32, kRowsQ };
 
-__device__ __forceinline__ void store_out(void* out, size_t at, float v, bool bf16) {
-  if (bf16)
-    reinterpret_cast<uint16_t*>(out)[at] = static_cast<uint16_t>(f32_to_bf16_bits(v));
-  else
-    reinterpret_cast<float*>(out)[at] = v;
-}
+constexpr int kFusedItems = 896;  // most (row, K block) pairs in LDS, 132 bytes each
+constexpr int kFewItems = 256;    // few enough for several workgroups a CU
 
-// One workgroup: 16 kRT weight rows x 16 kTT tokens, its 8 waves taking every
-// eighth K block. Each 128-K block is summed from zero (exact form, fp8_dev.h), scaled
-// in fp32 by (token scale x weight scale) into the running sum; the waves' sums
-// are added in wave order (deterministic).
-template <int kRT, int kTT>
-__global__ __launch_bounds__(512) void gemm_kernel(const uint8_t* __restrict__ xq,
-                                                   const float* __restrict__ xs,
-                                                   const uint8_t* __restrict__ w,
-                                                   const float* __restrict__ ws,
-                                                   void* __restrict__ out, int M, int N, int Kb,
-                                                   bool out_bf16, int row_blocks) {
-  __shared__ f32x4_t red[8][kRT][64];
+struct RowsArgs {
+  const void* x;      // kRowsBf16, kRowsFp32: [M][K]
+  const uint8_t* xq;  // kRowsQ
+  const float* xs;
+  const uint8_t* w;
+  const float* ws;
+  void* out;
+  int M, N, K, Kb;
+  bool out_bf16;
+  int row_blocks;
+  SplitK split;
+};
+
+template <int kRT, int kNW, int kSrc, int kItems>
+__global__ __launch_bounds__(64 * kNW) void rows_kernel(RowsArgs a) {
+  constexpr int kRing = kRT == 1 ? 4 : 2;
+  constexpr bool kFused = kSrc != kRowsQ;
+  __shared__ f32x4_t red[kNW][kRT][64];
+  __shared__ __attribute__((aligned(128))) uint8_t xl[kFused ? kItems * kFp8Block : 16];
+  __shared__ float sl[kFused ? kItems : 1];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int m16 = lane & 15, g = lane >> 4;
-  const int rb = blockIdx.x % row_blocks, tg = blockIdx.x / row_blocks;
-  const size_t Kp = static_cast<size_t>(Kb) * kFp8Block;
-  const uint8_t* wt = w + static_cast<size_t>(rb) * kRT * Kb * kFp8TileBytes + lane * 16;
-  const float* wsr = ws + static_cast<size_t>(rb * 16 * kRT / 128) * Kb;
-  int tok[kTT];
-  f32x4_t acc[kRT][kTT];
-#pragma unroll
-  for (int t = 0; t < kTT; ++t) {
-    tok[t] = min((tg * kTT + t) * 16 + m16, M - 1);
-#pragma unroll
-    for (int r = 0; r < kRT; ++r) acc[r][t] = f32x4_t{0, 0, 0, 0};
-  }
-  for (int kb = wave; kb < Kb; kb += 8) {
-    Bf16Frag a[kRT];
+  const int Kb = a.Kb, M = a.M;
+  const int rb = blockIdx.x % a.row_blocks, part = blockIdx.x / a.row_blocks;
+  int kb0, kb1;
+  part_range(Kb, a.split.parts, part, kb0, kb1);
+  const uint8_t* wt = a.w + static_cast<size_t>(rb) * kRT * Kb * kFp8TileBytes + lane * 16;
+  const float* wsr = a.ws + static_cast<size_t>(rb * 16 * kRT / 128) * Kb;
+  const int tok = min(m16, M - 1);
+  const uint8_t* xrow = kFused ? nullptr : a.xq + tok * (static_cast<size_t>(Kb) * kFp8Block) + 32 * g;
+
+  u32x4_t wreg[kRing][kRT][2], xreg[kFused ? 1 : kRing][2];
+  float sreg[kRing];
+  const auto load = [&](int i, int kb) {
 #pragma unroll
     for (int r = 0; r < kRT; ++r) {
       const uint8_t* p = wt + (static_cast<size_t>(r) * Kb + kb) * kFp8TileBytes;
-      a[r] = e4m3_to_bf16(join8(ld_nt<u32x4_t>(p), ld_nt<u32x4_t>(p + 1024)));
+      wreg[i][r][0] = ld_nt<u32x4_t>(p);
+      wreg[i][r][1] = ld_nt<u32x4_t>(p + 1024);
     }
-    const float sw = wsr[kb];
+    sreg[i] = wsr[kb];
+    if constexpr (!kFused) {
+      sreg[i] *= a.xs[static_cast<size_t>(kb) * M + tok];
+      xreg[i][0] = *reinterpret_cast<const u32x4_t*>(xrow + kb * kFp8Block);
+      xreg[i][1] = *reinterpret_cast<const u32x4_t*>(xrow + kb * kFp8Block + 16);
+    }
+  };
 #pragma unroll
-    for (int t = 0; t < kTT; ++t) {
-      const uint8_t* p = xq + tok[t] * Kp + kb * kFp8Block + 32 * g;
-      const Bf16Frag b = e4m3_to_bf16(join8(*reinterpret_cast<const u32x4_t*>(p),
-                                            *reinterpret_cast<const u32x4_t*>(p + 16)));
-      const float s = xs[static_cast<size_t>(kb) * M + tok[t]] * sw;
+  for (int i = 0; i < kRing; ++i)
+    if (kb0 + wave + kNW * i < kb1) load(i, kb0 + wave + kNW * i);
+
+  if constexpr (kFused) {
+    // item (kb - kb0) * M + row: 8 lanes of 16 columns; the 16-byte chunks of a
+    // row permuted by chunk ^ (row % 8)
+    using T = typename std::conditional<kSrc == kRowsBf16, uint16_t, float>::type;
+    const T* x = static_cast<const T*>(a.x);
+    const bool vec = a.K % (16 / sizeof(T)) == 0;
+    const int l8 = threadIdx.x & 7;
+    for (int item = threadIdx.x >> 3; item < M * (kb1 - kb0); item += 8 * kNW) {
+      const int row = item % M, kb = kb0 + item / M;
+      Raw16<T> v;
+      if (vec)
+        load16<T, true>(x + static_cast<size_t>(row) * a.K, kb * kFp8Block + l8 * 16, a.K, v);
+      else
+        load16<T, false>(x + static_cast<size_t>(row) * a.K, kb * kFp8Block + l8 * 16, a.K, v);
+      float sc;
+      const u32x4_t q = quant16(v, sc);
+      *reinterpret_cast<u32x4_t*>(xl + item * kFp8Block + ((l8 ^ (row & 7)) * 16)) = q;
+      if (l8 == 0) sl[item] = sc;
+    }
+    __syncthreads();
+  }
+
+  f32x4_t acc[kRT];
 #pragma unroll
-      for (int r = 0; r < kRT; ++r) {
-        const f32x4_t d = mfma_exact_block(a[r], b);
+  for (int r = 0; r < kRT; ++r) acc[r] = f32x4_t{0, 0, 0, 0};
+  const int c0 = ((2 * g) ^ (tok & 7)) * 16, c1 = ((2 * g + 1) ^ (tok & 7)) * 16;
+  for (int base = kb0 + wave; base < kb1; base += kNW * kRing) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(d[i], s, acc[r][t][i]);
+    for (int i = 0; i < kRing; ++i) {
+      const int kb = base + kNW * i;
+      if (kb < kb1) {
+        Bf16Frag b;
+        float s = sreg[i];
+        if constexpr (kFused) {
+          const int item = (kb - kb0) * M + tok;
+          const uint8_t* p = xl + item * kFp8Block;
+          b = e4m3_to_bf16(join8(*reinterpret_cast<const u32x4_t*>(p + c0),
+                                 *reinterpret_cast<const u32x4_t*>(p + c1)));
+          s *= sl[item];
+        } else {
+          b = e4m3_to_bf16(join8(xreg[i][0], xreg[i][1]));
+        }
+#pragma unroll
+        for (int r = 0; r < kRT; ++r) {
+          const f32x4_t d = mfma_exact_block(e4m3_to_bf16(join8(wreg[i][r][0], wreg[i][r][1])), b);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[r][c] = __builtin_fmaf(d[c], s, acc[r][c]);
+        }
+        if (kb + kNW * kRing < kb1) load(i, kb + kNW * kRing);
       }
     }
   }
+#pragma unroll
+  for (int r = 0; r < kRT; ++r) red[wave][r][lane] = acc[r];
+  __syncthreads();
+  f32x4_t sum[1] = {{0, 0, 0, 0}};
+  if (wave < kRT) {
+    sum[0] = red[0][wave][lane];
+#pragma unroll
+    for (int v = 1; v < kNW; ++v) sum[0] += red[v][wave][lane];
+  }
+  __shared__ int last;
+  if (!join_parts(a.split, rb, part, wave < kRT, sum, &last)) return;
+  if (wave < kRT && m16 < M) {
+    const int n0 = (rb * kRT + wave) * 16 + 4 * g;
+    store4<true>(a.out, static_cast<size_t>(m16) * a.N + n0, a.N - n0, a.N % 4 == 0, sum[0],
+                 a.out_bf16);
+  }
+}
+
+// ---------------------------------------------------------------- product, 17 to 128 rows
+//
+// 16 kRT weight rows x 16 kTT tokens a workgroup; its 8 waves take every eighth K
+// block of the workgroup's part, two blocks' loads in flight, straight into
+// registers (tokens through L2). The waves' sums are added through LDS, all
+// threads taking part.
+struct MidArgs {
+  const uint8_t* xq;
+  const float* xs;
+  const uint8_t* w;
+  const float* ws;
+  void* out;
+  int M, N, Kb;
+  bool out_bf16;
+  int row_blocks, tiles;
+  SplitK split;
+};
+
+constexpr int kCpolNt = 2;  // cache-policy operand of the buffer intrinsics: non-temporal
+
+__device__ __forceinline__ u32x4_t buffer16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+}
+
+template <int kRT, int kTT, bool kExact, int kRing>
+__device__ __forceinline__ void mid_body(const MidArgs& a, f32x4_t* red, int* last) {
+  constexpr int kEach = (kRT * kTT + 7) / 8;  // tiles a wave adds up at the end
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int m16 = lane & 15, g = lane >> 4;
+  const int uwave = __builtin_amdgcn_readfirstlane(wave);
+  const int part = blockIdx.x / a.tiles, tile = blockIdx.x - part * a.tiles;
+  const int rb = tile % a.row_blocks, t0 = tile / a.row_blocks * 16 * kTT;
+  const int Kb = a.Kb, M = a.M;
+  int kb0, kb1;
+  part_range(Kb, a.split.parts, part, kb0, kb1);
+  const uint32_t Kp = static_cast<uint32_t>(Kb) * kFp8Block;
+  const auto rsrc = [](const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes),
+                                             0x00020000);
+  };
+  const __amdgpu_buffer_rsrc_t wr =
+      rsrc(a.w + static_cast<size_t>(rb) * kRT * Kb * kFp8TileBytes, kRT * Kb * kFp8TileBytes);
+  const __amdgpu_buffer_rsrc_t xr = rsrc(a.xq, M * Kp), sr = rsrc(a.xs, M * Kb * 4);
+  const float* wsr = a.ws + static_cast<size_t>(rb * kRT / 8) * Kb;
+  uint32_t tok[kTT];
+  f32x4_t acc[kRT][kTT];
 #pragma unroll
   for (int t = 0; t < kTT; ++t) {
-    __syncthreads();
+    tok[t] = min(t0 + t * 16 + m16, M - 1);
 #pragma unroll
-    for (int r = 0; r < kRT; ++r) red[wave][r][lane] = acc[r][t];
-    __syncthreads();
-    if (wave < kRT) {
-      f32x4_t s = red[0][wave][lane];
+    for (int r = 0; r < kRT; ++r) acc[r][t] = f32x4_t{0, 0, 0, 0};
+  }
+  u32x4_t w[kRing][kRT][2], x[kRing][kTT][2];
+  float s[kRing][kTT], sw[kRing];
+  const auto load = [&](int i, int kb) {
 #pragma unroll
-      for (int v = 1; v < 8; ++v) s += red[v][wave][lane];
-      const int token = (tg * kTT + t) * 16 + m16;
-      const int n0 = (rb * kRT + wave) * 16 + 4 * g;
-      if (token < M) {
+    for (int r = 0; r < kRT; ++r) {
+      const uint32_t at = static_cast<uint32_t>(r * Kb + kb) * kFp8TileBytes;
+      w[i][r][0] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16, at, kCpolNt));
+      w[i][r][1] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16, at + 1024, kCpolNt));
+    }
+    sw[i] = wsr[kb];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n0 + i < N) store_out(out, static_cast<size_t>(token) * N + n0 + i, s[i], out_bf16);
+    for (int t = 0; t < kTT; ++t) {
+      const uint32_t v = tok[t] * Kp + 32 * g;
+      x[i][t][0] = buffer16(xr, v, kb * kFp8Block);
+      x[i][t][1] = buffer16(xr, v + 16, kb * kFp8Block);
+      s[i][t] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(sr, tok[t] * 4, kb * M * 4, 0));
+    }
+  };
+  const auto multiply = [&](int i) {
+    Bf16Frag xe[kExact ? kTT : 1];
+    float f[kTT];
+#pragma unroll
+    for (int t = 0; t < kTT; ++t) {
+      f[t] = s[i][t] * sw[i];
+      if constexpr (kExact) xe[t] = e4m3_to_bf16(join8(x[i][t][0], x[i][t][1]));
+    }
+#pragma unroll
+    for (int r = 0; r < kRT; ++r) {
+      const i32x8_t w8 = join8(w[i][r][0], w[i][r][1]);
+      Bf16Frag we;
+      if constexpr (kExact) we = e4m3_to_bf16(w8);
+#pragma unroll
+      for (int t = 0; t < kTT; ++t) {
+        f32x4_t d;
+        if constexpr (kExact)
+          d = mfma_exact_block(we, xe[t]);
+        else
+          d = mfma_fp8_block(w8, join8(x[i][t][0], x[i][t][1]));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[r][t][c] = __builtin_fmaf(d[c], f[t], acc[r][t][c]);
       }
     }
+  };
+  if constexpr (kRing == 2) {
+    int kb = kb0 + uwave;
+    if (kb < kb1) load(0, kb);
+    if (kb + 8 < kb1) load(1, kb + 8);
+    for (; kb < kb1; kb += 16) {
+      multiply(0);
+      if (kb + 16 < kb1) load(0, kb + 16);
+      if (kb + 8 < kb1) {
+        multiply(1);
+        if (kb + 24 < kb1) load(1, kb + 24);
+      }
+    }
+  } else {
+    for (int kb = kb0 + uwave; kb < kb1; kb += 8) {
+      load(0, kb);
+      multiply(0);
+    }
   }
+  // rounds of 8 tiles (tile i = r kTT + t), a tile a wave: red[wave][8][lane]
+  f32x4_t sum[kEach];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    if (e) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8 && e * 8 + i < kRT * kTT; ++i)
+      red[(wave * 8 + i) * 64 + lane] = acc[(e * 8 + i) / kTT][(e * 8 + i) % kTT];
+    __syncthreads();
+    sum[e] = red[wave * 64 + lane];
+#pragma unroll
+    for (int v = 1; v < 8; ++v) sum[e] += red[(v * 8 + wave) * 64 + lane];
+  }
+  if (!join_parts(a.split, tile, part, true, sum, last)) return;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = e * 8 + wave, token = t0 + (i % kTT) * 16 + m16;
+    const int n0 = (rb * kRT + i / kTT) * 16 + 4 * g;
+    if (token < M && i < kRT * kTT)
+      store4<kExact>(a.out, static_cast<size_t>(token) * a.N + n0, a.N - n0, a.N % 4 == 0, sum[e],
+                     a.out_bf16);
+  }
+}
+
+template <int kRT, int kTT, bool kExact, int kRing>
+__global__ __launch_bounds__(512) void mid_kernel(MidArgs a) {
+  __shared__ f32x4_t red[8 * 8 * 64];
+  __shared__ int last;
+  mid_body<kRT, kTT, kExact, kRing>(a, red, &last);
 }
 
 }  // namespace
@@ -231,50 +476,178 @@ void launch_fp8_pack(const void* q, const void* scales, void* packed, int n, int
 
 namespace {
 
+// How a product of these sizes runs: the kernel, and its K parts: as many as
+// bring the workgroups to the number of CUs, each with at least `least` K blocks
+// (adding up P parts costs the last workgroup of a tile about 2 us). Measured, us,
+// split / whole: M = 8, N = 512, K = 8192 6.0 / 9.3; M = 64, N = 4096, K = 7168
+// 16.9 / 22.2; M = 512, N = 4096, K = 7168 43 / 57.
+enum Form { kRows, kMid, kTile128, kTile256 };
+struct Plan {
+  Form form;
+  int tiles, parts;
+  size_t part_bytes;  // fp32 sums of one part of one tile
+};
+
+int split_parts(int tiles, int Kb, int least) {
+  if (tiles > kSplitTiles) return 1;
+  int p = 256 / tiles;
+  p = p < Kb / least ? p : Kb / least;
+  return p < 1 ? 1 : p;
+}
+
+inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// few rows: 16 weight rows a workgroup while that gives at most 512 workgroups, else 64
+inline bool thin_rows(const moe_fp8_dims& m) { return m.N <= 16 * 512; }
+// 17 to 128 rows: 32 tokens a workgroup while they are all, else 64; 32 weight rows
+// while that gives no more workgroups than CUs, else 64 (half the token bytes
+// through L2, but only one K block's loads at a time fit the registers at 64
+// tokens). Measured, us with the quantisation, 32 / 64 rows: M = 128, N = 7168, K
+// = 2048 17.1 / 12.7; M = 128, N = 512, K = 8192 11.7 / 14.7; M = 64, N = 4096, K =
+// 7168 17.2 / 18.1.
+inline int mid_tiles_m(const moe_fp8_dims& m) { return ceil_div(m.M, m.M <= 32 ? 32 : 64); }
+inline int mid_rows(const moe_fp8_dims& m) {
+  return ceil_div(m.N, 32) * mid_tiles_m(m) <= 256 ? 32 : 64;
+}
+
+Plan fp8_plan(const moe_fp8_dims& m) {
+  const int Kb = fp8_kb(m.K);
+  Plan p;
+  if (m.M <= 16) {
+    p.form = kRows;
+    p.tiles = thin_rows(m) ? ceil_div(m.N, 16) : ceil_div(m.N, 64);
+    p.parts = split_parts(p.tiles, Kb, 16);
+    p.part_bytes = 1024 * 16;
+    return p;
+  }
+  if (m.M <= 128) {
+    p.form = kMid;
+    p.tiles = ceil_div(m.N, mid_rows(m)) * mid_tiles_m(m);
+    p.parts = split_parts(p.tiles, Kb, 8);
+    p.part_bytes = 2 * 512 * 16;
+    return p;
+  }
+  // A step of one 256 x 256 tile a CU takes about 2.1 us, of two 128 x 128
+  // tiles 1.25 us; rounds over the 256 CUs times that decide. Measured (us,
+  // K = 7168, N = 4096, 256 against 128 tiles): M = 8192 240 / 259, M = 4096
+  // 122 / 135, M = 2048 107 / 69.5.
+  const auto rounds = [&](int tile, int slots) {
+    const size_t t = static_cast<size_t>(ceil_div(m.N, tile)) * ceil_div(m.M, tile);
+    return (t + slots - 1) / slots;
+  };
+  if (m.out_type == MOE_BF16 && rounds(256, 256) * 210 <= rounds(128, 512) * 125) {
+    p.form = kTile256;
+    p.tiles = ceil_div(m.N, 256) * ceil_div(m.M, 256);
+    p.parts = 1;
+  } else {
+    p.form = kTile128;
+    p.tiles = ceil_div(m.N, 128) * ceil_div(m.M, 128);
+    p.parts = split_parts(p.tiles, Kb, 8);
+  }
+  p.part_bytes = 16 * 256 * 16;
+  return p;
+}
+
+size_t gemm_workspace(const moe_fp8_dims& m) {
+  const Plan p = fp8_plan(m);
+  return kSplitCounterBytes + (p.parts > 1 ? p.tiles * p.parts * p.part_bytes : 0);
+}
+
+SplitK split_of(const Plan& p, void* workspace) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  return SplitK{p.parts, reinterpret_cast<int32_t*>(ws),
+                reinterpret_cast<f32x4_t*>(ws + kSplitCounterBytes)};
+}
+
 template <int kRT, int kTT, int kWN, int kWM, bool kExact>
 void launch_tiles(Fp8TileArgs a, hipStream_t stream) {
-  constexpr int BN = 16 * kRT * kWN, BM = 16 * kTT * kWM;
-  a.tiles_n = (a.N + BN - 1) / BN;
-  a.tiles_m = (a.M + BM - 1) / BM;
-  const unsigned grid = static_cast<unsigned>(a.tiles_n) * a.tiles_m;
+  a.tiles_n = ceil_div(a.N, 16 * kRT * kWN);
+  a.tiles_m = ceil_div(a.M, 16 * kTT * kWM);
+  const unsigned grid = static_cast<unsigned>(a.tiles_n) * a.tiles_m * a.split.parts;
   fp8_tile_kernel<kRT, kTT, kWN, kWM, kExact><<<grid, 64 * kWN * kWM, 0, stream>>>(a);
 }
 
+// 16 waves where a workgroup has a CU to itself and 8 could not have all of its K
+// blocks in flight. Measured, us, 16 / 8 waves: N = 4096, K = 7168, M = 16 13.3 /
+// 16.5; N = 4096, K = 4096, M = 8 7.3 / 7.6; N = 7168, K = 2048, M = 1 7.3 / 5.8;
+// N = 1024, K = 4096, M = 8 7.1 / 6.7.
+template <int kSrc>
+void launch_rows(RowsArgs a, const Plan& p, hipStream_t stream) {
+  const int Kpart = ceil_div(a.Kb, p.parts);
+  const bool few = kSrc != kRowsQ && a.M * Kpart <= kFewItems;
+  const bool thin = a.N <= 16 * 512;
+  const unsigned grid = p.tiles * p.parts;
+  a.row_blocks = p.tiles;
+  if (thin && few && grid <= 256 && Kpart > 32)
+    rows_kernel<1, 16, kSrc, kFewItems><<<grid, 1024, 0, stream>>>(a);
+  else if (thin && grid <= 256 && Kpart > 32)
+    rows_kernel<1, 16, kSrc, kFusedItems><<<grid, 1024, 0, stream>>>(a);
+  else if (thin && few)
+    rows_kernel<1, 8, kSrc, kFewItems><<<grid, 512, 0, stream>>>(a);
+  else if (thin)
+    rows_kernel<1, 8, kSrc, kFusedItems><<<grid, 512, 0, stream>>>(a);
+  else if (few)
+    rows_kernel<4, 8, kSrc, kFewItems><<<grid, 512, 0, stream>>>(a);
+  else
+    rows_kernel<4, 8, kSrc, kFusedItems><<<grid, 512, 0, stream>>>(a);
+}
+
+void launch_mid(const MidArgs& a, int rows, unsigned grid, hipStream_t stream) {
+  const auto launch = [&](auto kernel) { kernel<<<grid, 512, 0, stream>>>(a); };
+  const bool small = rows == 32;
+  if (a.M <= 32 && a.out_bf16)
+    small ? launch(mid_kernel<2, 2, false, 2>) : launch(mid_kernel<4, 2, false, 2>);
+  else if (a.M <= 32)
+    small ? launch(mid_kernel<2, 2, true, 2>) : launch(mid_kernel<4, 2, true, 1>);
+  else if (a.out_bf16)
+    small ? launch(mid_kernel<2, 4, false, 2>) : launch(mid_kernel<4, 4, false, 1>);
+  else
+    small ? launch(mid_kernel<2, 4, true, 2>) : launch(mid_kernel<4, 4, true, 1>);
+}
+
 void launch_fp8_gemm(const moe_fp8_dims& m, const void* xq, const float* xs, const void* packed,
-                     void* out, hipStream_t stream) {
+                     void* out, void* workspace, hipStream_t stream) {
   const int Kb = fp8_kb(m.K);
   const uint8_t* q = static_cast<const uint8_t*>(xq);
   const uint8_t* w = static_cast<const uint8_t*>(packed);
   const float* ws = reinterpret_cast<const float*>(w + fp8_tile_bytes(m.N, m.K));
   const bool bf = m.out_type == MOE_BF16;
-  if (m.M > 128) {
-    const Fp8TileArgs a = {q, xs, w, ws, out, m.M, m.N, Kb, bf, 0, 0};
-    // A step of one 256 x 256 tile a CU takes about 2.1 us, of two 128 x 128
-    // tiles 1.25 us; rounds over the 256 CUs times that decide. Measured (us,
-    // K = 7168, N = 4096, 256 against 128 tiles): M = 8192 240 / 259, M = 4096
-    // 122 / 135, M = 2048 107 / 69.5.
-    const auto rounds = [&](int tile, int slots) {
-      const size_t t = static_cast<size_t>((m.N + tile - 1) / tile) * ((m.M + tile - 1) / tile);
-      return (t + slots - 1) / slots;
-    };
-    if (!bf)
-      launch_tiles<4, 4, 2, 2, true>(a, stream);
-    else if (rounds(256, 256) * 210 <= rounds(128, 512) * 125)
+  const Plan p = fp8_plan(m);
+  const SplitK split = split_of(p, workspace);
+  if (p.form == kRows) {
+    launch_rows<kRowsQ>(RowsArgs{nullptr, q, xs, w, ws, out, m.M, m.N, m.K, Kb, bf, 0, split}, p,
+                        stream);
+  } else if (p.form == kMid) {
+    const MidArgs a = {q, xs, w, ws, out, m.M, m.N, Kb, bf, ceil_div(m.N, mid_rows(m)), p.tiles, split};
+    launch_mid(a, mid_rows(m), p.tiles * p.parts, stream);
+  } else {
+    const Fp8TileArgs a = {q, xs, w, ws, out, m.M, m.N, Kb, bf, 0, 0, split};
+    if (p.form == kTile256)
       launch_tiles<8, 4, 2, 4, false>(a, stream);
-    else
+    else if (bf)
       launch_tiles<4, 4, 2, 2, false>(a, stream);
-    return;
+    else
+      launch_tiles<4, 4, 2, 2, true>(a, stream);
   }
-  const int rbs = (m.N + 63) / 64;
-  const int tgs = m.M <= 16 ? 1 : (m.M + 63) / 64;
-  const dim3 grid(static_cast<unsigned>(rbs) * tgs);
-  if (m.M <= 16)
-    gemm_kernel<4, 1><<<grid, 512, 0, stream>>>(q, xs, w, ws, out, m.M, m.N, Kb, bf, rbs);
-  else
-    gemm_kernel<4, 4><<<grid, 512, 0, stream>>>(q, xs, w, ws, out, m.M, m.N, Kb, bf, rbs);
 }
 
-size_t gemm_workspace(const moe_fp8_dims&) { return 256; }
+// few rows, quantised by the product's own workgroups; false if that is not for them
+bool launch_fp8_fused(const moe_fp8_dims& m, const void* x, const void* packed, void* out,
+                      void* workspace, hipStream_t stream) {
+  const Plan p = fp8_plan(m);
+  const int Kb = fp8_kb(m.K);
+  if (p.form != kRows || m.M * ceil_div(Kb, p.parts) > kFusedItems) return false;
+  const uint8_t* w = static_cast<const uint8_t*>(packed);
+  const float* ws = reinterpret_cast<const float*>(w + fp8_tile_bytes(m.N, m.K));
+  const RowsArgs a = {x,   nullptr, nullptr, w,  ws, out, m.M, m.N, m.K, Kb, m.out_type == MOE_BF16,
+                      0, split_of(p, workspace)};
+  if (m.in_type == MOE_BF16)
+    launch_rows<kRowsBf16>(a, p, stream);
+  else
+    launch_rows<kRowsFp32>(a, p, stream);
+  return true;
+}
+
 size_t quant_bytes(const moe_fp8_dims& m) {
   return round_up(static_cast<size_t>(m.M) * fp8_kb(m.K) * kFp8Block, 256);
 }
@@ -329,7 +702,7 @@ int moe_fp8_gemm(const moe_fp8_dims* dims, const void* xq, const float* xs, cons
                   aligned16(workspace),
               MOE_ERR_ALIGN);
   MOE_REQUIRE(workspace_bytes >= gemm_workspace(*dims), MOE_ERR_WORKSPACE);
-  launch_fp8_gemm(*dims, xq, xs, w_packed, out, stream);
+  launch_fp8_gemm(*dims, xq, xs, w_packed, out, workspace, stream);
   return launch_status();
 }
 
@@ -349,8 +722,10 @@ int moe_fp8_proj(const moe_fp8_dims* dims, const void* x, const void* w_packed, 
   MOE_REQUIRE(workspace_bytes >= moe_fp8_proj_workspace_bytes(dims), MOE_ERR_WORKSPACE);
   uint8_t* xq = static_cast<uint8_t*>(workspace) + gemm_workspace(*dims);
   float* xs = reinterpret_cast<float*>(xq + quant_bytes(*dims));
-  launch_fp8_quant(x, dims->in_type, xq, xs, dims->M, dims->K, nullptr, stream);
-  launch_fp8_gemm(*dims, xq, xs, w_packed, out, stream);
+  if (!launch_fp8_fused(*dims, x, w_packed, out, workspace, stream)) {
+    launch_fp8_quant(x, dims->in_type, xq, xs, dims->M, dims->K, nullptr, stream);
+    launch_fp8_gemm(*dims, xq, xs, w_packed, out, workspace, stream);
+  }
   return launch_status();
 }
 

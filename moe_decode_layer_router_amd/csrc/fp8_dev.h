@@ -21,7 +21,6 @@ typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kFp8Block = 128;     // K (and weight rows) a scale covers
 constexpr int kFp8TileBytes = 2048;  // 16 rows x 128 K
-constexpr float kE4m3Max = 448.0f;
 
 __host__ __device__ inline int fp8_kb(int K) { return (K + kFp8Block - 1) / kFp8Block; }
 // row tiles, padded to whole blocks of 64 rows
@@ -86,31 +85,122 @@ __device__ __forceinline__ i32x8_t join8(u32x4_t lo, u32x4_t hi) {
 
 // The scale of a block of magnitude `amax`: 2^e with the smallest e >= -126
 // and amax <= 448 * 2^e; NaN if amax is not finite. 448 = 1.75 * 2^8, so e is
-// amax's exponent less 8, plus one where its mantissa is above 1.75. `inv` = 1 / scale
-// (exact; e <= 120, so it is a normal number).
-__device__ __forceinline__ float fp8_block_scale(float amax, float& inv) {
+// amax's exponent less 8, plus one where its mantissa is above 1.75.
+__device__ __forceinline__ float fp8_block_scale(float amax) {
   const uint32_t u = __float_as_uint(amax);
   int f = static_cast<int>(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // e + 127
   f = f < 1 ? 1 : f;
-  if ((u >> 23) >= 255u) {
-    inv = __uint_as_float(0x7fc00000u);
-    return inv;
+  return __uint_as_float((u >> 23) >= 255u ? 0x7fc00000u : static_cast<uint32_t>(f) << 23);
+}
+
+// four outputs of a row at element `at`, `left` of them inside the row; quad: rows
+// start at multiples of 4; kFp32: fp32 outputs are possible
+template <bool kFp32>
+__device__ __forceinline__ void store4(void* out, size_t at, int left, bool quad, f32x4_t v,
+                                       bool bf16) {
+  if (left <= 0) return;
+  if (!kFp32 || bf16) {
+    uint16_t* o = static_cast<uint16_t*>(out) + at;
+    const u32x2_t p = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    if (quad) {
+      *reinterpret_cast<u32x2_t*>(o) = p;
+    } else {
+      o[0] = static_cast<uint16_t>(p[0]);
+      if (left > 1) o[1] = static_cast<uint16_t>(p[0] >> 16);
+      if (left > 2) o[2] = static_cast<uint16_t>(p[1]);
+      if (left > 3) o[3] = static_cast<uint16_t>(p[1] >> 16);
+    }
+  } else {
+    float* o = static_cast<float*>(out) + at;
+    if (quad) {
+      *reinterpret_cast<f32x4_t*>(o) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < left) o[i] = v[i];
+    }
   }
-  inv = __uint_as_float(static_cast<uint32_t>(254 - f) << 23);
-  return __uint_as_float(static_cast<uint32_t>(f) << 23);
 }
 
-// max of magnitudes that keeps a NaN (fmaxf would drop it): non-negative
-// floats order as their bit patterns, NaNs above infinity
-__device__ __forceinline__ float max_mag(float a, float b) {
-  const uint32_t ua = __float_as_uint(a) & 0x7fffffffu, ub = __float_as_uint(b) & 0x7fffffffu;
-  return __uint_as_float(ua > ub ? ua : ub);
+// ---------------------------------------------------------------- K parts
+//
+// A product with too few tiles to fill the CUs is split over K: `parts`
+// workgroups a tile, each leaving its fp32 sums in memory; the last of a tile to
+// finish adds them in part order (deterministic) and writes the output. Sums are
+// stored through to memory (a device-scope release would write back the
+// whole L2), counted once every thread's stores are done, and loaded through.
+struct SplitK {
+  int parts;
+  int32_t* counters;  // one a tile, zero between calls
+  f32x4_t* sums;      // [tile][part][kN][threads]
+};
+
+constexpr int kSplitTiles = 256;                        // most tiles that are split
+constexpr size_t kSplitCounterBytes = 256 * kSplitTiles;  // 256 bytes apart: a line each
+
+__device__ __forceinline__ void store16_through(f32x4_t* p, f32x4_t v) {
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+  typedef uint64_t u64x2_t __attribute__((ext_vector_type(2)));
+  const u64x2_t u = __builtin_bit_cast(u64x2_t, v);
+  __hip_atomic_store(q, u[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(q + 1, u[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4_t load16_through(f32x4_t* p) {
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+  typedef uint64_t u64x2_t __attribute__((ext_vector_type(2)));
+  const u64x2_t u = {__hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+                     __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)};
+  return __builtin_bit_cast(f32x4_t, u);
 }
 
-// four fp32, each |v| <= 448 (or NaN), to e4m3, round to nearest even
-__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
+// v: this thread's kN sums of part p of tile `tile` (threads with `on`). True in
+// the workgroup that holds the tile's totals afterwards. Every thread of the
+// workgroup calls it; `last` is a word of LDS that nothing else uses by then.
+template <int kN>
+__device__ __forceinline__ bool join_parts(const SplitK& k, int tile, int p, bool on,
+                                           f32x4_t (&v)[kN], int* last) {
+  if (k.parts == 1) return true;
+  f32x4_t* t = k.sums + static_cast<size_t>(tile) * k.parts * kN * blockDim.x + threadIdx.x;
+  if (on) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      store16_through(t + (static_cast<size_t>(p) * kN + i) * blockDim.x, v[i]);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int32_t* c = k.counters + tile * 64;
+    *last = __hip_atomic_fetch_add(c, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == k.parts - 1;
+    if (*last) __hip_atomic_store(c, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!*last) return false;
+  if (on) {
+    constexpr int kBatch = kN >= 16 ? 1 : 16 / kN > 8 ? 8 : 16 / kN;  // parts loaded together
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = f32x4_t{0, 0, 0, 0};
+    for (int q = 0; q < k.parts; q += kBatch) {
+      f32x4_t u[kBatch][kN];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          u[j][i] = load16_through(t + (static_cast<size_t>(min(q + j, k.parts - 1)) * kN + i) *
+                                           blockDim.x);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (q + j < k.parts) v[i] += u[j][i];
+    }
+  }
+  return true;
+}
+
+// blocks [kb0, kb1) of part p
+__device__ __forceinline__ void part_range(int Kb, int parts, int p, int& kb0, int& kb1) {
+  kb0 = static_cast<int>(static_cast<int64_t>(Kb) * p / parts);
+  kb1 = static_cast<int>(static_cast<int64_t>(Kb) * (p + 1) / parts);
 }
 
 }  // namespace moeblk

@@ -41,6 +41,7 @@ struct Fp8TileArgs {
   int M, N, Kb;
   bool out_bf16;
   int tiles_n, tiles_m;
+  SplitK split;
 };
 
 // Workgroup b -> tile. Consecutive workgroups go round the 8 XCDs; each XCD
@@ -57,35 +58,6 @@ __device__ __forceinline__ void fp8_tile_of(int b, int tiles_n, int tiles_m, int
   tn = in / gm;
 }
 
-// four outputs of a row at element `at`, `left` of them inside the row; quad: rows
-// start at multiples of 4
-template <bool kExact>
-__device__ __forceinline__ void store4(void* out, size_t at, int left, bool quad, f32x4_t v,
-                                       bool bf16) {
-  if (left <= 0) return;
-  if (!kExact || bf16) {
-    uint16_t* o = static_cast<uint16_t*>(out) + at;
-    const u32x2_t p = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    if (quad) {
-      *reinterpret_cast<u32x2_t*>(o) = p;
-    } else {
-      o[0] = static_cast<uint16_t>(p[0]);
-      if (left > 1) o[1] = static_cast<uint16_t>(p[0] >> 16);
-      if (left > 2) o[2] = static_cast<uint16_t>(p[1]);
-      if (left > 3) o[3] = static_cast<uint16_t>(p[1] >> 16);
-    }
-  } else {
-    float* o = static_cast<float*>(out) + at;
-    if (quad) {
-      *reinterpret_cast<f32x4_t*>(o) = v;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < left) o[i] = v[i];
-    }
-  }
-}
-
 template <int kRT, int kTT, int kWN, int kWM, bool kExact>
 __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
   constexpr int kWaves = kWN * kWM;
@@ -98,8 +70,11 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
   const int m16 = lane & 15, g = lane >> 4;
   const int wn = wave % kWN, wm = wave / kWN;
   int tn, tm;
-  fp8_tile_of(blockIdx.x, a.tiles_n, a.tiles_m, tn, tm);
+  const int tiles = a.tiles_n * a.tiles_m, part = blockIdx.x / tiles;
+  fp8_tile_of(blockIdx.x - part * tiles, a.tiles_n, a.tiles_m, tn, tm);
   const int Kb = a.Kb, M = a.M;
+  int kb0, kb1;  // this workgroup's K part
+  part_range(Kb, a.split.parts, part, kb0, kb1);
   const size_t Kp = static_cast<size_t>(Kb) * kFp8Block;
 
   // This wave's copies, pieces wave + i kWaves: bases that are the same for the
@@ -179,12 +154,12 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
     }
   };
 
-  load_scales(0);
+  load_scales(kb0);
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) copy(i, 0, 0, 0);
-  if (Kb > 1) {
+  for (int i = 0; i < kLoads; ++i) copy(i, kb0, 0, 0);
+  if (kb0 + 1 < kb1) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) copy(i, 1, 1, 1);
+    for (int i = 0; i < kLoads; ++i) copy(i, kb0 + 1, 1, 1);
   }
   wait_all();
   i32x8_t w[2], b[kTT];
@@ -195,7 +170,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
   // one step; kCopy: there is a step kb + 2, kMore: there is a step kb + 1
   const auto step = [&](int kb, int wb, int wb1, int wb2, auto copy_c, auto more_c) {
     constexpr bool kCopy = decltype(copy_c)::value, kMore = decltype(more_c)::value;
-    const int xb = kb & 1;
+    const int xb = (kb - kb0) & 1;
     float s_now[kTT];
 #pragma unroll
     for (int t = 0; t < kTT; ++t) s_now[t] = s_next[t];
@@ -242,13 +217,13 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
       }
     }
   };
-  int kb = 0, wb = 0;
-  for (; kb + 2 < Kb; ++kb) {
+  int kb = kb0, wb = 0;
+  for (; kb + 2 < kb1; ++kb) {
     const int wb1 = wb == 2 ? 0 : wb + 1, wb2 = wb1 == 2 ? 0 : wb1 + 1;
     step(kb, wb, wb1, wb2, std::true_type{}, std::true_type{});
     wb = wb1;
   }
-  if (kb + 1 < Kb) {
+  if (kb + 1 < kb1) {
     const int wb1 = wb == 2 ? 0 : wb + 1;
     step(kb, wb, wb1, 0, std::false_type{}, std::true_type{});
     wb = wb1;
@@ -261,6 +236,11 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
     for (int i = 0; i < 4; ++i)
       acc[kRT - 1][t][i] = __builtin_fmaf(d[t][i], s[t], acc[kRT - 1][t][i]);
 
+  if constexpr (kRT * kTT <= 16) {  // the larger tiles are never split
+    f32x4_t(&v)[kRT * kTT] = reinterpret_cast<f32x4_t(&)[kRT * kTT]>(acc);
+    if (!join_parts(a.split, tm * a.tiles_n + tn, part, true, v, reinterpret_cast<int*>(lds)))
+      return;
+  }
   // lane: token m16 of a token tile, outputs 4 g .. + 3 of a row tile
 #pragma unroll
   for (int t = 0; t < kTT; ++t) {
