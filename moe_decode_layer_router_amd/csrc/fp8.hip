@@ -5,6 +5,7 @@
 
 #include "fp8_dev.h"
 #include "fp8_launch.h"
+#include "fp8_quant.h"
 #include "fp8_tile.h"
 #include "host.h"
 
@@ -12,106 +13,16 @@ namespace moeblk {
 namespace {
 
 // ---------------------------------------------------------------- quantise
-//
-// A (row, 128-column block) is 8 lanes of 16 columns: its magnitude maximum is
-// three DPP steps, each lane stores 16 bytes. Division by the scale is part of
-// the converts and exact (a power of two), so the only rounding is e4m3's.
-// Magnitudes are compared as integers (non-negative floats order as their bit
-// patterns, infinity and NaN last), two bf16 at a time.
-typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
-typedef int16_t i16x2_t __attribute__((ext_vector_type(2)));
 
-template <typename T>
-struct Raw16 {  // 16 columns of a row as loaded
-  uint32_t w[4 * sizeof(T)];
-};
-
-template <typename T, bool kVec>
-__device__ __forceinline__ void load16(const T* row, int c0, int K, Raw16<T>& v) {
-  if (kVec && c0 + 16 <= K) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) {
-      const u32x4_t q = *reinterpret_cast<const u32x4_t*>(row + c0 + 16 / sizeof(T) * i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v.w[4 * i + j] = q[j];
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(4 * sizeof(T)); ++i) v.w[i] = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (c0 + i < K) {
-      if constexpr (sizeof(T) == 2)
-        v.w[i >> 1] |= static_cast<uint32_t>(row[c0 + i]) << (16 * (i & 1));
-      else
-        v.w[i] = __float_as_uint(row[c0 + i]);
-    }
-  }
-}
-
-template <int kCtrl>
-__device__ __forceinline__ uint32_t max_dpp(uint32_t v) {
-  const uint32_t o = static_cast<uint32_t>(
-      __builtin_amdgcn_update_dpp(0, static_cast<int>(v), kCtrl, 0xf, 0xf, false));
-  return v > o ? v : o;
-}
-
-// 16 columns of a block by one of 8 adjacent lanes: the e4m3 values, and the
-// block's scale (the same in all 8 lanes, which must all take part)
-template <typename T>
-__device__ __forceinline__ u32x4_t quant16(const Raw16<T>& v, float& scale) {
-  uint32_t m;
-  if constexpr (sizeof(T) == 2) {
-    u16x2_t p = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      p = __builtin_elementwise_max(p, __builtin_bit_cast(u16x2_t, v.w[i] & 0x7fff7fffu));
-    m = static_cast<uint32_t>(p[0] > p[1] ? p[0] : p[1]) << 16;
-  } else {
-    m = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t a = v.w[i] & 0x7fffffffu;
-      m = m > a ? m : a;
-    }
-  }
-  m = max_dpp<0xb1>(m);   // lane ^ 1
-  m = max_dpp<0x4e>(m);   // lane ^ 2
-  m = max_dpp<0x141>(m);  // the mirror within 8 lanes: the other four
-  scale = fp8_block_scale(__uint_as_float(m));
-  u32x4_t q;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    i16x2_t r = {0, 0};
-    if constexpr (sizeof(T) == 2) {
-      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, v.w[2 * i]),
-                                                    scale, false);
-      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, v.w[2 * i + 1]),
-                                                    scale, true);
-    } else {
-      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(v.w[4 * i]),
-                                                   __uint_as_float(v.w[4 * i + 1]), scale, false);
-      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, __uint_as_float(v.w[4 * i + 2]),
-                                                   __uint_as_float(v.w[4 * i + 3]), scale, true);
-    }
-    q[i] = __builtin_bit_cast(uint32_t, r);
-  }
-  return q;
-}
-
-// nrows: rows to quantise, or NULL for all `M` (a device count, for bucket rows)
 template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void quant_kernel(const T* __restrict__ x,
                                                     uint8_t* __restrict__ xq,
-                                                    float* __restrict__ xs, int M, int K, int Kb,
-                                                    const int32_t* __restrict__ nrows) {
+                                                    float* __restrict__ xs, int M, int K, int Kb) {
   const size_t item = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) >> 3;
   const int l8 = threadIdx.x & 7;
   const size_t row = item / Kb;
   const int kb = static_cast<int>(item - row * Kb);
-  const int n = nrows ? min(*nrows, M) : M;
-  if (row >= static_cast<size_t>(n)) return;
+  if (row >= static_cast<size_t>(M)) return;
   Raw16<T> v;
   float sc;
   load16<T, kVec>(x + row * K, kb * kFp8Block + l8 * 16, K, v);
@@ -445,21 +356,21 @@ __global__ __launch_bounds__(512) void mid_kernel(MidArgs a) {
 }  // namespace
 
 void launch_fp8_quant(const void* x, int in_type, uint8_t* xq, float* xs, int M, int K,
-                      const int32_t* nrows, hipStream_t stream) {
+                      hipStream_t stream) {
   const int Kb = fp8_kb(K);
   const dim3 grid(static_cast<unsigned>((static_cast<size_t>(M) * Kb * 8 + 255) / 256));
   if (in_type == MOE_BF16) {
     const uint16_t* p = static_cast<const uint16_t*>(x);
     if (K % 8 == 0)
-      quant_kernel<uint16_t, true><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb, nrows);
+      quant_kernel<uint16_t, true><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb);
     else
-      quant_kernel<uint16_t, false><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb, nrows);
+      quant_kernel<uint16_t, false><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb);
   } else {
     const float* p = static_cast<const float*>(x);
     if (K % 4 == 0)
-      quant_kernel<float, true><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb, nrows);
+      quant_kernel<float, true><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb);
     else
-      quant_kernel<float, false><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb, nrows);
+      quant_kernel<float, false><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb);
   }
 }
 
@@ -684,8 +595,7 @@ int moe_fp8_quant(const moe_fp8_dims* dims, const void* x, void* xq, float* xs,
   if (rc) return rc;
   MOE_REQUIRE(x && xq && xs, MOE_ERR_NULL);
   MOE_REQUIRE(aligned16(x) && aligned16(xq) && aligned16(xs), MOE_ERR_ALIGN);
-  launch_fp8_quant(x, dims->in_type, static_cast<uint8_t*>(xq), xs, dims->M, dims->K, nullptr,
-                   stream);
+  launch_fp8_quant(x, dims->in_type, static_cast<uint8_t*>(xq), xs, dims->M, dims->K, stream);
   return launch_status();
 }
 
@@ -723,7 +633,7 @@ int moe_fp8_proj(const moe_fp8_dims* dims, const void* x, const void* w_packed, 
   uint8_t* xq = static_cast<uint8_t*>(workspace) + gemm_workspace(*dims);
   float* xs = reinterpret_cast<float*>(xq + quant_bytes(*dims));
   if (!launch_fp8_fused(*dims, x, w_packed, out, workspace, stream)) {
-    launch_fp8_quant(x, dims->in_type, xq, xs, dims->M, dims->K, nullptr, stream);
+    launch_fp8_quant(x, dims->in_type, xq, xs, dims->M, dims->K, stream);
     launch_fp8_gemm(*dims, xq, xs, w_packed, out, workspace, stream);
   }
   return launch_status();

@@ -1,147 +1,265 @@
 // fp8_ffn.hip -- the expert FFNs on FP8 weights with block-128 scales
 // (moe_fp8_expert_ffn), and their weight packing.
 //
-// Four launches: the rows x to e4m3; gate_up + SwiGLU of every (expert, block of
-// 64 packed rows = 32 intermediates), h in fp32; h to e4m3; down of every
-// (expert, 64 output rows). A workgroup's 8 waves take every eighth K block and
-// stream the packed weights straight into registers.
+// gate_up + SwiGLU of every (expert, block of 64 packed rows = 32 intermediates),
+// h in fp32, then down of every (expert, 64 output rows). The weights' bytes bound
+// both. A workgroup's 4 waves take every fourth K block, a ring of blocks' loads in
+// flight each, straight from the packed order into registers (exact form,
+// fp8_dev.h); the waves' sums are added through LDS in wave order.
+//
+// The rows of either launch are quantised by its own workgroups, into LDS, while
+// their first weight loads are in flight, in steps of up to 16 rows whose (row, K
+// block) pairs fit (kFusedItems; an expert rarely has more than a few of the rows);
+// else by a launch of their own in front of it.
+#include <type_traits>
+
 #include "fp8_dev.h"
 #include "fp8_launch.h"
+#include "fp8_quant.h"
 #include "host.h"
 
 namespace moeblk {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
+constexpr int kFusedRows = 16;    // most rows of a step whose workgroups quantise
+constexpr int kFusedItems = 576;  // most (row, K block) pairs: two workgroups a CU
+constexpr int kFewItems = 256;    // three
+constexpr int kCpolNt = 2;        // cache-policy operand of the buffer intrinsics: non-temporal
 
+// rows of a launch: quantised (xq, xs), or (fused) as they are
 struct RowSet {
+  const void* x;      // bf16 (gate_up) or fp32 (down) rows, K columns
   const uint8_t* xq;  // e4m3 rows
-  const float* xs;    // scales [Kb][xs_rows]
-  int xs_rows;        // rows of the scale array
-  size_t Kp;          // bytes a row
+  const float* xs;    // scales [Kb][rows]
+  int rows;           // rows of the set
 };
-
-// 64 packed weight rows x 16 kTT tokens over all K blocks: acc[r][t] of this
-// wave. `tok`: this lane's row of the row set for each token tile. Lane rows 0,
-// 1 of a D tile take the scale sw0, rows 2, 3 sw1 (gate / up; the same array for
-// down).
-template <int kTT>
-__device__ __forceinline__ void stream_rows(const uint8_t* wt, const float* sw0, const float* sw1,
-                                            int Kb, const RowSet& x, const int (&tok)[kTT],
-                                            int wave, int lane, f32x4_t (&acc)[4][kTT]) {
-  const int g = lane >> 4;
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int t = 0; t < kTT; ++t) acc[r][t] = f32x4_t{0, 0, 0, 0};
-  for (int kb = wave; kb < Kb; kb += kWaves) {
-    Bf16Frag a[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint8_t* p = wt + (static_cast<size_t>(r) * Kb + kb) * kFp8TileBytes + lane * 16;
-      a[r] = e4m3_to_bf16(join8(ld_nt<u32x4_t>(p), ld_nt<u32x4_t>(p + 1024)));
-    }
-    const float w0 = sw0[kb], w1 = sw1[kb];
-#pragma unroll
-    for (int t = 0; t < kTT; ++t) {
-      const uint8_t* p = x.xq + tok[t] * x.Kp + kb * kFp8Block + 32 * g;
-      const Bf16Frag b = e4m3_to_bf16(join8(*reinterpret_cast<const u32x4_t*>(p),
-                                            *reinterpret_cast<const u32x4_t*>(p + 16)));
-      const float s = x.xs[static_cast<size_t>(kb) * x.xs_rows + tok[t]];
-      const float s0 = s * w0, s1 = s * w1;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const f32x4_t d = mfma_exact_block(a[r], b);
-        acc[r][t][0] = __builtin_fmaf(d[0], s0, acc[r][t][0]);
-        acc[r][t][1] = __builtin_fmaf(d[1], s0, acc[r][t][1]);
-        acc[r][t][2] = __builtin_fmaf(d[2], s1, acc[r][t][2]);
-        acc[r][t][3] = __builtin_fmaf(d[3], s1, acc[r][t][3]);
-      }
-    }
-  }
-}
-
-// sums the waves' acc[.][t] in wave order; wave r < 4 returns the sum of row
-// tile r in its lanes
-template <int kTT>
-__device__ __forceinline__ f32x4_t sum_waves(f32x4_t (&red)[kWaves][4][64],
-                                             const f32x4_t (&acc)[4][kTT], int t, int wave,
-                                             int lane) {
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < 4; ++r) red[wave][r][lane] = acc[r][t];
-  __syncthreads();
-  f32x4_t s = {0, 0, 0, 0};
-  if (wave < 4) {
-    s = red[0][wave][lane];
-#pragma unroll
-    for (int v = 1; v < kWaves; ++v) s += red[v][wave][lane];
-  }
-  return s;
-}
 
 struct FfnArgs {
   int S, d, n_local, r_max, I, Is;
   const int32_t *counts, *offsets, *rows, *active;
   const uint8_t *w13, *w2, *ws13, *ws2;  // packed; ws*: shared expert or NULL
-  RowSet x;                              // quantised input rows
-  RowSet h, hsh;                         // quantised SwiGLU rows: routed, shared
+  RowSet x, h, hsh;                      // input rows; SwiGLU rows: routed, shared
   float *hf, *hshf;                      // fp32 SwiGLU rows: routed [r_max][I], shared [S][Is]
   uint16_t* y;
 };
 
+// LDS of a workgroup: the quantised rows, then (one token group) the waves' sums
+struct Sums {
+  f32x4_t v[kWaves][4][64];
+};
+template <int kItems>
+struct FusedRows {
+  uint8_t x[kItems * kFp8Block];
+  float s[kItems];
+};
+
 __device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// token groups of one weight block, 16 kTT tokens each
-template <int kTT, bool kDown>
-__device__ __forceinline__ void ffn_block(const FfnArgs& a, bool shared, int el, int rb,
-                                          f32x4_t (&red)[kWaves][4][64]) {
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes),
+                                           0x00020000);
+}
+
+// One block of 64 packed weight rows of an expert, all of its tokens in groups of
+// 16 kTT. Lane rows 0, 1 of a D tile are gate rows and 2, 3 up rows (one scale
+// each; in down the same one).
+template <int kTT, bool kDown, int kItems>
+__device__ __forceinline__ void ffn_block(const FfnArgs& a, bool shared, int el, int rb, int n,
+                                          Sums& sums, FusedRows<kItems>& fl) {
+  constexpr bool kFused = kItems > 0;
+  constexpr bool kExact = !kDown;
+  constexpr int kRing = kTT == 1 ? 2 : 1;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int uwave = __builtin_amdgcn_readfirstlane(wave);
   const int m16 = lane & 15, g = lane >> 4;
   const int I = shared ? a.Is : a.I;
   const int N = kDown ? a.d : 2 * I, K = kDown ? I : a.d, Kb = K / kFp8Block;
-  const uint8_t* w = kDown ? (shared ? a.ws2 : a.w2) : (shared ? a.ws13 : a.w13);
-  w += el * fp8_packed_bytes(N, K);
-  const float* sc = reinterpret_cast<const float*>(w + fp8_tile_bytes(N, K));
-  const uint8_t* wt = w + static_cast<size_t>(rb) * 4 * Kb * kFp8TileBytes;
+  const uint8_t* wm = kDown ? (shared ? a.ws2 : a.w2) : (shared ? a.ws13 : a.w13);
+  wm += el * fp8_packed_bytes(N, K);
+  const float* sc = reinterpret_cast<const float*>(wm + fp8_tile_bytes(N, K));
   const float* sw0 = sc + static_cast<size_t>(kDown ? rb / 2 : rb / 4) * Kb;
-  const float* sw1 = kDown ? sw0 : sc + static_cast<size_t>((I / 128 + rb / 4)) * Kb;
+  const float* sw1 = kDown ? sw0 : sc + static_cast<size_t>(I / 128 + rb / 4) * Kb;
   const int base = shared ? 0 : a.offsets[el];
-  const int n = shared ? a.S : a.counts[el];
-  const RowSet x = kDown ? (shared ? a.hsh : a.h) : a.x;
+  const RowSet& set = kDown ? (shared ? a.hsh : a.h) : a.x;
+  const __amdgpu_buffer_rsrc_t wr =
+      rsrc(wm + static_cast<size_t>(rb) * 4 * Kb * kFp8TileBytes, 4 * Kb * kFp8TileBytes);
+  const __amdgpu_buffer_rsrc_t xr = rsrc(set.xq, static_cast<size_t>(set.rows) * K);
+  const __amdgpu_buffer_rsrc_t sr = rsrc(set.xs, static_cast<size_t>(set.rows) * Kb * 4);
+  // row r of this expert in the row set
+  const auto row_of = [&](int r) {
+    return (kDown || shared) ? base + r : min(max(a.rows[base + r], 0), a.S - 1);
+  };
+
   for (int t0 = 0; t0 < n; t0 += 16 * kTT) {
-    int tok[kTT];
+    u32x4_t w[kRing][4][2], x[kFused ? 1 : kRing][kTT][2];
+    float s[kFused ? 1 : kRing][kTT], w0[kRing], w1[kRing];
+    uint32_t tok[kTT];
+    const auto load_w = [&](int i, int kb) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t at = static_cast<uint32_t>(r * Kb + kb) * kFp8TileBytes;
+        w[i][r][0] = __builtin_bit_cast(
+            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16, at, kCpolNt));
+        w[i][r][1] = __builtin_bit_cast(
+            u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, lane * 16, at + 1024, kCpolNt));
+      }
+      w0[i] = sw0[kb];
+      w1[i] = sw1[kb];
+    };
+    const auto load_x = [&](int i, int kb) {
+      if constexpr (!kFused) {
+#pragma unroll
+        for (int t = 0; t < kTT; ++t) {
+          const uint32_t v = tok[t] * static_cast<uint32_t>(K) + 32 * g;
+          x[i][t][0] = __builtin_bit_cast(
+              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(xr, v, kb * kFp8Block, 0));
+          x[i][t][1] = __builtin_bit_cast(
+              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(xr, v + 16, kb * kFp8Block, 0));
+          s[i][t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                  sr, tok[t] * 4, kb * set.rows * 4, 0));
+        }
+      }
+    };
+    // the first weights are on their way before the rows are known
+#pragma unroll
+    for (int i = 0; i < kRing; ++i)
+      if (uwave + i * kWaves < Kb) load_w(i, uwave + i * kWaves);
 #pragma unroll
     for (int t = 0; t < kTT; ++t) {
       const int r = min(t0 + 16 * t + m16, n - 1);
-      tok[t] = (kDown || shared) ? base + r : min(max(a.rows[base + r], 0), a.S - 1);
+      tok[t] = kFused ? r : row_of(r);
     }
+    if constexpr (kFused) {
+      {  // item kb * n + r; 16-byte chunks permuted by chunk ^ (r % 8)
+        using T = typename std::conditional<kDown, float, uint16_t>::type;
+        const int l8 = threadIdx.x & 7;
+        for (int item = threadIdx.x >> 3; item < n * Kb; item += kWaves * 8) {
+          const int r = item % n, kb = item / n;
+          Raw16<T> v;
+          load16<T, true>(static_cast<const T*>(set.x) + static_cast<size_t>(row_of(r)) * K,
+                          kb * kFp8Block + l8 * 16, K, v);
+          float scale;
+          const u32x4_t q = quant16(v, scale);
+          *reinterpret_cast<u32x4_t*>(fl.x + item * kFp8Block + ((l8 ^ (r & 7)) * 16)) = q;
+          if (l8 == 0) fl.s[item] = scale;
+        }
+        __syncthreads();
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRing; ++i)
+        if (uwave + i * kWaves < Kb) load_x(i, uwave + i * kWaves);
+    }
+
     f32x4_t acc[4][kTT];
-    stream_rows<kTT>(wt, sw0, sw1, Kb, x, tok, wave, lane, acc);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int t = 0; t < kTT; ++t) acc[r][t] = f32x4_t{0, 0, 0, 0};
+    for (int first = uwave; first < Kb; first += kWaves * kRing) {
+#pragma unroll
+      for (int i = 0; i < kRing; ++i) {
+        const int kb = first + i * kWaves;
+        if (kb < Kb) {
+          constexpr bool kHold = kExact && kTT <= 2;  // else the converted rows do not fit
+          i32x8_t x8[kHold ? 1 : kTT];
+          Bf16Frag xe[kHold ? kTT : 1];
+          float s0[kTT], s1[kTT];
+#pragma unroll
+          for (int t = 0; t < kTT; ++t) {
+            i32x8_t v;
+            float f;
+            if constexpr (kFused) {
+              const int item = kb * n + tok[t];
+              const uint8_t* p = fl.x + item * kFp8Block;
+              const int sw = tok[t] & 7;
+              v = join8(*reinterpret_cast<const u32x4_t*>(p + (((2 * g) ^ sw) * 16)),
+                        *reinterpret_cast<const u32x4_t*>(p + (((2 * g + 1) ^ sw) * 16)));
+              f = fl.s[item];
+            } else {
+              v = join8(x[i][t][0], x[i][t][1]);
+              f = s[i][t];
+            }
+            s0[t] = f * w0[i];
+            s1[t] = f * w1[i];
+            if constexpr (kHold)
+              xe[t] = e4m3_to_bf16(v);
+            else
+              x8[t] = v;
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            // one row tile's operands at a time: the registers of kTT = 2 are tight
+            if constexpr (kTT > 1) __builtin_amdgcn_sched_barrier(0);
+            const i32x8_t w8 = join8(w[i][r][0], w[i][r][1]);
+            Bf16Frag we;
+            if constexpr (kExact) we = e4m3_to_bf16(w8);
+#pragma unroll
+            for (int t = 0; t < kTT; ++t) {
+              f32x4_t d;
+              if constexpr (kHold) {
+                d = mfma_exact_block(we, xe[t]);
+              } else if constexpr (kExact) {
+                i32x8_t v = x8[t];
+                asm volatile("" : "+v"(v));  // converted here, not once for all row tiles
+                d = mfma_exact_block(we, e4m3_to_bf16(v));
+                __builtin_amdgcn_sched_barrier(0);
+              } else {
+                d = mfma_fp8_block(w8, x8[t]);
+              }
+              acc[r][t][0] = __builtin_fmaf(d[0], s0[t], acc[r][t][0]);
+              acc[r][t][1] = __builtin_fmaf(d[1], s0[t], acc[r][t][1]);
+              acc[r][t][2] = __builtin_fmaf(d[2], s1[t], acc[r][t][2]);
+              acc[r][t][3] = __builtin_fmaf(d[3], s1[t], acc[r][t][3]);
+            }
+          }
+          if constexpr (kTT > 1) __builtin_amdgcn_sched_barrier(0);
+          if (kb + kWaves * kRing < Kb) {
+            load_w(i, kb + kWaves * kRing);
+            load_x(i, kb + kWaves * kRing);
+          }
+        }
+      }
+    }
 #pragma unroll
     for (int t = 0; t < kTT; ++t) {
-      const f32x4_t s = sum_waves<kTT>(red, acc, t, wave, lane);
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sums.v[wave][r][lane] = acc[r][t];
+      __syncthreads();
       const int r = t0 + 16 * t + m16;
       if (wave >= 4 || r >= n) continue;
+      f32x4_t v = sums.v[0][wave][lane];
+#pragma unroll
+      for (int u = 1; u < kWaves; ++u) v += sums.v[u][wave][lane];
       if constexpr (kDown) {
         const size_t row = shared ? static_cast<size_t>(a.r_max) + r : static_cast<size_t>(base) + r;
-        const u32x2_t v = {pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
-        *reinterpret_cast<u32x2_t*>(a.y + row * a.d + rb * 64 + wave * 16 + 4 * g) = v;
+        const u32x2_t o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        *reinterpret_cast<u32x2_t*>(a.y + row * a.d + rb * 64 + wave * 16 + 4 * g) = o;
       } else {
         float* hf = (shared ? a.hshf : a.hf) + static_cast<size_t>(base + r) * I;
-        float2 v;
-        v.x = swiglu(s[0], s[2]);
-        v.y = swiglu(s[1], s[3]);
-        *reinterpret_cast<float2*>(hf + rb * 32 + wave * 8 + 2 * g) = v;
+        float2 o;
+        o.x = swiglu(v[0], v[2]);
+        o.y = swiglu(v[1], v[3]);
+        *reinterpret_cast<float2*>(hf + rb * 32 + wave * 8 + 2 * g) = o;
       }
     }
   }
 }
 
-// workgroups: the shared expert's weight blocks, then (expert slot, block)
-template <bool kDown>
-__global__ __launch_bounds__(512) void ffn_kernel(FfnArgs a, int shared_blocks, int blocks) {
-  __shared__ f32x4_t red[kWaves][4][64];
+// kItems > 0: rows quantised here, at most 16 of an expert and kItems (row, K block)
+// pairs. launch_bounds: two workgroups a CU, three with few items (the 16-token
+// form alone needs fewer registers).
+template <bool kDown, int kItems>
+__global__ __launch_bounds__(64 * kWaves, kItems > 0 && kItems <= kFewItems ? 3 : 2) void ffn_kernel(
+    FfnArgs a, int shared_blocks, int blocks) {
+  __shared__ union Lds {
+    Sums sums;
+    FusedRows<kItems> rows;
+    __device__ Lds() {}
+  } lds;
+  // workgroups: the shared expert's weight blocks, then (expert slot, block)
   int b = blockIdx.x, el = 0;
   const bool shared = b < shared_blocks;
   int n = a.S;
@@ -151,14 +269,56 @@ __global__ __launch_bounds__(512) void ffn_kernel(FfnArgs a, int shared_blocks, 
     b -= slot * blocks;
     if (slot >= a.active[0]) return;
     el = a.active[1 + slot];
-    n = a.counts[el];
+    n = min(a.counts[el], a.S);
   }
-  if (n <= 16)
-    ffn_block<1, kDown>(a, shared, el, b, red);
-  else if (n <= 32)
-    ffn_block<2, kDown>(a, shared, el, b, red);
+  if constexpr (kItems > 0) {
+    ffn_block<1, kDown, kItems>(a, shared, el, b, n, lds.sums, lds.rows);
+  } else {
+    if (n <= 16)
+      ffn_block<1, kDown, 0>(a, shared, el, b, n, lds.sums, lds.rows);
+    else
+      ffn_block<4, kDown, 0>(a, shared, el, b, n, lds.sums, lds.rows);
+  }
+}
+
+// the SwiGLU rows of both kinds to e4m3: 8 lanes a (row, K block), the routed ones
+// (rows in front of *used) first
+__global__ __launch_bounds__(256) void quant_h_kernel(FfnArgs a, const int32_t* __restrict__ used) {
+  int item = (blockIdx.x * 256 + threadIdx.x) >> 3;
+  const int l8 = threadIdx.x & 7;
+  const int routed = a.r_max * (a.I / kFp8Block);
+  const bool shared = item >= routed;
+  if (shared) item -= routed;
+  const RowSet& set = shared ? a.hsh : a.h;
+  const int K = shared ? a.Is : a.I, Kb = K / kFp8Block;
+  if (Kb == 0) return;
+  const int row = item / Kb, kb = item - row * Kb;
+  if (row >= (shared ? a.S : min(*used, a.r_max))) return;
+  Raw16<float> v;
+  load16<float, true>(static_cast<const float*>(set.x) + static_cast<size_t>(row) * K,
+                      kb * kFp8Block + l8 * 16, K, v);
+  float scale;
+  const u32x4_t q = quant16(v, scale);
+  *reinterpret_cast<u32x4_t*>(const_cast<uint8_t*>(set.xq) + static_cast<size_t>(row) * K +
+                              kb * kFp8Block + l8 * 16) = q;
+  if (l8 == 0) const_cast<float*>(set.xs)[static_cast<size_t>(kb) * set.rows + row] = scale;
+}
+
+template <bool kDown>
+void launch_step(const FfnArgs& a, int items, int shared_blocks, int blocks, hipStream_t stream) {
+  const unsigned grid = shared_blocks + a.n_local * blocks;
+  if (items == 0)
+    ffn_kernel<kDown, 0><<<grid, 64 * kWaves, 0, stream>>>(a, shared_blocks, blocks);
+  else if (items <= kFewItems)
+    ffn_kernel<kDown, kFewItems><<<grid, 64 * kWaves, 0, stream>>>(a, shared_blocks, blocks);
   else
-    ffn_block<4, kDown>(a, shared, el, b, red);
+    ffn_kernel<kDown, kFusedItems><<<grid, 64 * kWaves, 0, stream>>>(a, shared_blocks, blocks);
+}
+
+// (row, K block) pairs an expert may have where its workgroups quantise them, else 0
+int fused_items(int S, int K) {
+  const int items = S * (K / kFp8Block);
+  return S <= kFusedRows && items <= kFusedItems ? items : 0;
 }
 
 bool weight_shape(const moe_dims& m, int which, int& n, int& N, int& K) {
@@ -255,19 +415,21 @@ int moe_fp8_expert_ffn(const moe_dims* dims, const void* x, const void* w13_pack
   a.counts = counts, a.offsets = offsets, a.rows = rows, a.active = active;
   a.w13 = static_cast<const uint8_t*>(w13_packed), a.w2 = static_cast<const uint8_t*>(w2_packed);
   a.ws13 = static_cast<const uint8_t*>(ws13_packed), a.ws2 = static_cast<const uint8_t*>(ws2_packed);
-  a.x = RowSet{ws + l.xq, f32(l.xs), m.S, static_cast<size_t>(m.d)};
-  a.h = RowSet{ws + l.hq, f32(l.hs), R, static_cast<size_t>(m.I)};
-  a.hsh = RowSet{ws + l.hshq, f32(l.hshs), m.S, static_cast<size_t>(m.shared_I)};
+  a.x = RowSet{x, ws + l.xq, f32(l.xs), m.S};
+  a.h = RowSet{f32(l.hf), ws + l.hq, f32(l.hs), R};
+  a.hsh = RowSet{f32(l.hshf), ws + l.hshq, f32(l.hshs), m.S};
   a.hf = f32(l.hf), a.hshf = f32(l.hshf);
   a.y = static_cast<uint16_t*>(y);
 
-  launch_fp8_quant(x, MOE_BF16, ws + l.xq, f32(l.xs), m.S, m.d, nullptr, stream);
-  const int up_sh = m.shared_I / 32, up = m.I / 32;
-  ffn_kernel<false><<<up_sh + m.n_local * up, 512, 0, stream>>>(a, up_sh, up);
-  launch_fp8_quant(a.hf, MOE_FP32, ws + l.hq, f32(l.hs), R, m.I, offsets + m.n_local, stream);
-  if (sh) launch_fp8_quant(a.hshf, MOE_FP32, ws + l.hshq, f32(l.hshs), m.S, m.shared_I, nullptr, stream);
-  const int dn = m.d / 64, dn_sh = sh ? dn : 0;
-  ffn_kernel<true><<<dn_sh + m.n_local * dn, 512, 0, stream>>>(a, dn_sh, dn);
+  const int up_items = fused_items(m.S, m.d);
+  if (!up_items) launch_fp8_quant(x, MOE_BF16, ws + l.xq, f32(l.xs), m.S, m.d, stream);
+  launch_step<false>(a, up_items, m.shared_I / 32, m.I / 32, stream);
+  const int down_items = fused_items(m.S, m.I > m.shared_I ? m.I : m.shared_I);
+  if (!down_items) {
+    const int items = R * (m.I / kFp8Block) + m.S * (m.shared_I / kFp8Block);
+    quant_h_kernel<<<(items + 31) / 32, 256, 0, stream>>>(a, offsets + m.n_local);
+  }
+  launch_step<true>(a, down_items, sh ? m.d / 64 : 0, m.d / 64, stream);
   return launch_status();
 }
 

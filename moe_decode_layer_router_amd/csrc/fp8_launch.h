@@ -5,10 +5,9 @@
 
 namespace moeblk {
 
-// rows [M][K] (in_type) -> e4m3 [M][Kb * 128] and scales [Kb][M]; with `nrows`
-// only the first *nrows rows (a device count, at most M)
+// rows [M][K] (in_type) -> e4m3 [M][Kb * 128] and scales [Kb][M]
 void launch_fp8_quant(const void* x, int in_type, uint8_t* xq, float* xs, int M, int K,
-                      const int32_t* nrows, hipStream_t stream);
+                      hipStream_t stream);
 // n canonical matrices [N][K] with scales [Nb][Kb] -> packed (fp8_dev.h);
 // which = MOE_W13: rows interleaved gate / up (common.h packed_row)
 void launch_fp8_pack(const void* q, const void* scales, void* packed, int n, int N, int K,
