@@ -206,7 +206,7 @@ __global__ __launch_bounds__(64 * kNW) void rows_kernel(RowsArgs a) {
   }
 }
 
-// ---------------------------------------------------------------- product, 17 to 128 rows
+// ---------------------------------------------------------------- product, from 17 rows
 //
 // 16 kRT weight rows x 16 kTT tokens a workgroup; its 8 waves take every eighth K
 // block of the workgroup's part, two blocks' loads in flight, straight into
@@ -410,7 +410,7 @@ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // few rows: 16 weight rows a workgroup while that gives at most 512 workgroups, else 64
 inline bool thin_rows(const moe_fp8_dims& m) { return m.N <= 16 * 512; }
-// 17 to 128 rows: 32 tokens a workgroup while they are all, else 64; 32 weight rows
+// From 17 rows: 32 tokens a workgroup while they are all, else 64; 32 weight rows
 // while that gives no more workgroups than CUs, else 64 (half the token bytes
 // through L2, but only one K block's loads at a time fit the registers at 64
 // tokens). Measured, us with the quantisation, 32 / 64 rows: M = 128, N = 7168, K
@@ -419,6 +419,16 @@ inline bool thin_rows(const moe_fp8_dims& m) { return m.N <= 16 * 512; }
 inline int mid_tiles_m(const moe_fp8_dims& m) { return ceil_div(m.M, m.M <= 32 ? 32 : 64); }
 inline int mid_rows(const moe_fp8_dims& m) {
   return ceil_div(m.N, 32) * mid_tiles_m(m) <= 256 ? 32 : 64;
+}
+
+// The register kernel (mid) or LDS tiles: mid for one 64-token group, and while its
+// 64-row tiles are few; with more, the tokens' bytes through L2 cost more than
+// the tiles' steps. Measured, us with the quantisation, mid / tiles: M = 160, N =
+// 1000, K = 1000 7.6 / 12.5; M = 160, N = 4096, K = 7168 27.5 / 32.4; M = 300, N = 4096,
+// K = 4096 30.2 / 29.6; M = 128, N = 16384, K = 4096 35.9 / 33.8; M = 512, N = 4096, K =
+// 7168 51.7 / 42.9.
+inline bool use_mid(const moe_fp8_dims& m) {
+  return m.M <= 64 || ceil_div(m.N, 64) * ceil_div(m.M, 64) <= 320;
 }
 
 Plan fp8_plan(const moe_fp8_dims& m) {
@@ -431,7 +441,7 @@ Plan fp8_plan(const moe_fp8_dims& m) {
     p.part_bytes = 1024 * 16;
     return p;
   }
-  if (m.M <= 128) {
+  if (use_mid(m)) {
     p.form = kMid;
     p.tiles = ceil_div(m.N, mid_rows(m)) * mid_tiles_m(m);
     p.parts = split_parts(p.tiles, Kb, 8);
