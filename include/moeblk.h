@@ -49,7 +49,9 @@ extern "C" {
 #endif
 
 #define MOEBLK_ABI_VERSION 4 /* 2: moe_dims.bias_mode; 3: moe_route workspace;
-                                4: moe_forward_static, moe_forward_one_launch */
+                                4: moe_forward_static, moe_forward_one_launch.
+                                Entry points added since (FP8 weights, the
+                                router's balance) change none of these. */
 
 /* status codes */
 #define MOE_OK 0
@@ -408,7 +410,8 @@ int moe_topk(const moe_dims* dims, const float* logits, const float* bias, int32
  * Sizes (elements). Supported ranges: 1 <= M <= 262144; 1 <= N <= 32768;
  * 1 <= K <= 32768 (any of them odd); in_type, out_type in {MOE_BF16,
  * MOE_FP32}. Kb = ceil(K / 128) and Nb = ceil(N / 128) are the numbers of
- * blocks, Kp = 128 Kb. */
+ * blocks, Kp = 128 Kb. In this section and the next, outputs and workspaces must
+ * not overlap inputs or each other. */
 #define MOE_BF16 0
 #define MOE_FP32 1
 typedef struct moe_fp8_dims {
@@ -447,8 +450,12 @@ int moe_pack_fp8(const moe_fp8_dims* dims, const void* q, const float* scales, v
  *               (sum over the block's k of xq[t][k] * q[n][k])
  *   xq, xs   as moe_fp8_quant writes them; any fp32 scales are taken (rows
  *            quantised elsewhere included), columns K .. Kp - 1 must be finite;
- *   out      [M, N] out_type, written: fp32 accumulation in a fixed order
- *            (deterministic), one rounding; NaNs and infinite scales propagate;
+ *   out      [M, N] out_type, written: fp32 sums in a fixed order
+ *            (deterministic), one rounding; NaNs and infinite scales propagate.
+ *            A block's sum over k is an fp32 sum too, except for bf16 out at M >
+ *            16: there it comes from the e4m3 matrix instruction, whose adder
+ *            keeps about 16 bits (measured 1.5e-5 of the block's sum; out is
+ *            rounded to 2^-8);
  *   workspace device scratch of at least moe_fp8_gemm_workspace_bytes. It must
  *            be zero-filled once before its first use; every call leaves it
  *            ready for the next, with any dims of no larger workspace. Calls
@@ -485,16 +492,17 @@ int moe_pack_fp8_expert(const moe_dims* dims, int which, const void* q, const fl
  *   y[r] = bf16( Q(h) . W2[el]^T ),
  * and, if shared_I > 0, the same chain on every token t with the shared weights
  * into y[R_max + t]. Between x and y the values are rounded only where they are
- * quantised (moe_expert_ffn rounds gu and h to bf16).
+ * quantised (moe_expert_ffn rounds gu and h to bf16); the sums are fp32, in down
+ * with the e4m3 instruction's block sums (see moe_fp8_gemm).
  *   x, counts, offsets, rows, active, y: as for moe_expert_ffn (all four
  *              moe_bucket outputs are read here), so that moe_bucket feeds this
  *              call and moe_combine takes its y;
  *   w13_packed .. ws2_packed: moe_pack_fp8_expert outputs (ws*: NULL when
  *              shared_I == 0);
- *   workspace  device scratch of at least moe_fp8_ffn_workspace_bytes(dims),
- *              zero-filled once before its first use. A workspace used with
- *              other dims must be zero-filled again. Calls sharing it must not
- *              overlap. */
+ *   workspace  device scratch of at least moe_fp8_ffn_workspace_bytes(dims), no
+ *              initial contents needed. Calls sharing it must not overlap.
+ * Two launches at S <= 16 while S * max(d, I, shared_I) <= 576 * 128 (the rows are
+ * quantised by the launches that multiply them), else up to four. */
 size_t moe_fp8_ffn_workspace_bytes(const moe_dims* dims);
 int moe_fp8_expert_ffn(const moe_dims* dims, const void* x, const void* w13_packed,
                        const void* w2_packed, const int32_t* counts, const int32_t* offsets,

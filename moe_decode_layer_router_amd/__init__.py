@@ -499,8 +499,8 @@ def _buf(t, name: str, n: int, kinds, device: int):
     """The pointer of a tensor of ``n`` elements or more (None -> NULL) of one
     of the dtypes ``kinds`` (None: dims the library refuses) on GPU ``device``:
     the calls below launch on the current device."""
-    if t is None:
-        return None
+    if t is None or type(t) is int:  # a raw pointer passes through
+        return t
     if t.get_device() != device:
         raise ValueError(f"{name}: tensor is not on the current GPU device")
     if not t.is_contiguous():
@@ -530,7 +530,9 @@ def _workspace(ws, workspace_bytes, T: _Torch, device: int):
     """The workspace's pointer and bytes (``workspace_bytes`` may state fewer
     than the tensor has)."""
     ptr = _buf(ws, "workspace", workspace_bytes or 0, T.bytes, device)
-    return ptr, workspace_bytes if workspace_bytes is not None or ws is None else ws.numel()
+    if workspace_bytes is None:
+        workspace_bytes = 0 if ws is None else ws.numel()
+    return ptr, workspace_bytes
 
 
 def fp8_dims_from(cfg) -> MoeFp8Dims:

@@ -141,6 +141,22 @@ def test_product(M, N, K, kind_out):
     _check_product(M, N, K, "bf16", kind_out)
 
 
+# further kernels and K splits: 64-row register tiles, LDS tiles of 128 with one,
+# two and many K blocks, split and whole, tiles of 256, rows too many to quantise
+# in the product, 64 weight rows a workgroup at few rows
+FORMS = [
+    (16, 4096, 8192), (16, 8200, 640), (3, 300, 20000), (20, 8300, 384), (64, 8300, 640), (100, 5000, 700),
+    (1000, 4096, 100), (1000, 4096, 256), (700, 2000, 2100), (1500, 2100, 640), (3900, 4000, 300), (4096, 4096, 130),
+    (300, 300, 300), (640, 64, 4096),
+]
+
+
+@pytest.mark.parametrize("kind_out", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", FORMS)
+def test_product_forms(M, N, K, kind_out):
+    _check_product(M, N, K, "bf16", kind_out, seed=1)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 512, 512), (8, 1024, 4096), (100, 99, 333), (300, 256, 260)])
 def test_product_from_fp32_rows(M, N, K):
     _check_product(M, N, K, "fp32", "fp32", seed=3)
@@ -265,6 +281,10 @@ def _check_experts(cfg, seed, ids=None):
 SMALL = get_config("tiny")
 EXPERTS = {
     "tiny": SMALL,
+    "S16_many_blocks": SMALL.with_(S=16, d=4608, I=256),  # 576 (row, K block) pairs: still quantised in place
+    "S16_too_many_blocks": SMALL.with_(S=16, d=4736, I=256),
+    "S17": SMALL.with_(S=17, E=2, n_local=2, topk=2),  # two token tiles a bucket
+    "shared_wider_than_I": SMALL.with_(S=9, I=128, shared_I=1024),
     "S1": SMALL.with_(S=1),
     "S1_top8": SMALL.with_(S=1, topk=8),
     "one_expert_64_rows": SMALL.with_(S=64, E=1, n_local=1, topk=1),
@@ -342,10 +362,10 @@ def _proj_case(M=8, N=512, K=2048, seed=0):
     return dims, x, packed, torch.empty((M, N), dtype=torch.bfloat16, device="cuda"), ws
 
 
-@pytest.mark.parametrize("M", [1, 8, 100, 400])
-def test_graph_replays_match_eager(M):
+@pytest.mark.parametrize("M,N", [(1, 512), (8, 512), (100, 512), (400, 512), (700, 2000)])
+def test_graph_replays_match_eager(M, N):
     """Two captured graphs share a workspace and take turns with eager calls."""
-    dims, x, packed, out, ws = _proj_case(M=M)
+    dims, x, packed, out, ws = _proj_case(M=M, N=N)
     mb.moe_fp8_proj(dims, x, packed, out, ws)
     torch.cuda.synchronize()
     ref = out.clone()
@@ -385,6 +405,31 @@ def test_block_graph_replays_match_eager(name):
         blk.step()
         torch.cuda.synchronize()
         assert torch.equal(blk.out, ref), (i, "eager")
+
+
+def test_experts_two_streams_and_shared_weights():
+    """Two blocks on the same packed weights, buckets of their own, on two
+    streams at once."""
+    from moe_decode_layer_router_amd.block import Fp8Block
+
+    inp = make_fp8_inputs(EXPERTS["shared"], 8)
+    blocks = [Fp8Block(inp), Fp8Block(inp)]
+    blocks[1].x.copy_(-blocks[1].x)
+    blocks[1].packed = blocks[0].packed
+    refs = []
+    for b in blocks:
+        b.step()
+        refs.append(b.out.clone())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in blocks]
+    for _ in range(10):
+        for st, b in zip(streams, blocks):
+            with torch.cuda.stream(st):
+                b.expert_ffn()
+                b.combine()
+    torch.cuda.synchronize()
+    for b, ref in zip(blocks, refs):
+        assert torch.equal(b.out, ref)
 
 
 def test_two_streams_with_their_own_workspaces():
