@@ -11,6 +11,11 @@
 // their first weight loads are in flight, in steps of up to 16 rows whose (row, K
 // block) pairs fit (kFusedItems; an expert rarely has more than a few of the rows);
 // else by a launch of their own in front of it.
+//
+// Measured (gate_up + down, us): S = 8, 7.7 active experts of 4096 x 2048 23.8 + 14.4
+// (5.5, 4.5 TB/s); S = 128, 32 experts of 7168 x 2048 and a shared one 163 + 78 (6.0,
+// 6.2 TB/s). 4 waves instead of 8 let two or three workgroups share a CU, one's
+// first loads under another's last sums: S = 8 47 -> 40 us.
 #include <type_traits>
 
 #include "fp8_dev.h"
