@@ -4,8 +4,9 @@
 // gate_up + SwiGLU of every (expert, block of 64 packed rows = 32 intermediates),
 // h in fp32, then down of every (expert, 64 output rows). The weights' bytes bound
 // both. A workgroup's 4 waves take every fourth K block, a ring of blocks' loads in
-// flight each, straight from the packed order into registers (exact form,
-// fp8_dev.h); the waves' sums are added through LDS in wave order.
+// flight each, straight from the packed order into registers (gate_up in the exact
+// form, down in the fast one, fp8_dev.h); the waves' sums are added through LDS in
+// wave order.
 //
 // The rows of either launch are quantised by its own workgroups, into LDS, while
 // their first weight loads are in flight, in steps of up to 16 rows whose (row, K
