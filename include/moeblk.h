@@ -564,7 +564,9 @@ int moe_balance_loss(const moe_balance_dims* dims, const float* logits, const in
 /* Its gradient with respect to the logits, the counts held constant: with
  * a[e] = dloss coef / n_seq * E / (topk T_b^2) * counts[b][e],
  *   dlogits[t][j] = p_j (1 - sigmoid(l_j)) (a_j - sum_e a_e p_e)   (sigmoid)
- *   dlogits[t][j] = p_j (a_j - sum_e a_e p_e)                      (softmax).
+ *   dlogits[t][j] = p_j (a_j - sum_e a_e p_e)                      (softmax),
+ * evaluated with the counts taken against their mean (the same value, since a
+ * row's p add up to 1): evenly loaded experts give a gradient of exactly zero.
  *   counts  moe_balance_loss's (or moe_expert_counts');
  *   dloss   [1] fp32, the gradient of the loss, or NULL for 1;
  *   dlogits [T, E] fp32, written for the rows of a sequence; other rows are

@@ -439,11 +439,15 @@ __global__ __launch_bounds__(256) void backward_kernel(const float* __restrict__
     const double len = q1 - q0;
     const float f =
         static_cast<float>(static_cast<double>(g) * coef / n_seq * E / (topk * len * len));
+    // The gradient does not change with a constant taken off every count (the p of a
+    // row add up to 1), so the counts are taken against the mean: near balance
+    // a_j - sum a p would otherwise be a small difference of large terms.
+    const int mean_count = static_cast<int>((2ll * topk * (q1 - q0) + E) / (2 * E));
     float a[4 * kNI];
 #pragma unroll
     for (int i = 0; i < 4 * kNI; ++i) {
       const int e = 64 * (i >> 2) + 4 * j + (i & 3);
-      a[i] = e < E ? f * static_cast<float>(counts[static_cast<size_t>(b) * E + e]) : 0.0f;
+      a[i] = e < E ? f * static_cast<float>(counts[static_cast<size_t>(b) * E + e] - mean_count) : 0.0f;
     }
     for (; row < s1; row += kPass) {
       const Row<kNI> l = next;

@@ -216,6 +216,35 @@ def test_one_workspace_serves_other_dims_and_graphs():
         assert all(torch.equal(out[k], ref[k]) for k in ref), (i, "eager")
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_even_load_has_no_gradient(score):
+    """Every expert picked equally often: a_j - sum a p is zero in exact
+    arithmetic, and has to be zero here, not the rounding of its terms."""
+    l, ids = _case(500, 8, 8, 10)  # top-8 of 8
+    got = _check(l, ids, [0, 200, 500], 2, score, coef=100.0)
+    assert not got[3].any()
+    l, _ = _case(512, 64, 2, 11)
+    ids = (np.arange(1024) % 64).reshape(512, 2).astype(np.int32)
+    assert not _check(l, ids, None, 1, score)[3].any()
+
+
+def test_near_even_load_keeps_its_digits():
+    """One pick more on one expert: the gradient is a difference of nearly equal
+    terms, still good to the bound of its own size: p f |c_j - mean| instead of p f
+    |c_j| (the counts against their mean, at most 1 apart here, r and u as above)."""
+    E, T = 64, 4096
+    l, _ = _case(T, E, 1, 12)
+    ids = (np.arange(T) % E).astype(np.int32)[:, None]
+    ids[0] = 1
+    got = _run(l, ids, None, 1, "softmax", coef=1.0)[3]
+    c, _, _, grad = rf.balance(l.astype(np.float64), ids, [0, T], 1, "softmax", 1.0)
+    w = np.abs(c[0] - T // E) * E / T**2
+    p, f = rf.balance_scores(l.astype(np.float64), "softmax")
+    r = (24 + 4 * float(np.abs(l).max())) * U
+    tol = (2 * r + 16 * U) * p * f * (w[None, :] + (p @ w)[:, None])
+    assert np.all(np.abs(got - grad) <= tol + 1e-12 * np.abs(grad) + 2.0**-50 * E / T**2)
+
+
 def test_large_offsets():
     """dlogits and logits past 2^31 bytes: the last rows of 2.4e6 x 256."""
     T, E, k = 2400000, 256, 1
