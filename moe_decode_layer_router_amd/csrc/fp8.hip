@@ -16,7 +16,7 @@ namespace {
 //
 // One pass over the rows, bound by memory: 16384 x 7168 bf16 in 63.5 us, 5.6 TB/s.
 
-template <typename T, bool kVec>
+template <typename T>
 __global__ __launch_bounds__(256) void quant_kernel(const T* __restrict__ x,
                                                     uint8_t* __restrict__ xq,
                                                     float* __restrict__ xs, int M, int K, int Kb) {
@@ -27,7 +27,7 @@ __global__ __launch_bounds__(256) void quant_kernel(const T* __restrict__ x,
   if (row >= static_cast<size_t>(M)) return;
   Raw16<T> v;
   float sc;
-  load16<T, kVec>(x + row * K, kb * kFp8Block + l8 * 16, K, v);
+  load16<T>(x + row * K, kb * kFp8Block + l8 * 16, K, v);
   const u32x4_t q = quant16(v, sc);
   *reinterpret_cast<u32x4_t*>(xq + row * (static_cast<size_t>(Kb) * kFp8Block) + kb * kFp8Block +
                               l8 * 16) = q;
@@ -144,15 +144,11 @@ __global__ __launch_bounds__(64 * kNW) void rows_kernel(RowsArgs a) {
     // row permuted by chunk ^ (row % 8)
     using T = typename std::conditional<kSrc == kRowsBf16, uint16_t, float>::type;
     const T* x = static_cast<const T*>(a.x);
-    const bool vec = a.K % (16 / sizeof(T)) == 0;
     const int l8 = threadIdx.x & 7;
     for (int item = threadIdx.x >> 3; item < M * (kb1 - kb0); item += 8 * kNW) {
       const int row = item % M, kb = kb0 + item / M;
       Raw16<T> v;
-      if (vec)
-        load16<T, true>(x + static_cast<size_t>(row) * a.K, kb * kFp8Block + l8 * 16, a.K, v);
-      else
-        load16<T, false>(x + static_cast<size_t>(row) * a.K, kb * kFp8Block + l8 * 16, a.K, v);
+      load16<T>(x + static_cast<size_t>(row) * a.K, kb * kFp8Block + l8 * 16, a.K, v);
       float sc;
       const u32x4_t q = quant16(v, sc);
       *reinterpret_cast<u32x4_t*>(xl + item * kFp8Block + ((l8 ^ (row & 7)) * 16)) = q;
@@ -363,19 +359,10 @@ void launch_fp8_quant(const void* x, int in_type, uint8_t* xq, float* xs, int M,
                       hipStream_t stream) {
   const int Kb = fp8_kb(K);
   const dim3 grid(static_cast<unsigned>((static_cast<size_t>(M) * Kb * 8 + 255) / 256));
-  if (in_type == MOE_BF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(x);
-    if (K % 8 == 0)
-      quant_kernel<uint16_t, true><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb);
-    else
-      quant_kernel<uint16_t, false><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb);
-  } else {
-    const float* p = static_cast<const float*>(x);
-    if (K % 4 == 0)
-      quant_kernel<float, true><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb);
-    else
-      quant_kernel<float, false><<<grid, 256, 0, stream>>>(p, xq, xs, M, K, Kb);
-  }
+  if (in_type == MOE_BF16)
+    quant_kernel<uint16_t><<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(x), xq, xs, M, K, Kb);
+  else
+    quant_kernel<float><<<grid, 256, 0, stream>>>(static_cast<const float*>(x), xq, xs, M, K, Kb);
 }
 
 void launch_fp8_pack(const void* q, const void* scales, void* packed, int n, int N, int K,

@@ -143,7 +143,7 @@ __device__ __forceinline__ void ffn_block(const FfnArgs& a, bool shared, int el,
         for (int item = threadIdx.x >> 3; item < n * Kb; item += kWaves * 8) {
           const int r = item % n, kb = item / n;
           Raw16<T> v;
-          load16<T, true>(static_cast<const T*>(set.x) + static_cast<size_t>(row_of(r)) * K,
+          load16<T>(static_cast<const T*>(set.x) + static_cast<size_t>(row_of(r)) * K,
                           kb * kFp8Block + l8 * 16, K, v);
           float scale;
           const u32x4_t q = quant16(v, scale);
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(256) void quant_h_kernel(FfnArgs a, const int32_t* 
   const int row = item / Kb, kb = item - row * Kb;
   if (row >= (shared ? a.S : min(*used, a.r_max))) return;
   Raw16<float> v;
-  load16<float, true>(static_cast<const float*>(set.x) + static_cast<size_t>(row) * K,
+  load16<float>(static_cast<const float*>(set.x) + static_cast<size_t>(row) * K,
                       kb * kFp8Block + l8 * 16, K, v);
   float scale;
   const u32x4_t q = quant16(v, scale);

@@ -19,12 +19,16 @@ struct Raw16 {  // 16 columns of a row as loaded
   uint32_t w[4 * sizeof(T)];
 };
 
-template <typename T, bool kVec>
+// 16 bytes at an element's alignment: rows of any length start anywhere, and global
+// loads of any width take any alignment
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+
+template <typename T>
 __device__ __forceinline__ void load16(const T* row, int c0, int K, Raw16<T>& v) {
-  if (kVec && c0 + 16 <= K) {
+  if (c0 + 16 <= K) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)); ++i) {
-      const u32x4_t q = *reinterpret_cast<const u32x4_t*>(row + c0 + 16 / sizeof(T) * i);
+      const u32x4_t q = *reinterpret_cast<const u32x4_any_t*>(row + c0 + 16 / sizeof(T) * i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v.w[4 * i + j] = q[j];
     }
