@@ -110,22 +110,26 @@ struct Row {
   float v[4 * kNI];
 };
 
+// 16-byte loads and stores at any element (rows of any length)
+typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
+
 template <int kNI>
-__device__ __forceinline__ void load_row(const float* logits, size_t row, int E, bool vec, int j,
+__device__ __forceinline__ void load_row(const float* logits, size_t row, int E, int j,
                                          Row<kNI>& l) {
   const float* p = logits + row * E;
 #pragma unroll
   for (int i = 0; i < kNI; ++i) {
     const int e = 64 * i + 4 * j;
-    if (vec) {  // E % 4 == 0: whole groups of four, 16-byte aligned
-      f32x4_t q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (e < E) q = *reinterpret_cast<const f32x4_t*>(p + e);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) l.v[4 * i + c] = q[c];
+    f32x4_t q = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (e + 4 <= E) {
+      q = *reinterpret_cast<const f32x4_any_t*>(p + e);
     } else {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) l.v[4 * i + c] = e + c < E ? p[e + c] : -INFINITY;
+      for (int c = 0; c < 3; ++c)
+        if (e + c < E) q[c] = p[e + c];
     }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) l.v[4 * i + c] = q[c];
   }
 }
 
@@ -280,12 +284,11 @@ __global__ __launch_bounds__(256) void chunk_kernel(ForwardArgs a) {
   __shared__ float sums[kPass][kMaxE];
   const int tid = threadIdx.x, j = tid & 15, group = tid >> 4;
   const int c = blockIdx.x, rows = forward_rows(a.T), E = a.E;
-  const bool vec = E % 4 == 0;
   const int lo = c * rows, hi = min(a.T, lo + rows);
   // the chunk's first rows and its picks are on their way before the sequences are known
   Row<kNI> next;
   int have = lo + group;
-  if (a.logits && have < hi) load_row<kNI>(a.logits, have, E, vec, j, next);
+  if (a.logits && have < hi) load_row<kNI>(a.logits, have, E, j, next);
   int id[8];  // picks tid, tid + 256, ... of the chunk's at most 2048
   const int picks = (hi - lo) * a.topk;
 #pragma unroll
@@ -308,10 +311,10 @@ __global__ __launch_bounds__(256) void chunk_kernel(ForwardArgs a) {
     if (a.logits) {
       float acc[4 * kNI] = {};
       int row = lo + (s0 - lo) / kPass * kPass + group;
-      if (row != have && row < s1) load_row<kNI>(a.logits, row, E, vec, j, next);
+      if (row != have && row < s1) load_row<kNI>(a.logits, row, E, j, next);
       for (; row < s1; row += kPass) {
         const Row<kNI> l = next;
-        if (row + kPass < s1) load_row<kNI>(a.logits, row + kPass, E, vec, j, next);
+        if (row + kPass < s1) load_row<kNI>(a.logits, row + kPass, E, j, next);
         Row<kNI> p, unused;
         row_scores<kNI, false>(l, a.score, p, unused);
         if (row >= s0) {
@@ -422,10 +425,9 @@ __global__ __launch_bounds__(256) void backward_kernel(const float* __restrict__
   const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
   const int rows = backward_rows(T);
   const int lo = blockIdx.x * rows, hi = min(T, lo + rows);
-  const bool vec = E % 4 == 0;
   Row<kNI> next;
   int have = lo + group;
-  if (have < hi) load_row<kNI>(logits, have, E, vec, j, next);
+  if (have < hi) load_row<kNI>(logits, have, E, j, next);
   const float g = dloss ? *dloss : 1.0f;
   const Starts seq(starts, n_seq, T);
   for (int b = seq.find(lo); b < n_seq; ++b) {
@@ -434,7 +436,7 @@ __global__ __launch_bounds__(256) void backward_kernel(const float* __restrict__
     if (s0 >= hi) break;
     if (s1 <= s0) continue;
     int row = lo + (s0 - lo) / kPass * kPass + group;
-    if (row != have && row < s1) load_row<kNI>(logits, row, E, vec, j, next);
+    if (row != have && row < s1) load_row<kNI>(logits, row, E, j, next);
     have = -1;
     const double len = q1 - q0;
     const float f =
@@ -451,7 +453,7 @@ __global__ __launch_bounds__(256) void backward_kernel(const float* __restrict__
     }
     for (; row < s1; row += kPass) {
       const Row<kNI> l = next;
-      if (row + kPass < s1) load_row<kNI>(logits, row + kPass, E, vec, j, next);
+      if (row + kPass < s1) load_row<kNI>(logits, row + kPass, E, j, next);
       Row<kNI> p, slope;
       row_scores<kNI, true>(l, score, p, slope);
       float mean = 0.0f;
@@ -466,11 +468,11 @@ __global__ __launch_bounds__(256) void backward_kernel(const float* __restrict__
         f32x4_t v;
 #pragma unroll
         for (int c = 0; c < 4; ++c) v[c] = slope.v[4 * i + c] * (a[4 * i + c] - mean);
-        if (vec) {
-          if (e < E) *reinterpret_cast<f32x4_t*>(out + e) = v;
+        if (e + 4 <= E) {
+          *reinterpret_cast<f32x4_any_t*>(out + e) = v;
         } else {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 3; ++c)
             if (e + c < E) out[e + c] = v[c];
         }
       }

@@ -200,7 +200,7 @@ __global__ __launch_bounds__(64 * kNW) void rows_kernel(RowsArgs a) {
   if (!join_parts(a.split, rb, part, wave < kRT, sum, &last)) return;
   if (wave < kRT && m16 < M) {
     const int n0 = (rb * kRT + wave) * 16 + 4 * g;
-    store4<true>(a.out, static_cast<size_t>(m16) * a.N + n0, a.N - n0, a.N % 4 == 0, sum[0],
+    store4<true>(a.out, static_cast<size_t>(m16) * a.N + n0, a.N - n0, sum[0],
                  a.out_bf16);
   }
 }
@@ -341,7 +341,7 @@ __device__ __forceinline__ void mid_body(const MidArgs& a, f32x4_t* red, int* la
     const int i = e * 8 + wave, token = t0 + (i % kTT) * 16 + m16;
     const int n0 = (rb * kRT + i / kTT) * 16 + 4 * g;
     if (token < M && i < kRT * kTT)
-      store4<kExact>(a.out, static_cast<size_t>(token) * a.N + n0, a.N - n0, a.N % 4 == 0, sum[e],
+      store4<kExact>(a.out, static_cast<size_t>(token) * a.N + n0, a.N - n0, sum[e],
                      a.out_bf16);
   }
 }

@@ -93,30 +93,30 @@ __device__ __forceinline__ float fp8_block_scale(float amax) {
   return __uint_as_float((u >> 23) >= 255u ? 0x7fc00000u : static_cast<uint32_t>(f) << 23);
 }
 
-// four outputs of a row at element `at`, `left` of them inside the row; quad: rows
-// start at multiples of 4; kFp32: fp32 outputs are possible
+// four outputs of a row at element `at`, `left` of them inside the row; kFp32: fp32
+// outputs are possible. Stores of four take any alignment (rows of any length).
 template <bool kFp32>
-__device__ __forceinline__ void store4(void* out, size_t at, int left, bool quad, f32x4_t v,
-                                       bool bf16) {
+__device__ __forceinline__ void store4(void* out, size_t at, int left, f32x4_t v, bool bf16) {
+  typedef u32x2_t u32x2_any_t __attribute__((aligned(2)));
+  typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
   if (left <= 0) return;
   if (!kFp32 || bf16) {
     uint16_t* o = static_cast<uint16_t*>(out) + at;
     const u32x2_t p = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-    if (quad) {
-      *reinterpret_cast<u32x2_t*>(o) = p;
+    if (left >= 4) {
+      *reinterpret_cast<u32x2_any_t*>(o) = p;
     } else {
       o[0] = static_cast<uint16_t>(p[0]);
       if (left > 1) o[1] = static_cast<uint16_t>(p[0] >> 16);
       if (left > 2) o[2] = static_cast<uint16_t>(p[1]);
-      if (left > 3) o[3] = static_cast<uint16_t>(p[1] >> 16);
     }
   } else {
     float* o = static_cast<float*>(out) + at;
-    if (quad) {
-      *reinterpret_cast<f32x4_t*>(o) = v;
+    if (left >= 4) {
+      *reinterpret_cast<f32x4_any_t*>(o) = v;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 3; ++i)
         if (i < left) o[i] = v[i];
     }
   }

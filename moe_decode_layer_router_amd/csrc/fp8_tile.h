@@ -252,7 +252,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
 #pragma unroll
     for (int r = 0; r < kRT; ++r) {
       const int n0 = tn * BN + (wn * kRT + r) * 16 + 4 * g;
-      if (token < M) store4<kExact>(a.out, orow + n0, a.N - n0, a.N % 4 == 0, acc[r][t], a.out_bf16);
+      if (token < M) store4<kExact>(a.out, orow + n0, a.N - n0, acc[r][t], a.out_bf16);
       __builtin_amdgcn_sched_barrier(0);  // one tile's addresses at a time
     }
   }
