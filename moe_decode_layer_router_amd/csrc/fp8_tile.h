@@ -27,8 +27,6 @@
 // one chunk fall on different banks.
 #pragma once
 
-#include <type_traits>
-
 #include "fp8_dev.h"
 
 namespace moeblk {
@@ -99,16 +97,17 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
   const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(a.w) + static_cast<size_t>(rt0) * Kb * kFp8TileBytes, 0,
       static_cast<int>(n_rt * Kb * kFp8TileBytes), 0x00020000);
-  // copy i < kLoads of step kb into weight buffer wb, token buffer xb
-  const auto copy = [&](int i, int kb, int wb, int xb) {
+  // copy i < kLoads of step kb into weight buffer wb, token buffer xb (all offsets are
+  // below 2^31)
+  const auto copy = [&](int i, int kb, int wb, int xb, uint32_t past = 0) {
     if (i < kXLoads) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          xr, (fp8_lptr_t)(lds + 3 * kWBuf + xb * kXBuf + (uwave + i * kWaves) * 1024), 16, xoff[i],
-          kb * kFp8Block, 0, 0);
+          xr, (fp8_lptr_t)(lds + 3 * kWBuf + xb * kXBuf + (uwave + i * kWaves) * 1024), 16,
+          xoff[i] | past, kb * kFp8Block, 0, 0);
     } else {
       const int p = uwave + (i - kXLoads) * kWaves;  // piece: row tile p / 2, half p % 2
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          wr, (fp8_lptr_t)(lds + wb * kWBuf + p * 1024), 16, lane * 16,
+          wr, (fp8_lptr_t)(lds + wb * kWBuf + p * 1024), 16, (lane * 16) | past,
           (min(p >> 1, n_rt - 1) * Kb + kb) * kFp8TileBytes + (p & 1) * 1024, 0, 0);
     }
   };
@@ -170,14 +169,19 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
 #pragma unroll
   for (int t = 0; t < kTT; ++t) b[t] = read_x(0, t);
 
-  // one step; kCopy: there is a step kb + 2, kMore: there is a step kb + 1
-  const auto step = [&](int kb, int wb, int wb1, int wb2, auto copy_c, auto more_c) {
-    constexpr bool kCopy = decltype(copy_c)::value, kMore = decltype(more_c)::value;
+  // The steps, one piece of code without branches (several copies of it, or a branch
+  // in it, spill the accumulators): the last steps copy, wait and read as if more
+  // followed. Their copies get an offset past the buffer's range, which reads
+  // nothing; what they leave in LDS is not used.
+  int wb = 0;
+  for (int kb = kb0; kb < kb1; ++kb) {
     const int xb = (kb - kb0) & 1;
+    const int wb1 = wb == 2 ? 0 : wb + 1, wb2 = wb1 == 2 ? 0 : wb1 + 1;
+    const uint32_t past = kb + 2 < kb1 ? 0u : 1u << 31;
     float s_now[kTT];
 #pragma unroll
     for (int t = 0; t < kTT; ++t) s_now[t] = s_next[t];
-    if constexpr (kMore) load_scales(kb + 1);
+    load_scales(min(kb + 1, kb1 - 1));
     Bf16Frag be[kExact ? kTT : 1];
     if constexpr (kExact) {
 #pragma unroll
@@ -187,8 +191,7 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
     for (int r = 0; r < kRT; ++r) {
       Bf16Frag we;
       if constexpr (kExact) we = e4m3_to_bf16(w[r & 1]);
-      if constexpr (kMore)
-        if (r == kRT - 2) wait_all();
+      if (r == kRT - 2) wait_all();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int t = 0; t < kTT; ++t) {
@@ -201,38 +204,25 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
         else
           d[t] = mfma_fp8_block(w[r & 1], b[t]);
         if (t == 0 && r + 1 < kRT) w[(r + 1) & 1] = read_w(wb, r + 1);
-        if constexpr (kMore) {
-          if (r == kRT - 1) {  // the next step's first operands
-            if (t == 0) w[0] = read_w(wb1, 0);
-            b[t] = read_x(xb ^ 1, t);
-          }
+        if (r == kRT - 1) {  // the next step's first operands
+          if (t == 0) w[0] = read_w(wb1, 0);
+          b[t] = read_x(xb ^ 1, t);
         }
-        if constexpr (kCopy) {
+        {
           constexpr int kUnits = 2 * kTT;  // the last two row tiles
           const int u = (r - (kRT - 2)) * kTT + t;
           if (u >= 0) {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-              if (i * kUnits / kLoads == u) copy(i, kb + 2, wb2, xb);
+              if (i * kUnits / kLoads == u) copy(i, min(kb + 2, kb1 - 1), wb2, xb, past);
           }
         }
         __builtin_amdgcn_sched_barrier(0);  // units stay in order
       }
     }
-  };
-  int kb = kb0, wb = 0;
-  for (; kb + 2 < kb1; ++kb) {
-    const int wb1 = wb == 2 ? 0 : wb + 1, wb2 = wb1 == 2 ? 0 : wb1 + 1;
-    step(kb, wb, wb1, wb2, std::true_type{}, std::true_type{});
     wb = wb1;
   }
-  if (kb + 1 < kb1) {
-    const int wb1 = wb == 2 ? 0 : wb + 1;
-    step(kb, wb, wb1, 0, std::false_type{}, std::true_type{});
-    wb = wb1;
-    ++kb;
-  }
-  step(kb, wb, 0, 0, std::false_type{}, std::false_type{});
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // no copy may still be on its way into LDS
 #pragma unroll
   for (int t = 0; t < kTT; ++t)
 #pragma unroll
