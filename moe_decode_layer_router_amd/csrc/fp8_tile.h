@@ -234,6 +234,40 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
     if (!join_parts(a.split, tm * a.tiles_n + tn, part, true, v, reinterpret_cast<int*>(lds)))
       return;
   }
+  if constexpr (kRT == 8 && !kExact) {
+    // bf16 through LDS (each wave its own part, rows padded by 16 bytes), so that a
+    // token's 128 outputs leave as whole lines, 16 bytes a lane
+    typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+    constexpr int kPitch = kRT * 32 + 16;
+    static_assert(kWaves * 16 * kTT * kPitch <= 3 * kWBuf + 2 * kXBuf, "LDS");
+    __syncthreads();  // every wave's operand reads are done
+    uint8_t* o = lds + wave * (16 * kTT * kPitch);
+#pragma unroll
+    for (int t = 0; t < kTT; ++t)
+#pragma unroll
+      for (int r = 0; r < kRT; ++r) {
+        const f32x4_t v = acc[r][t];
+        *reinterpret_cast<u32x2_t*>(o + (t * 16 + m16) * kPitch + r * 32 + 8 * g) =
+            u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      }
+    __syncthreads();
+    const int n0 = tn * BN + wn * 128 + 8 * m16, left = a.N - n0;
+#pragma unroll 4
+    for (int i = 0; i < 4 * kTT; ++i) {
+      const int row = 4 * i + g, token = tm * BM + wm * 16 * kTT + row;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(o + row * kPitch + 16 * m16);
+      if (token >= M) continue;
+      uint16_t* to = static_cast<uint16_t*>(a.out) + static_cast<size_t>(token) * a.N + n0;
+      if (left >= 8) {
+        *reinterpret_cast<u32x4_any_t*>(to) = v;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 7; ++c)
+          if (c < left) to[c] = static_cast<uint16_t>(v[c >> 1] >> (16 * (c & 1)));
+      }
+    }
+    return;
+  }
   // lane: token m16 of a token tile, outputs 4 g .. + 3 of a row tile
 #pragma unroll
   for (int t = 0; t < kTT; ++t) {
