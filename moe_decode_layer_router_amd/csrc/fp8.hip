@@ -439,15 +439,15 @@ Plan fp8_plan(const moe_fp8_dims& m) {
     p.part_bytes = 2 * 512 * 16;
     return p;
   }
-  // A step of one 256 x 256 tile a CU takes about 2.1 us, of two 128 x 128
+  // A step of one 256 x 256 tile a CU takes about 1.9 us, of two 128 x 128
   // tiles 1.25 us; rounds over the 256 CUs times that decide. Measured (us,
-  // K = 7168, N = 4096, 256 against 128 tiles): M = 8192 240 / 259, M = 4096
-  // 122 / 135, M = 2048 107 / 69.5.
+  // K = 7168, N = 4096, 256 against 128 tiles): M = 8192 210 / 259, M = 4096
+  // 109 / 135, M = 2048 104 / 69.5.
   const auto rounds = [&](int tile, int slots) {
     const size_t t = static_cast<size_t>(ceil_div(m.N, tile)) * ceil_div(m.M, tile);
     return (t + slots - 1) / slots;
   };
-  if (m.out_type == MOE_BF16 && rounds(256, 256) * 210 <= rounds(128, 512) * 125) {
+  if (m.out_type == MOE_BF16 && rounds(256, 256) * 190 <= rounds(128, 512) * 125) {
     p.form = kTile256;
     p.tiles = ceil_div(m.N, 256) * ceil_div(m.M, 256);
     p.parts = 1;

@@ -234,9 +234,9 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
     if (!join_parts(a.split, tm * a.tiles_n + tn, part, true, v, reinterpret_cast<int*>(lds)))
       return;
   }
-  if constexpr (kRT == 8 && !kExact) {
+  if constexpr (!kExact) {
     // bf16 through LDS (each wave its own part, rows padded by 16 bytes), so that a
-    // token's 128 outputs leave as whole lines, 16 bytes a lane
+    // token's 16 kRT outputs leave as whole lines, 16 bytes a lane
     typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
     constexpr int kPitch = kRT * 32 + 16;
     static_assert(kWaves * 16 * kTT * kPitch <= 3 * kWBuf + 2 * kXBuf, "LDS");
@@ -251,11 +251,13 @@ __device__ __forceinline__ void fp8_tile(const Fp8TileArgs& a, uint8_t* lds) {
             u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
       }
     __syncthreads();
-    const int n0 = tn * BN + wn * 128 + 8 * m16, left = a.N - n0;
+    constexpr int kLanes = 2 * kRT;  // a token
+    const int c16 = lane % kLanes;
+    const int n0 = tn * BN + wn * 16 * kRT + 8 * c16, left = a.N - n0;
 #pragma unroll 4
-    for (int i = 0; i < 4 * kTT; ++i) {
-      const int row = 4 * i + g, token = tm * BM + wm * 16 * kTT + row;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(o + row * kPitch + 16 * m16);
+    for (int i = 0; i < kTT * kRT / 2; ++i) {
+      const int row = i * (64 / kLanes) + lane / kLanes, token = tm * BM + wm * 16 * kTT + row;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(o + row * kPitch + 16 * c16);
       if (token >= M) continue;
       uint16_t* to = static_cast<uint16_t*>(a.out) + static_cast<size_t>(token) * a.N + n0;
       if (left >= 8) {
