@@ -20,8 +20,8 @@
 // slots (up to 16: T <= 240 in one sequence) the last workgroup of the first launch
 // does that instead, which saves a launch of about 3 us.
 //
-// T = 65536, E = 256: forward 22 us (3.0 TB/s) and 10 for the second launch, gradient
-// 31 us (4.3 TB/s); T = 128: 7.5 and 6.6 us.
+// T = 65536, E = 256: forward 19.4 us (3.6 TB/s) and 10 for the second launch, gradient
+// 27.8 us (4.9 TB/s); T = 128: 7.2 and 6.5 us.
 #include <math.h>
 
 #include "common.h"
