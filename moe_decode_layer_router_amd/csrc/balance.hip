@@ -173,7 +173,7 @@ __device__ __forceinline__ void row_scores(const Row<kNI>& l, int score, Row<kNI
 #pragma unroll
   for (int i = 0; i < n; ++i) s += p.v[i];
   s = row_sum(s);
-  const float inv = none ? 0.0f : 1.0f / s;
+  const float inv = s == 0.0f ? 0.0f : 1.0f / s;  // zero only where all are -inf; NaN stays
 #pragma unroll
   for (int i = 0; i < n; ++i) {
     p.v[i] *= inv;

@@ -159,6 +159,21 @@ def test_nan_stays_in_its_sequence():
     assert bad[100] and bad.sum() == 1
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_nan_among_masked_experts(score):
+    """One NaN in a row whose other logits are all -inf: the row's p and gradient
+    are NaN, the loss with them; other rows are as without it."""
+    l, ids = _case(200, 96, 2, 7)
+    l[150] = -np.inf
+    want = _check(l, ids, [0, 100, 200], 2, score)
+    l[150, 5] = np.nan
+    c, p, L, d = _run(l, ids, [0, 100, 200], 2, score)
+    assert np.array_equal(c, want[0]) and np.array_equal(p[0], want[1][0])
+    assert np.isnan(p[1]).all() and np.isnan(L) and np.isnan(d[150]).all()
+    rest = np.arange(200) != 150
+    assert np.array_equal(d[rest], want[3][rest])
+
+
 def test_gradient_against_differences_of_the_loss():
     """Directional central differences of the GPU's own fp32 loss: the error is
     the loss's rounding (2^-24 L, twice, over 2 h) and h^2 |d3L| / 6; the third
