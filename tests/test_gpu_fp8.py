@@ -212,6 +212,49 @@ def _product_nan(dims, x, q, s):
     return out.double().cpu().numpy(), "fp32"
 
 
+def test_quant_offsets_past_32_bits():
+    """Rows behind 2^32 elements: the same bits as a call on those rows alone."""
+    M, K, n = 135000, 32768, 40
+    r = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    x[-n:] = torch.randn((n, K), generator=r, device="cuda").to(torch.bfloat16)
+    xq = torch.empty((M, K), dtype=torch.uint8, device="cuda")
+    xs = torch.empty((K // 128, M), dtype=torch.float32, device="cuda")
+    mb.moe_fp8_quant(dict(M=M, K=K), x, xq, xs)
+    q1 = torch.empty((n, K), dtype=torch.uint8, device="cuda")
+    s1 = torch.empty((K // 128, n), dtype=torch.float32, device="cuda")
+    mb.moe_fp8_quant(dict(M=n, K=K), x[-n:].clone(), q1, s1)
+    assert torch.equal(xq[-n:], q1) and torch.equal(xs[:, -n:], s1)
+    assert not bool(xq[:-n].any())
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+def test_product_offsets_past_32_bits(out):
+    """Outputs behind 2^32 elements. One K block: every kernel form sums it alike
+    for one output type from 17 rows on, so the bits are those of a call on
+    the last rows alone."""
+    M, N, K, n = 262144, 16500, 100, 77
+    r = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn((M, K), generator=r, device="cuda").to(torch.bfloat16)
+    q = torch.randn((N, K), generator=r, device="cuda").to(torch.float8_e4m3fn)
+    sc = torch.rand((-(-N // 128), 1), generator=r, device="cuda") + 0.5
+    kind = mb.MOE_BF16 if out == torch.bfloat16 else mb.MOE_FP32
+    big = dict(M=M, N=N, K=K, out_type=kind)
+    w = torch.empty(mb.moe_packed_fp8_bytes(big), dtype=torch.uint8, device="cuda")
+    mb.moe_pack_fp8(big, q, sc, w)
+
+    def run(dims, rows):
+        ws = torch.zeros(mb.moe_fp8_proj_workspace_bytes(dims), dtype=torch.uint8, device="cuda")
+        o = torch.empty((dims["M"], N), dtype=out, device="cuda")
+        mb.moe_fp8_proj(dims, rows, w, o, ws)
+        return o
+
+    got = run(big, x)
+    want = run(dict(big, M=n), x[-n:].clone())
+    assert bool(want.abs().max() > 1)
+    assert torch.equal(got[-n:], want)
+
+
 def test_one_workspace_serves_other_dims():
     """The gemm workspace is left ready for any dims it is large enough for."""
     sizes = [(8, 1024, 4096), (1, 512, 8192), (100, 256, 2048), (8, 64, 16384), (400, 512, 640)]
