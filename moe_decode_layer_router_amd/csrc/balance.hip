@@ -20,7 +20,7 @@
 // slots (up to 16: T <= 240 in one sequence) the last workgroup of the first launch
 // does that instead, which saves a launch of about 3 us.
 //
-// T = 65536, E = 256: forward 19.4 us (3.6 TB/s) and 10 for the second launch, gradient
+// T = 65536, E = 256: forward 19.2 us (3.6 TB/s) and 7 for the second launch, gradient
 // 27.8 us (4.9 TB/s); T = 128: 7.2 and 6.5 us.
 #include <math.h>
 
@@ -227,13 +227,17 @@ __device__ __forceinline__ bool last_workgroup(int32_t* done) {
   return last;
 }
 
-// The sums of (b, 16 experts) over the sequence's slots by 256 threads: expert
-// tid % 16, slots tid / 16, + 16, ... Returns the 16 experts' loss term in
-// thread 0.
+// The sums of (b, kJ experts) over the sequence's slots by kReduce threads: expert
+// tid % kJ, every kReduce / kJ-th slot (1024 threads against 256: one sequence of 65536
+// rows, 1024 slots, 75 -> 60 us with the gradient). Returns the kJ experts' loss term in thread 0.
+constexpr int kReduce = 1024;
+
+template <int kJ>
 __device__ __forceinline__ double reduce_group(const ForwardArgs& a, int b, int e0) {
-  __shared__ int cnt[16][17];
-  __shared__ double sums[16][17];
-  const int j = threadIdx.x & 15, k = threadIdx.x >> 4;
+  constexpr int kWaves = kReduce / kWave;
+  __shared__ int cnt[kWaves][kJ + 1];
+  __shared__ double sums[kWaves][kJ + 1];
+  const int j = threadIdx.x % kJ, k = threadIdx.x / kJ, wave = threadIdx.x / kWave;
   const int e = e0 + j;
   const int rows = forward_rows(a.T);
   const int s0 = seq_start(a.starts, b, a.T), s1 = seq_start(a.starts, b + 1, a.T);
@@ -242,22 +246,30 @@ __device__ __forceinline__ double reduce_group(const ForwardArgs& a, int b, int 
   if (s1 > s0 && e < a.E) {
     const int last = (s1 - 1) / rows;
 #pragma unroll 8
-    for (int c = s0 / rows + k; c <= last; c += 16) {
+    for (int c = s0 / rows + k; c <= last; c += kReduce / kJ) {
       const size_t at = static_cast<size_t>(c + b) * a.E + e;
       n += a.slot_counts[at];
       if (a.loss) p += a.slot_probs[at];
     }
   }
-  __syncthreads();
-  cnt[k][j] = n;
-  sums[k][j] = p;
+  // the slots of a wave, then the waves
+#pragma unroll
+  for (int m = kJ; m < kWave; m <<= 1) {
+    n += __shfl_xor(n, m, kWave);
+    p += __shfl_xor(p, m, kWave);
+  }
+  __syncthreads();  // the sums in front have been read
+  if (threadIdx.x % kWave < kJ) {
+    cnt[wave][j] = n;
+    sums[wave][j] = p;
+  }
   __syncthreads();
   double term = 0.0;
-  if (k == 0) {
+  if (threadIdx.x < kJ) {
     n = 0;
     p = 0.0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kWaves; ++i) {
       n += cnt[i][j];
       p += sums[i][j];
     }
@@ -269,7 +281,7 @@ __device__ __forceinline__ double reduce_group(const ForwardArgs& a, int b, int 
       term = static_cast<double>(a.E) / (a.topk * len) * n * p;
     }
 #pragma unroll
-    for (int m = 8; m >= 1; m >>= 1) term += __shfl_xor(term, m, 16);
+    for (int m = kJ / 2; m >= 1; m >>= 1) term += __shfl_xor(term, m, kJ);
   }
   return term;
 }
@@ -395,21 +407,25 @@ __global__ __launch_bounds__(256) void chunk_kernel(ForwardArgs a) {
   }
 }
 
-// workgroup (b, 16 experts); the last one to finish adds the terms of the loss
-__global__ __launch_bounds__(256) void reduce_kernel(ForwardArgs a) {
-  __shared__ double part[4];
-  const int groups = (a.E + 15) / 16;
-  const int b = blockIdx.x / groups, e0 = (blockIdx.x % groups) * 16;
-  const double term = reduce_group(a, b, e0);
+// a workgroup: every gridDim.x-th (b, kJ experts); the last one to finish adds the terms of the loss
+template <int kJ>
+__global__ __launch_bounds__(kReduce) void reduce_kernel(ForwardArgs a) {
+  __shared__ double part[kReduce / kWave];
+  const int groups = (a.E + kJ - 1) / kJ, items = a.n_seq * groups;
+  for (int i = blockIdx.x; i < items; i += gridDim.x) {
+    const double term = reduce_group<kJ>(a, i / groups, i % groups * kJ);
+    if (a.loss && threadIdx.x == 0) store_through(&a.terms[i], term);
+  }
   if (!a.loss) return;
-  if (threadIdx.x == 0) store_through(&a.terms[blockIdx.x], term);
   if (!last_workgroup(a.done)) return;
   double sum = 0.0;
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) sum += load_through(&a.terms[i]);
+  for (int i = threadIdx.x; i < items; i += kReduce) sum += load_through(&a.terms[i]);
   sum = wave_sum_f64(sum);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) store_loss(a, (part[0] + part[1]) + (part[2] + part[3]));
+  if (threadIdx.x != 0) return;
+  for (int i = 1; i < kReduce / kWave; ++i) sum += part[i];  // thread 0 holds part[0]
+  store_loss(a, sum);
 }
 
 // ---------------------------------------------------------------- backward
@@ -491,10 +507,24 @@ int check_balance_dims(const moe_balance_dims* d) {
   return MOE_OK;
 }
 
+// Most workgroups of the second launch: their counting is one after another. 256 /
+// 512 / 2048 / one a group, with 16 experts: 256 sequences 95 / 87 / 96 / 116 us, 4000
+// sequences 509 / 364 / 361 / 847.
+constexpr int kReduceGroups = 512;
+
 inline int chunks(const moe_balance_dims& d) {
   return (d.T + forward_rows(d.T) - 1) / forward_rows(d.T);
 }
-inline int reduce_groups(const moe_balance_dims& d) { return d.n_seq * ((d.E + 15) / 16); }
+// 16 experts a workgroup of the second launch while that gives no more of them than
+// CUs, else 64 (a slot line read whole, a quarter of the groups). Measured, us a
+// forward and backward, 16 / 64: T = 65536, E = 256, 16 sequences 58.8 / 61.1, 32
+// 63.3 / 61.2, 256 86 / 75; T = 20000, 4000 sequences 365 / 164.
+inline int reduce_experts(const moe_balance_dims& d) {
+  return d.n_seq * ((d.E + 15) / 16) <= 256 ? 16 : 64;
+}
+inline int reduce_items(const moe_balance_dims& d) {
+  return d.n_seq * ((d.E + reduce_experts(d) - 1) / reduce_experts(d));
+}
 
 // workspace: the done counter (zero between calls), the loss terms, the slots
 struct BalanceLayout {
@@ -505,20 +535,25 @@ BalanceLayout balance_layout(const moe_balance_dims& d) {
   BalanceLayout l;
   const size_t slots = static_cast<size_t>(chunks(d) + d.n_seq) * d.E;
   l.terms = 256;
-  l.counts = l.terms + round_up(static_cast<size_t>(reduce_groups(d)) * 8, 256);
+  l.counts = l.terms + round_up(static_cast<size_t>(reduce_items(d)) * 8, 256);
   l.probs = l.counts + round_up(slots * 4, 256);
   l.total = l.probs + round_up(slots * 4, 256);
   return l;
 }
 
 template <int kNI>
-void launch_forward(const ForwardArgs& a, int n_chunks, int groups, hipStream_t stream) {
+void launch_forward(const ForwardArgs& a, const moe_balance_dims& m, hipStream_t stream) {
+  const int n_chunks = chunks(m);
   if (n_chunks + a.n_seq <= kOneSlots) {
     chunk_kernel<kNI, true><<<n_chunks, 256, 0, stream>>>(a);
     return;
   }
   chunk_kernel<kNI, false><<<n_chunks, 256, 0, stream>>>(a);
-  reduce_kernel<<<groups, 256, 0, stream>>>(a);
+  const int items = reduce_items(m), grid = items < kReduceGroups ? items : kReduceGroups;
+  if (reduce_experts(m) == 64)
+    reduce_kernel<64><<<grid, kReduce, 0, stream>>>(a);
+  else
+    reduce_kernel<16><<<grid, kReduce, 0, stream>>>(a);
 }
 
 int forward(const moe_balance_dims* dims, const float* logits, const int32_t* topk_ids,
@@ -540,11 +575,11 @@ int forward(const moe_balance_dims* dims, const float* logits, const int32_t* to
   a.terms = reinterpret_cast<double*>(ws + l.terms), a.done = reinterpret_cast<int32_t*>(ws);
   a.T = m.T, a.E = m.E, a.topk = m.topk, a.n_seq = m.n_seq, a.score = m.score, a.coef = m.coef;
   if (m.E <= 64)
-    launch_forward<1>(a, chunks(m), reduce_groups(m), stream);
+    launch_forward<1>(a, m, stream);
   else if (m.E <= 128)
-    launch_forward<2>(a, chunks(m), reduce_groups(m), stream);
+    launch_forward<2>(a, m, stream);
   else
-    launch_forward<4>(a, chunks(m), reduce_groups(m), stream);
+    launch_forward<4>(a, m, stream);
   return launch_status();
 }
 

@@ -114,6 +114,14 @@ def test_many_sequences():
     _check(l, ids, [0, *cuts, T], 1500, "sigmoid")
 
 
+@pytest.mark.parametrize("T,E,k,n_seq", [(20000, 64, 4, 1), (9000, 255, 8, 16), (9000, 250, 8, 17), (9000, 33, 2, 700)])
+def test_sums_of_many_slots(T, E, k, n_seq):
+    """Sequences of many slots, and more sequences than workgroups that sum them."""
+    l, ids = _case(T, E, k, 8)
+    cuts = np.sort(np.random.default_rng(n_seq).integers(0, T + 1, n_seq - 1)).tolist()
+    _check(l, ids, [0, *cuts, T], n_seq, "softmax")
+
+
 def test_starts_outside_the_rows_are_clamped():
     l, ids = _case(100, 16, 2, 3)
     a = _run(l, ids, [-5, 40, 500], 2, "softmax")
