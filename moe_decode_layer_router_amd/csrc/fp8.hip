@@ -210,8 +210,7 @@ __global__ __launch_bounds__(64 * kNW) void rows_kernel(RowsArgs a) {
 // 16 kRT weight rows x 16 kTT tokens a workgroup; its 8 waves take every eighth K
 // block of the workgroup's part, one or two blocks' loads in flight (kRing),
 // straight into registers (tokens through L2). The waves' sums are added through
-// LDS, all threads taking part. Bound by the bytes a CU loads (25-40 GB/s): 128 x
-// 7168 x 2048 in 10.5 us, 256 KB a CU.
+// LDS, all threads taking part. 128 x 7168 x 2048: 11.2 us.
 struct MidArgs {
   const uint8_t* xq;
   const float* xs;
@@ -341,8 +340,7 @@ __device__ __forceinline__ void mid_body(const MidArgs& a, f32x4_t* red, int* la
     const int i = e * 8 + wave, token = t0 + (i % kTT) * 16 + m16;
     const int n0 = (rb * kRT + i / kTT) * 16 + 4 * g;
     if (token < M && i < kRT * kTT)
-      store4<kExact>(a.out, static_cast<size_t>(token) * a.N + n0, a.N - n0, sum[e],
-                     a.out_bf16);
+      store4<kExact>(a.out, static_cast<size_t>(token) * a.N + n0, a.N - n0, sum[e], a.out_bf16);
   }
 }
 
@@ -420,6 +418,16 @@ inline int mid_rows(const moe_fp8_dims& m) {
 // 7168 51.7 / 42.9.
 inline bool use_mid(const moe_fp8_dims& m) {
   return m.M <= 64 || ceil_div(m.N, 64) * ceil_div(m.M, 64) <= 320;
+}
+
+// The exact form of the block sums (fp8_dev.h): always for fp32 outputs, at M <= 16, and
+// in the register kernel up to 128 rows (a decode step's), which loads bound. Measured, us
+// with the quantisation, fast / exact: M = 32, N = 4096, K = 7168 13.8 / 14.3; M = 64 17.2
+// / 18.2; M = 128, N = 7168, K = 2048 12.7 / 13.3. Beyond, the matrix rate counts: M = 160,
+// N = 4096, K = 7168 27.5 / 32.0; M = 300, K = 4096 30.1 / 35.7; in LDS tiles M = 1024, K =
+// 7168 58 / 71, M = 2048 76 / 116.
+inline bool exact_sums(const moe_fp8_dims& m) {
+  return m.out_type == MOE_FP32 || (m.M <= 128 && use_mid(m));
 }
 
 Plan fp8_plan(const moe_fp8_dims& m) {
@@ -504,17 +512,15 @@ void launch_rows(RowsArgs a, const Plan& p, hipStream_t stream) {
     rows_kernel<4, 8, kSrc, kFusedItems><<<grid, 512, 0, stream>>>(a);
 }
 
-void launch_mid(const MidArgs& a, int rows, unsigned grid, hipStream_t stream) {
+void launch_mid(const MidArgs& a, int rows, bool exact, unsigned grid, hipStream_t stream) {
   const auto launch = [&](auto kernel) { kernel<<<grid, 512, 0, stream>>>(a); };
   const bool small = rows == 32;
-  if (a.M <= 32 && a.out_bf16)
-    small ? launch(mid_kernel<2, 2, false, 2>) : launch(mid_kernel<4, 2, false, 2>);
-  else if (a.M <= 32)
+  if (a.M <= 32)
     small ? launch(mid_kernel<2, 2, true, 2>) : launch(mid_kernel<4, 2, true, 1>);
-  else if (a.out_bf16)
-    small ? launch(mid_kernel<2, 4, false, 2>) : launch(mid_kernel<4, 4, false, 1>);
-  else
+  else if (exact)
     small ? launch(mid_kernel<2, 4, true, 2>) : launch(mid_kernel<4, 4, true, 1>);
+  else
+    small ? launch(mid_kernel<2, 4, false, 2>) : launch(mid_kernel<4, 4, false, 1>);
 }
 
 void launch_fp8_gemm(const moe_fp8_dims& m, const void* xq, const float* xs, const void* packed,
@@ -531,7 +537,7 @@ void launch_fp8_gemm(const moe_fp8_dims& m, const void* xq, const float* xs, con
                         stream);
   } else if (p.form == kMid) {
     const MidArgs a = {q, xs, w, ws, out, m.M, m.N, Kb, bf, ceil_div(m.N, mid_rows(m)), p.tiles, split};
-    launch_mid(a, mid_rows(m), p.tiles * p.parts, stream);
+    launch_mid(a, mid_rows(m), exact_sums(m), p.tiles * p.parts, stream);
   } else {
     const Fp8TileArgs a = {q, xs, w, ws, out, m.M, m.N, Kb, bf, 0, 0, split};
     if (p.form == kTile256)

@@ -4,9 +4,8 @@
 // gate_up + SwiGLU of every (expert, block of 64 packed rows = 32 intermediates),
 // h in fp32, then down of every (expert, 64 output rows). The weights' bytes bound
 // both. A workgroup's 4 waves take every fourth K block, a ring of blocks' loads in
-// flight each, straight from the packed order into registers (gate_up in the exact
-// form, down in the fast one, fp8_dev.h); the waves' sums are added through LDS in
-// wave order.
+// flight each, straight from the packed order into registers (exact form, fp8_dev.h);
+// the waves' sums are added through LDS in wave order.
 //
 // The rows of either launch are quantised by its own workgroups, into LDS, while
 // their first weight loads are in flight, in steps of up to 16 rows whose (row, K
@@ -74,7 +73,6 @@ template <int kTT, bool kDown, int kItems>
 __device__ __forceinline__ void ffn_block(const FfnArgs& a, bool shared, int el, int rb, int n,
                                           Sums& sums, FusedRows<kItems>& fl) {
   constexpr bool kFused = kItems > 0;
-  constexpr bool kExact = !kDown;
   constexpr int kRing = kTT == 1 ? 2 : 1;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int uwave = __builtin_amdgcn_readfirstlane(wave);
@@ -168,7 +166,7 @@ __device__ __forceinline__ void ffn_block(const FfnArgs& a, bool shared, int el,
       for (int i = 0; i < kRing; ++i) {
         const int kb = first + i * kWaves;
         if (kb < Kb) {
-          constexpr bool kHold = kExact && kTT <= 2;  // else the converted rows do not fit
+          constexpr bool kHold = kTT == 1;  // else the converted rows do not fit
           i32x8_t x8[kHold ? 1 : kTT];
           Bf16Frag xe[kHold ? kTT : 1];
           float s0[kTT], s1[kTT];
@@ -196,23 +194,20 @@ __device__ __forceinline__ void ffn_block(const FfnArgs& a, bool shared, int el,
           }
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            // one row tile's operands at a time: the registers of kTT = 2 are tight
+            // one row tile's operands at a time: the registers are tight
             if constexpr (kTT > 1) __builtin_amdgcn_sched_barrier(0);
             const i32x8_t w8 = join8(w[i][r][0], w[i][r][1]);
-            Bf16Frag we;
-            if constexpr (kExact) we = e4m3_to_bf16(w8);
+            const Bf16Frag we = e4m3_to_bf16(w8);
 #pragma unroll
             for (int t = 0; t < kTT; ++t) {
               f32x4_t d;
               if constexpr (kHold) {
                 d = mfma_exact_block(we, xe[t]);
-              } else if constexpr (kExact) {
+              } else {
                 i32x8_t v = x8[t];
                 asm volatile("" : "+v"(v));  // converted here, not once for all row tiles
                 d = mfma_exact_block(we, e4m3_to_bf16(v));
                 __builtin_amdgcn_sched_barrier(0);
-              } else {
-                d = mfma_fp8_block(w8, x8[t]);
               }
               acc[r][t][0] = __builtin_fmaf(d[0], s0[t], acc[r][t][0]);
               acc[r][t][1] = __builtin_fmaf(d[1], s0[t], acc[r][t][1]);
