@@ -223,8 +223,6 @@ struct MidArgs {
   SplitK split;
 };
 
-constexpr int kCpolNt = 2;  // cache-policy operand of the buffer intrinsics: non-temporal
-
 __device__ __forceinline__ u32x4_t buffer16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
 }
@@ -398,7 +396,7 @@ int split_parts(int tiles, int Kb, int least) {
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // few rows: 16 weight rows a workgroup while that gives at most 512 workgroups, else 64
-inline bool thin_rows(const moe_fp8_dims& m) { return m.N <= 16 * 512; }
+inline bool thin_rows(int N) { return N <= 16 * 512; }
 // From 17 rows: 32 tokens a workgroup while they are all, else 64; 32 weight rows
 // while that gives no more workgroups than CUs, else 64 (half the token bytes
 // through L2, but only one K block's loads at a time fit the registers at 64
@@ -435,7 +433,7 @@ Plan fp8_plan(const moe_fp8_dims& m) {
   Plan p;
   if (m.M <= 16) {
     p.form = kRows;
-    p.tiles = thin_rows(m) ? ceil_div(m.N, 16) : ceil_div(m.N, 64);
+    p.tiles = thin_rows(m.N) ? ceil_div(m.N, 16) : ceil_div(m.N, 64);
     p.parts = split_parts(p.tiles, Kb, 16);
     p.part_bytes = 1024 * 16;
     return p;
@@ -494,22 +492,23 @@ void launch_tiles(Fp8TileArgs a, hipStream_t stream) {
 template <int kSrc>
 void launch_rows(RowsArgs a, const Plan& p, hipStream_t stream) {
   const int Kpart = ceil_div(a.Kb, p.parts);
-  const bool few = kSrc != kRowsQ && a.M * Kpart <= kFewItems;
-  const bool thin = a.N <= 16 * 512;
   const unsigned grid = p.tiles * p.parts;
   a.row_blocks = p.tiles;
-  if (thin && few && grid <= 256 && Kpart > 32)
-    rows_kernel<1, 16, kSrc, kFewItems><<<grid, 1024, 0, stream>>>(a);
-  else if (thin && grid <= 256 && Kpart > 32)
-    rows_kernel<1, 16, kSrc, kFusedItems><<<grid, 1024, 0, stream>>>(a);
-  else if (thin && few)
-    rows_kernel<1, 8, kSrc, kFewItems><<<grid, 512, 0, stream>>>(a);
-  else if (thin)
-    rows_kernel<1, 8, kSrc, kFusedItems><<<grid, 512, 0, stream>>>(a);
-  else if (few)
-    rows_kernel<4, 8, kSrc, kFewItems><<<grid, 512, 0, stream>>>(a);
+  const auto launch = [&](auto items) {
+    constexpr int kItems = decltype(items)::value;
+    if (!thin_rows(a.N))
+      rows_kernel<4, 8, kSrc, kItems><<<grid, 512, 0, stream>>>(a);
+    else if (grid <= 256 && Kpart > 32)
+      rows_kernel<1, 16, kSrc, kItems><<<grid, 1024, 0, stream>>>(a);
+    else
+      rows_kernel<1, 8, kSrc, kItems><<<grid, 512, 0, stream>>>(a);
+  };
+  if constexpr (kSrc == kRowsQ)
+    launch(std::integral_constant<int, 0>());
+  else if (a.M * Kpart <= kFewItems)
+    launch(std::integral_constant<int, kFewItems>());
   else
-    rows_kernel<4, 8, kSrc, kFusedItems><<<grid, 512, 0, stream>>>(a);
+    launch(std::integral_constant<int, kFusedItems>());
 }
 
 void launch_mid(const MidArgs& a, int rows, bool exact, unsigned grid, hipStream_t stream) {

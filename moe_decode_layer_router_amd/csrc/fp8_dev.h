@@ -21,6 +21,7 @@ typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kFp8Block = 128;     // K (and weight rows) a scale covers
 constexpr int kFp8TileBytes = 2048;  // 16 rows x 128 K
+constexpr int kCpolNt = 2;  // cache-policy operand of the buffer intrinsics: non-temporal
 
 __host__ __device__ inline int fp8_kb(int K) { return (K + kFp8Block - 1) / kFp8Block; }
 // row tiles, padded to whole blocks of 64 rows

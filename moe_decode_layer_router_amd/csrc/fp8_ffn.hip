@@ -26,11 +26,10 @@
 namespace moeblk {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;  // also the row tiles of a workgroup: each wave adds up one
 constexpr int kFusedRows = 16;    // most rows of a step whose workgroups quantise
 constexpr int kFusedItems = 576;  // most (row, K block) pairs: two workgroups a CU
 constexpr int kFewItems = 256;    // three
-constexpr int kCpolNt = 2;        // cache-policy operand of the buffer intrinsics: non-temporal
 
 // rows of a launch: quantised (xq, xs), or (fused) as they are
 struct RowSet {
@@ -230,7 +229,7 @@ __device__ __forceinline__ void ffn_block(const FfnArgs& a, bool shared, int el,
       for (int r = 0; r < 4; ++r) sums.v[wave][r][lane] = acc[r][t];
       __syncthreads();
       const int r = t0 + 16 * t + m16;
-      if (wave >= 4 || r >= n) continue;
+      if (r >= n) continue;
       f32x4_t v = sums.v[0][wave][lane];
 #pragma unroll
       for (int u = 1; u < kWaves; ++u) v += sums.v[u][wave][lane];
@@ -355,7 +354,7 @@ FfnLayout ffn_layout(const moe_dims& m) {
   l.hs = take(R * (I / 128) * 4);
   l.hshq = take(S * Is);
   l.hshs = take(S * (Is / 128) * 4);
-  l.total = at + 256;
+  l.total = at;
   return l;
 }
 
