@@ -528,11 +528,14 @@ def _fp8_bytes(N: int, K: int) -> int:
 
 def _workspace(ws, workspace_bytes, T: _Torch, device: int):
     """The workspace's pointer and bytes (``workspace_bytes`` may state fewer
-    than the tensor has)."""
-    ptr = _buf(ws, "workspace", workspace_bytes or 0, T.bytes, device)
+    than the tensor has; a raw pointer needs it)."""
     if workspace_bytes is None:
+        if type(ws) is int:
+            raise ValueError("workspace: a raw pointer needs workspace_bytes")
         workspace_bytes = 0 if ws is None else ws.numel()
-    return ptr, workspace_bytes
+    elif workspace_bytes < 0:  # would be a huge size_t
+        raise ValueError(f"workspace_bytes: {workspace_bytes}")
+    return _buf(ws, "workspace", workspace_bytes, T.bytes, device), workspace_bytes
 
 
 def fp8_dims_from(cfg) -> MoeFp8Dims:
