@@ -58,7 +58,11 @@ struct FusedRows {
   float s[kItems];
 };
 
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// silu(g) u; through exp(-|g|), which does not overflow where silu(g) is still a normal number
+__device__ __forceinline__ float swiglu(float g, float u) {
+  const float e = expf(-fabsf(g));
+  return (g < 0.0f ? g * e : g) / (1.0f + e) * u;
+}
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, size_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, static_cast<int>(bytes),

@@ -176,3 +176,40 @@ def test_experts_cancelling_products(name):
     if cfg.shared_I:
         want = torch.from_numpy(y_shared[0]).to(torch.bfloat16).double().numpy()
         assert all(np.array_equal(row, want) for row in y[R:])
+
+
+def test_experts_far_negative_gates():
+    """gate = -89 .. -91.75, where exp(-gate) is above fp32's range and silu(gate) is
+    still a normal number, times up = 2^101: h = -5e-7 .. -3e-8. down takes one h a
+    column. Off by e4m3's half step, by fp32's 8 ulp, and by exp(gate)'s own half step
+    among the subnormals (2^-150 of 1.4e-40 and more)."""
+    from moe_decode_layer_router_amd.block import Fp8Block
+
+    cfg = TINY
+    inp = make_fp8_inputs(cfg, 4)
+    d, I, n = cfg.d, cfg.I, cfg.n_local  # noqa: E741
+    x = np.full((cfg.S, d), 2.0, np.float32)
+    x[:, 0::128] = 448.0
+    inp["x"] = (x.view(np.uint32) >> 16).astype(np.uint16)
+    w13, w2 = np.zeros((n, 2 * I, d)), np.zeros((n, d, I))
+    tail = np.array([0.5, 0.75, 1.0, 1.25, 1.5, 1.75, 1.875, 0.625])[np.arange(I) % 8]
+    w13[:, :I, 4], w13[:, :I, 5] = -44.0, -tail
+    w13[:, I:, 6] = 1.0
+    w2[:, np.arange(d), np.arange(d) % I] = 1.0
+    s13 = np.ones((n, 2 * I // 128, d // 128), np.float32)
+    s13[:, I // 128 :] = 2.0**100
+    inp["w13"] = (rf.e4m3_encode(w13), s13)
+    inp["w2"] = (rf.e4m3_encode(w2), np.ones((n, d // 128, I // 128), np.float32))
+    blk = Fp8Block(inp)
+    blk.ids.copy_(torch.arange(cfg.topk)[None] + torch.arange(cfg.S)[:, None]).remainder_(cfg.E)
+    blk.bucket()
+    blk.expert_ffn()
+    torch.cuda.synchronize()
+    g = -2.0 * (44.0 + tail)
+    h = g * np.exp(g) / (1 + np.exp(g)) * 2.0**101
+    used = int(to_np(blk.offsets)[-1])
+    y = bf16_val(to_np(blk.y))[:used]
+    want = h[np.arange(d) % I][None]
+    rel = 2.0**-4 + 8 * rf.U24 + 2.0**-150 / np.exp(g).min()
+    assert used == cfg.S * cfg.topk
+    assert np.all(np.abs(y - want) <= (rel + rf.half_step("bf16") * (1 + rel)) * np.abs(want)), np.abs(y / want - 1).max()
