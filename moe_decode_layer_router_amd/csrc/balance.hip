@@ -99,7 +99,9 @@ __device__ __forceinline__ float row_max(float v) {
 }
 
 // exp through the hardware's exp2: the argument's rounding is |x| 2^-24 relative
-// in the result, the instruction's own error 1 ulp
+// in the result, the instruction's own error 1 ulp (that of the reciprocal below too;
+// at 65536 x 256 the outputs are 1.2e-7 off the 64-bit ones, with fp32's exp and
+// division 0.8e-7)
 __device__ __forceinline__ float exp_hw(float x) {
   return __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
 }

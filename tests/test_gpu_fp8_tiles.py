@@ -9,7 +9,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 import moe_decode_layer_router_amd as mb  # noqa: E402
-from synth import make_fp8_weight  # noqa: E402
+from synth import get_config, make_fp8_inputs, make_fp8_weight  # noqa: E402
 from tests import _ref_fp8 as rf  # noqa: E402
 from tests._fp8_plan import plan  # noqa: E402
 from tests.gpu_util import to_np  # noqa: E402
@@ -30,6 +30,7 @@ TILES = [
     (3900, 4000, 1300, "fp32", "tile128", 1), (1500, 2100, 1290, "fp32", "tile128", 1), (1500, 2100, 1290, "bf16", "tile128", 1),
     (2048, 4096, 392, "bf16", "tile128", 1), (700, 2000, 2100, "bf16", "tile128", 2), (700, 2000, 2100, "fp32", "tile128", 2),
     (513, 2700, 3500, "bf16", "tile128", 2), (330, 4096, 4200, "fp32", "tile128", 2), (1000, 1500, 4001, "fp32", "tile128", 2),
+    (25000, 17, 300, "bf16", "tile128", 1), (25000, 17, 300, "fp32", "tile128", 1), (25000, 1, 129, "bf16", "tile128", 1),
     (6500, 256, 3400, "bf16", "tile128", 2), (1300, 1100, 4000, "bf16", "tile128", 2),
 ]
 
@@ -216,3 +217,30 @@ def test_experts_at_full_width(S, d, I, Is, E):  # noqa: E741
         tol = tol + rf.half_step("bf16") * (np.abs(ref) + tol)
         assert np.all(err <= tol), (k13, e, float((err / tol).max()))
         assert np.linalg.norm(err) <= (rf.half_step("bf16") + 1e-4) * np.linalg.norm(ref), (k13, e)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(), dict(S=40, E=16, n_local=16), dict(S=100, E=1, n_local=1, topk=1), dict(S=30, shared_I=256),
+])
+def test_experts_of_rows_that_are_not_finite(kw):
+    """A token with an infinity or a NaN gives NaN rows; every other row keeps its bits,
+    also those of the same expert and the same 16 rows."""
+    from moe_decode_layer_router_amd.block import Fp8Block
+
+    cfg = get_config("tiny").with_(**kw)
+    blk = Fp8Block(make_fp8_inputs(cfg, 9))
+    blk.ids.copy_(torch.arange(cfg.topk)[None] + torch.arange(cfg.S)[:, None]).remainder_(cfg.E)
+    blk.bucket()
+    blk.expert_ffn()
+    clean = blk.y.clone()
+    blk.x[2, 5], blk.x[cfg.S - 1, cfg.d - 1] = float("inf"), float("nan")
+    blk.expert_ffn()
+    torch.cuda.synchronize()
+    used, R = int(blk.offsets[-1]), blk.dims.r_max
+    token = torch.full((blk.y.shape[0],), -1, device="cuda")
+    token[:used] = blk.rows[:used]
+    if cfg.shared_I:
+        token[R:] = torch.arange(cfg.S, device="cuda")
+    bad = (token == 2) | (token == cfg.S - 1)
+    assert int(bad.sum()) == 2 * (cfg.topk + bool(cfg.shared_I))
+    assert bool(torch.isnan(blk.y[bad]).all()) and torch.equal(blk.y[~bad], clean[~bad])
