@@ -464,7 +464,8 @@ int moe_pack_fp8(const moe_fp8_dims* dims, const void* q, const float* scales, v
  *            sums at any size;
  *   workspace device scratch of at least moe_fp8_gemm_workspace_bytes. It must
  *            be zero-filled once before its first use; every call leaves it
- *            ready for the next, with any dims of no larger workspace. Calls
+ *            ready for the next, with any dims of no larger workspace, of
+ *            moe_fp8_gemm or moe_fp8_proj; other functions need their own. Calls
  *            sharing it must not overlap. */
 size_t moe_fp8_gemm_workspace_bytes(const moe_fp8_dims* dims);
 int moe_fp8_gemm(const moe_fp8_dims* dims, const void* xq, const float* xs, const void* w_packed,
@@ -540,7 +541,8 @@ int moe_check_balance_dims(const moe_balance_dims* dims);
 
 /* Scratch of moe_expert_counts and moe_balance_loss (0 if `dims` is invalid):
  * zero-filled once before its first use; every call leaves it ready for the
- * next, with any dims of no larger workspace. Calls sharing it must not overlap. */
+ * next, of either function, with any dims of no larger workspace; other functions
+ * need their own. Calls sharing it must not overlap. */
 size_t moe_balance_workspace_bytes(const moe_balance_dims* dims);
 
 /* Picks per expert of every sequence, over all E experts (moe_bucket counts the
