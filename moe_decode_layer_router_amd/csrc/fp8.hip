@@ -81,8 +81,8 @@ __global__ __launch_bounds__(256) void pack_fp8_kernel(const uint8_t* __restrict
 // kSrc says where the rows come from. kRowsX: the rows themselves; every
 // workgroup quantises them into LDS while its first weight loads are in flight,
 // which costs less than a launch in front as long as they are few (rows x K
-// blocks up to kFusedItems): 1 x 4096 x 7168 15.6 us with the launch, 7.9 without
-// (29 MB of weights, 3.7 TB/s). kRowsQ: quantised rows, read from memory.
+// blocks up to kFusedItems): 1 x 4096 x 7168 15.6 us a call with the launch, 7.6 without
+// (29 MB of weights, 3.9 TB/s). kRowsQ: quantised rows, read from memory.
 enum RowSource { kRowsBf16, kRowsFp32, kRowsQ };
 
 constexpr int kFusedItems = 896;  // most (row, K block) pairs in LDS, 132 bytes each
@@ -210,7 +210,8 @@ __global__ __launch_bounds__(64 * kNW) void rows_kernel(RowsArgs a) {
 // 16 kRT weight rows x 16 kTT tokens a workgroup; its 8 waves take every eighth K
 // block of the workgroup's part, one or two blocks' loads in flight (kRing),
 // straight into registers (tokens through L2). The waves' sums are added through
-// LDS, all threads taking part. 128 x 7168 x 2048: 11.2 us.
+// LDS, all threads taking part. 128 x 7168 x 2048: 11.7 us (one 8-wave workgroup a CU,
+// one K block's loads in flight a wave).
 struct MidArgs {
   const uint8_t* xq;
   const float* xs;
@@ -378,7 +379,7 @@ namespace {
 // bring the workgroups to the number of CUs, each with at least `least` K blocks
 // (adding up P parts costs the last workgroup of a tile about 2 us). Measured, us,
 // split / whole: M = 8, N = 512, K = 8192 6.0 / 9.3; M = 64, N = 4096, K = 7168
-// 16.9 / 22.2; M = 512, N = 4096, K = 7168 43 / 57.
+// 18.0 / 21.9; M = 512, N = 4096, K = 7168 43 / 57.
 enum Form { kRows, kMid, kTile128, kTile256 };
 struct Plan {
   Form form;
@@ -401,8 +402,8 @@ inline bool thin_rows(int N) { return N <= 16 * 512; }
 // while that gives no more workgroups than CUs, else 64 (half the token bytes
 // through L2, but only one K block's loads at a time fit the registers at 64
 // tokens). Measured, us with the quantisation, 32 / 64 rows: M = 128, N = 7168, K
-// = 2048 17.1 / 12.7; M = 128, N = 512, K = 8192 11.7 / 14.7; M = 64, N = 4096, K =
-// 7168 17.2 / 18.1.
+// = 2048 18.2 / 13.3; M = 128, N = 512, K = 8192 12.0 / 15.0; M = 64, N = 4096, K =
+// 7168 18.0 / 18.6; M = 77, N = 4099, K = 2120 (258 / 130 workgroups) 15.3 / 15.2.
 inline int mid_tiles_m(const moe_fp8_dims& m) { return ceil_div(m.M, m.M <= 32 ? 32 : 64); }
 inline int mid_rows(const moe_fp8_dims& m) {
   return ceil_div(m.N, 32) * mid_tiles_m(m) <= 256 ? 32 : 64;

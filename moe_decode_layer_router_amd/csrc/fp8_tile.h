@@ -18,8 +18,9 @@
 // are needed, and the first operands of step k + 1 are read during the last row
 // tile, so no wave waits for LDS at the start of a step.
 //
-// 8192 x 4096 x 7168 (256 x 256 tiles): 212 us, 2.27 PFLOP/s. The operand copies
-// alone take 183 us (39 GB/s a CU), so they bound it more than the MFMAs do.
+// 8192 x 4096 x 7168 (256 x 256 tiles): median 231 us, 2.08 PFLOP/s; the fastest of 60
+// launches 211. The operand copies alone took 183 us (39 GB/s a CU), so they bound it more
+// than the MFMAs do.
 //
 // Weights are copied as packed (a 1 KiB piece is one operand half, read back
 // contiguously). Token rows are copied as whole 128-byte lines, the 16-byte

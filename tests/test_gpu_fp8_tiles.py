@@ -22,7 +22,7 @@ def _need_gpu():
         pytest.skip("no GPU")
 
 
-# M, N, K, outputs, form, K parts: 1 to 11 K blocks a part (the weights' three and the
+# M, N, K, outputs, form, K parts: 2 to 17 K blocks a part (the weights' three and the
 # rows' two buffers come round several times), last blocks that are not whole, rows and
 # columns that end inside a tile
 TILES = [
