@@ -15,8 +15,9 @@
 // Measured (gate_up + down, us): S = 8, 7.7 active experts of 4096 x 2048 23.5 + 14.9
 // (5.5, 4.3 TB/s); S = 128, 32 experts of 7168 x 2048 and a shared one 162 + 80 (5.9,
 // 6.0 TB/s). With few active experts most CUs idle (K is not split): one of 4096 x 2048,
-// 64 working workgroups a launch, 22 us in all for 25 MB. 4 waves instead of 8 let two or three workgroups share a CU, one's
-// first loads under another's last sums: S = 8 47 -> 40 us.
+// 64 working workgroups a launch, 22 us in all for 25 MB. 4 waves instead of 8 let two or
+// three workgroups share a CU, one's first loads under another's last sums: S = 8 47 -> 40
+// us.
 #include <type_traits>
 
 #include "fp8_dev.h"
