@@ -51,7 +51,8 @@ extern "C" {
 #define MOEBLK_ABI_VERSION 4 /* 2: moe_dims.bias_mode; 3: moe_route workspace;
                                 4: moe_forward_static, moe_forward_one_launch.
                                 Entry points added since (FP8 weights, the
-                                router's balance) change none of these. */
+                                router's balance, the path for many rows)
+                                change none of these. */
 
 /* status codes */
 #define MOE_OK 0
@@ -581,6 +582,235 @@ int moe_balance_loss(const moe_balance_dims* dims, const float* logits, const in
 int moe_balance_backward(const moe_balance_dims* dims, const float* logits, const int32_t* counts,
                          const int32_t* seq_starts, const float* dloss, float* dlogits,
                          hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* many rows: top-k with its gradient                                        */
+/* ------------------------------------------------------------------------ */
+
+/* The layer for rows beyond a decode step (prefill, training):
+ *   router logits -> moe_gate -> moe_sort -> the experts -> moe_return,
+ * with the experts on MXFP4 weights and rows (moe_mx_quant, moe_mx_gate_up,
+ * moe_mx_down), or a caller's own between moe_dispatch and moe_return. In these
+ * sections outputs and workspaces must not overlap inputs or each other, but where
+ * stated.
+ * Supported ranges: 1 <= T <= 2^22; 1 <= E <= 256; 1 <= topk <= 8, topk <= E;
+ * renorm, bias_mode in {0, 1}. */
+typedef struct moe_gate_dims {
+  int32_t T;         /* token rows */
+  int32_t E;         /* experts routed over */
+  int32_t topk;      /* picks per token */
+  int32_t score;     /* MOE_SCORE_SIGMOID or MOE_SCORE_SOFTMAX */
+  int32_t renorm;    /* 1: the weights of a token's picks add up to 1 */
+  int32_t bias_mode; /* 1: bias steers the selection (moe_dims.bias_mode); 0: not read */
+} moe_gate_dims;
+
+/* Host-only check of `dims`: MOE_OK, MOE_ERR_NULL, _SHAPE or _UNSUPPORTED. */
+int moe_check_gate_dims(const moe_gate_dims* dims);
+
+/* moe_topk for any number of rows, and for softmax scores.
+ *   logits   [T, E] fp32; bias [E] fp32 or NULL;
+ *   topk_ids [T, topk] int32, written: the token's experts by descending key, equal
+ *            keys to the lower id; the key is the logit, or under bias_mode 1 the fp32
+ *            sum logit + bias[e]. A key of -inf is never picked: a token with fewer
+ *            others gets -1 in the places behind them. NaN ranks above every number;
+ *   topk_w   [T, topk] fp32, written, 0 beside an id of -1; with l the logits and P the
+ *            token's picks:
+ *              sigmoid: 1 / (1 + exp(-l)), with renorm divided by its sum over P;
+ *              softmax: exp(l) / sum over all E of exp, with renorm over P. */
+int moe_gate(const moe_gate_dims* dims, const float* logits, const float* bias, int32_t* topk_ids,
+             float* topk_w, hipStream_t stream);
+
+/* Its gradient with respect to the logits, the picks held constant: with g = dtopk_w
+ * and w the weights that moe_gate gives,
+ *   sigmoid            dlogits[p] = g_p w_p (1 - sigmoid(l_p))
+ *   sigmoid, renorm    dlogits[p] = w_p (1 - sigmoid(l_p)) (g_p - sum_P g w)
+ *   softmax            dlogits[e] = softmax(l)_e (sum of g over picks of e - sum_P g w)
+ *   softmax, renorm    dlogits[p] = w_p (g_p - sum_P g w)
+ * and 0 elsewhere.
+ *   topk_ids [T, topk] moe_gate's, or others: a place whose id is outside [0, E) has no
+ *            gradient (its dtopk_w is not looked at), an expert picked twice counts twice;
+ *   dtopk_w  [T, topk] fp32;
+ *   dadd     [T, E] fp32, added to the result (moe_balance_backward's, say; may be
+ *            dlogits itself), or NULL;
+ *   dlogits  [T, E] fp32, written. */
+int moe_gate_backward(const moe_gate_dims* dims, const float* logits, const int32_t* topk_ids,
+                      const float* dtopk_w, const float* dadd, float* dlogits, hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* many rows: sorted by expert and back                                      */
+/* ------------------------------------------------------------------------ */
+
+/* Supported ranges: 1 <= T <= 2^22; 1 <= E <= 256; 1 <= topk <= 8, topk <= E; 1 <=
+ * n_local; 0 <= local_base, local_base + n_local <= E; 1 <= d <= 16384 (odd ones
+ * too); tok_type, row_type in {MOE_BF16, MOE_FP32}. R = T * topk sorted rows are
+ * the most a call can have; they are indexed 0 .. R - 1. */
+typedef struct moe_rows_dims {
+  int32_t T;          /* token rows */
+  int32_t E;          /* experts routed over */
+  int32_t topk;       /* picks per token */
+  int32_t n_local;    /* experts held by this GPU */
+  int32_t local_base; /* id of the first local expert */
+  int32_t d;          /* row width */
+  int32_t tok_type;   /* rows of tokens: x, out, dout */
+  int32_t row_type;   /* sorted rows: xs, y, dy */
+} moe_rows_dims;
+
+/* Host-only check of `dims`: MOE_OK, MOE_ERR_NULL, _SHAPE or _UNSUPPORTED. */
+int moe_check_rows_dims(const moe_rows_dims* dims);
+
+/* moe_bucket for any number of rows (reads every field but d and the types).
+ *   topk_ids [T, topk] int32; an id outside [local_base, local_base + n_local) is not
+ *            local (-1 among them: a padded pick); a token may pick an expert twice;
+ *   counts   [n_local] int32, written: picks of local expert el;
+ *   offsets  [n_local + 1] int32, written: exclusive prefix sum of counts;
+ *   rows     [R] int32, written: token of sorted row r (rows of expert el are
+ *            offsets[el] .. offsets[el + 1] - 1, by token, then by slot); -1 from
+ *            offsets[n_local] on;
+ *   pick_pos [T, topk] int32, written: sorted row of each pick, -1 if not local;
+ *   workspace device scratch of at least moe_sort_workspace_bytes, no initial
+ *            contents needed. Calls sharing it must not overlap. */
+size_t moe_sort_workspace_bytes(const moe_rows_dims* dims);
+int moe_sort(const moe_rows_dims* dims, const int32_t* topk_ids, int32_t* counts, int32_t* offsets,
+             int32_t* rows, int32_t* pick_pos, void* workspace, size_t workspace_bytes,
+             hipStream_t stream);
+
+/* The tokens' rows in sorted order: xs[pick_pos[t][s]] = x[t] for every place with
+ * pick_pos in [0, R).
+ *   x [T, d] tok_type; pick_pos moe_sort's;
+ *   xs [R, d] row_type, written for the rows some pick has; other rows are left as they
+ *      were. One rounding where row_type is the smaller.
+ * Its gradient is moe_return without weights. */
+int moe_dispatch(const moe_rows_dims* dims, const void* x, const int32_t* pick_pos, void* xs,
+                 hipStream_t stream);
+
+/* The weighted sums back at the tokens: out[t] = sum over t's slots s in order with
+ * pick_pos[t][s] in [0, R) of topk_w[t][s] * y[pick_pos[t][s]], in fp32, rounded once;
+ * zeros for a token without such a slot. (moe_combine does this for a decode step,
+ * with a norm of every row.)
+ *   y [R, d] row_type (rows that no pick has are not read); topk_w [T, topk] fp32, or
+ *     NULL for ones (the gradient of moe_dispatch); out [T, d] tok_type, written. */
+int moe_return(const moe_rows_dims* dims, const void* y, const float* topk_w,
+               const int32_t* pick_pos, void* out, hipStream_t stream);
+
+/* The gradient of moe_return:
+ *   dy[pick_pos[t][s]] = topk_w[t][s] * dout[t],  dtopk_w[t][s] = <dout[t], y[pick_pos[t][s]]>
+ * (fp32 sums in a fixed order), 0 for a slot without a sorted row.
+ *   dout [T, d] tok_type; y, topk_w, pick_pos as given to moe_return (topk_w not NULL);
+ *   dy [R, d] row_type, written for the rows some pick has; dtopk_w [T, topk] fp32,
+ *   written. */
+int moe_return_backward(const moe_rows_dims* dims, const void* dout, const void* y,
+                        const float* topk_w, const int32_t* pick_pos, void* dy, float* dtopk_w,
+                        hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* many rows: MXFP4 rows and products                                        */
+/* ------------------------------------------------------------------------ */
+
+/* Rows and weights held as OCP MXFP4: e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) with an e8m0 scale per 32 columns, 2^(byte - 127), byte 255: NaN.
+ * Sizes (elements). Supported ranges: 1 <= M <= 262144; 1 <= N <= 32768; 1 <= K <=
+ * 32768 (any of them odd); in_type, out_type in {MOE_BF16, MOE_FP32}. Kp = 128
+ * ceil(K / 128) is the padded width: codes are [M, Kp / 2] bytes (two a byte, the even
+ * column in the low nibble) and scales [M, Kp / 32] bytes, the layout moe_pack_mxfp4
+ * takes where K is whole. */
+typedef struct moe_mx_dims {
+  int32_t M;        /* rows (tokens) */
+  int32_t N;        /* weight rows = outputs a token */
+  int32_t K;        /* input width */
+  int32_t in_type;  /* x of moe_mx_quant and moe_mx_proj */
+  int32_t out_type; /* x of moe_mx_dequant, out of moe_mx_gemm and moe_mx_proj */
+} moe_mx_dims;
+
+/* Host-only check of `dims`: MOE_OK, MOE_ERR_NULL, _SHAPE or _UNSUPPORTED. */
+int moe_check_mx_dims(const moe_mx_dims* dims);
+
+/* Rows to MXFP4 (reads dims->M, K, in_type; the others must be in range).
+ *   x      [M, K] in_type;
+ *   q      [M, Kp / 2], scales [M, Kp / 32], written: a block's scale is 2^e with the
+ *          smallest integer e >= -127 such that its largest |x| is below 7 * 2^e, so
+ *          that values round (to nearest even) to at most 6 * 2^e and none saturates;
+ *          a zero block gets byte 0. Columns K .. Kp - 1 are zeros. A block that holds
+ *          an infinity or a NaN gets byte 255 and zero codes (its values are NaN). */
+int moe_mx_quant(const moe_mx_dims* dims, const void* x, void* q, void* scales,
+                 hipStream_t stream);
+
+/* Their values (reads dims->M, K, out_type): x [M, K] out_type, written, exact but for
+ * magnitudes of 2^128 and more (bytes 253, 254), which are +-inf. */
+int moe_mx_dequant(const moe_mx_dims* dims, const void* q, const void* scales, void* x,
+                   hipStream_t stream);
+
+/* Packed size of an MXFP4 weight [N, K] (0 if `dims` is invalid) and its packing into
+ * the kernels' tile order: q [N, Kp / 2], scales [N, Kp / 32] as moe_mx_quant lays them
+ * out (columns K .. Kp - 1 are not looked at). The packed buffer is opaque: only
+ * moe_mx_gemm and moe_mx_proj read it. It depends on N and K alone. */
+size_t moe_packed_mx_bytes(const moe_mx_dims* dims);
+int moe_pack_mx(const moe_mx_dims* dims, const void* q, const void* scales, void* packed,
+                hipStream_t stream);
+
+/* The product of MXFP4 rows and a packed weight:
+ *   out[t][n] = sum over the 32-column blocks j of 2^(xs[t][j] - 127) * 2^(ws[n][j] - 127)
+ *               * (sum over the block's k of xq[t][k] * q[n][k])
+ *   xq, xs   as moe_mx_quant writes them; any scale bytes are taken, columns K .. Kp - 1
+ *            must be finite;
+ *   out      [M, N] out_type, written: fp32 sums in a fixed order (deterministic), one
+ *            rounding; a NaN scale makes its rows' sums NaN;
+ *   workspace device scratch of at least moe_mx_gemm_workspace_bytes. It must be
+ *            zero-filled once before its first use; every call leaves it ready for the
+ *            next, with any dims of no larger workspace, of moe_mx_gemm or moe_mx_proj;
+ *            other functions need their own. Calls sharing it must not overlap. */
+size_t moe_mx_gemm_workspace_bytes(const moe_mx_dims* dims);
+int moe_mx_gemm(const moe_mx_dims* dims, const void* xq, const void* xs, const void* w_packed,
+                void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* moe_mx_quant of x and moe_mx_gemm in one call, with identical outputs (one launch up
+ * to 16 rows, whose workgroups quantise them; else the quantised rows live in the
+ * workspace).
+ *   x [M, K] in_type; out [M, N] out_type; workspace: moe_mx_gemm's rules. */
+size_t moe_mx_proj_workspace_bytes(const moe_mx_dims* dims);
+int moe_mx_proj(const moe_mx_dims* dims, const void* x, const void* w_packed, void* out,
+                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The experts' products on the weights of moe_expert_ffn (moe_pack_mxfp4), for any number
+ * of tokens and with MXFP4 rows. Supported ranges: 1 <= T <= 262144; 1 <= E <= 256;
+ * 1 <= topk <= 8, topk <= E; 1 <= n_local <= 32, n_local <= E; d, I as in moe_dims;
+ * h_type in {MOE_BF16, MOE_MXFP4}; out_type in {MOE_BF16, MOE_FP32}. R = T * topk, as
+ * for moe_sort, which makes offsets and rows. */
+#define MOE_MXFP4 2
+typedef struct moe_mx_group_dims {
+  int32_t T;        /* token rows */
+  int32_t E;        /* experts routed over (T topk / E rows an expert are expected) */
+  int32_t topk;     /* picks per token */
+  int32_t n_local;  /* experts held by this GPU */
+  int32_t d;        /* hidden size */
+  int32_t I;        /* expert intermediate size */
+  int32_t h_type;   /* moe_mx_gate_up's result */
+  int32_t out_type; /* moe_mx_down's result */
+} moe_mx_group_dims;
+
+/* Host-only check of `dims`: MOE_OK, MOE_ERR_NULL, _SHAPE or _UNSUPPORTED. */
+int moe_check_mx_group_dims(const moe_mx_group_dims* dims);
+
+/* gate_up and SwiGLU: for every sorted row r of local expert el (token t = rows[r]), with
+ * the product of moe_mx_gemm,
+ *   gu = x[t] . W13[el]^T,  h[r] = silu(gu[0:I]) * gu[I:2I]   (fp32), rounded once
+ *   xq [T, d / 2], xs [T, d / 32]: moe_mx_quant of the tokens' rows (M = T, K = d);
+ *   offsets [n_local + 1] int32 ascending, rows [R] int32 (tokens; values outside the
+ *      tokens are taken as the nearer end);
+ *   w13_packed: moe_pack_mxfp4's, MOE_W13;
+ *   h  h_type MOE_BF16: [R, I] bf16; MOE_MXFP4: [R, I / 2] codes, with hs [R, I / 32]
+ *      scale bytes (else hs may be NULL), quantised as by moe_mx_quant from the fp32
+ *      values. Written for rows < offsets[n_local]; other rows are left as they were. */
+int moe_mx_gate_up(const moe_mx_group_dims* dims, const void* xq, const void* xs,
+                   const int32_t* offsets, const int32_t* rows, const void* w13_packed, void* h,
+                   void* hs, hipStream_t stream);
+
+/* down: y[r] = hq[r] . W2[el]^T.
+ *   hq [R, I / 2], hs [R, I / 32]: moe_mx_gate_up's MXFP4 result;
+ *   w2_packed: moe_pack_mxfp4's, MOE_W2;
+ *   y [R, d] out_type, written for rows < offsets[n_local]; other rows are left as
+ *     they were. moe_return takes it. */
+int moe_mx_down(const moe_mx_group_dims* dims, const void* hq, const void* hs,
+                const int32_t* offsets, const void* w2_packed, void* y, hipStream_t stream);
 
 #ifdef __cplusplus
 }

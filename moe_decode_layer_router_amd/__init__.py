@@ -76,6 +76,36 @@ __all__ = [
     "moe_balance_backward",
     "MOE_SCORE_SIGMOID",
     "MOE_SCORE_SOFTMAX",
+    "MoeGateDims",
+    "gate_dims_from",
+    "moe_check_gate_dims",
+    "moe_gate",
+    "moe_gate_backward",
+    "MoeRowsDims",
+    "rows_dims_from",
+    "moe_check_rows_dims",
+    "moe_sort_workspace_bytes",
+    "moe_sort",
+    "moe_dispatch",
+    "moe_return",
+    "moe_return_backward",
+    "MoeMxDims",
+    "mx_dims_from",
+    "moe_check_mx_dims",
+    "moe_mx_quant",
+    "moe_mx_dequant",
+    "moe_packed_mx_bytes",
+    "moe_pack_mx",
+    "moe_mx_gemm_workspace_bytes",
+    "moe_mx_gemm",
+    "moe_mx_proj_workspace_bytes",
+    "moe_mx_proj",
+    "MoeMxGroupDims",
+    "mx_group_dims_from",
+    "moe_check_mx_group_dims",
+    "moe_mx_gate_up",
+    "moe_mx_down",
+    "MOE_MXFP4",
 ]
 
 MOE_OK = 0
@@ -91,6 +121,7 @@ MOE_WS13 = 2
 MOE_WS2 = 3
 MOE_BF16 = 0
 MOE_FP32 = 1
+MOE_MXFP4 = 2
 MOE_SCORE_SIGMOID = 0
 MOE_SCORE_SOFTMAX = 1
 MOE_STATIC_SCRATCH_BYTES = 16 << 20  # moe_forward_static's static scratch a GPU
@@ -150,6 +181,24 @@ class MoeBalanceDims(ctypes.Structure):
         ("score", ctypes.c_int32),
         ("coef", ctypes.c_float),
     ]
+
+
+class MoeGateDims(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("T", "E", "topk", "score", "renorm", "bias_mode")]
+
+
+class MoeRowsDims(ctypes.Structure):
+    _fields_ = [
+        (f, ctypes.c_int32) for f in ("T", "E", "topk", "n_local", "local_base", "d", "tok_type", "row_type")
+    ]
+
+
+class MoeMxDims(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("M", "N", "K", "in_type", "out_type")]
+
+
+class MoeMxGroupDims(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("T", "E", "topk", "n_local", "d", "I", "h_type", "out_type")]
 
 
 class MoeError(RuntimeError):
@@ -212,10 +261,13 @@ def lib() -> ctypes.CDLL:
         L.moe_post_expert.argtypes = [_PD] + [_P] * 4 + [ctypes.c_size_t, _P]
         L.moe_topk.argtypes = [_DP, _P, _P, _P, _P, _P]
         _FD, _BD, _Z = ctypes.POINTER(MoeFp8Dims), ctypes.POINTER(MoeBalanceDims), ctypes.c_size_t
+        _GD, _RD = ctypes.POINTER(MoeGateDims), ctypes.POINTER(MoeRowsDims)
+        _XD, _XG = ctypes.POINTER(MoeMxDims), ctypes.POINTER(MoeMxGroupDims)
         for f, dims in (
             ("moe_packed_fp8_bytes", _FD), ("moe_fp8_gemm_workspace_bytes", _FD),
             ("moe_fp8_proj_workspace_bytes", _FD), ("moe_fp8_ffn_workspace_bytes", _DP),
-            ("moe_balance_workspace_bytes", _BD),
+            ("moe_balance_workspace_bytes", _BD), ("moe_sort_workspace_bytes", _RD),
+            ("moe_packed_mx_bytes", _XD), ("moe_mx_gemm_workspace_bytes", _XD), ("moe_mx_proj_workspace_bytes", _XD),
         ):
             getattr(L, f).argtypes = [dims]
             getattr(L, f).restype = _Z
@@ -233,6 +285,23 @@ def lib() -> ctypes.CDLL:
             ("moe_expert_counts", [_BD] + [_P] * 4 + [_Z, _P]),
             ("moe_balance_loss", [_BD] + [_P] * 7 + [_Z, _P]),
             ("moe_balance_backward", [_BD] + [_P] * 6),
+            ("moe_check_gate_dims", [_GD]),
+            ("moe_gate", [_GD] + [_P] * 5),
+            ("moe_gate_backward", [_GD] + [_P] * 6),
+            ("moe_check_rows_dims", [_RD]),
+            ("moe_sort", [_RD] + [_P] * 6 + [_Z, _P]),
+            ("moe_dispatch", [_RD] + [_P] * 4),
+            ("moe_return", [_RD] + [_P] * 5),
+            ("moe_return_backward", [_RD] + [_P] * 7),
+            ("moe_check_mx_dims", [_XD]),
+            ("moe_mx_quant", [_XD] + [_P] * 4),
+            ("moe_mx_dequant", [_XD] + [_P] * 4),
+            ("moe_pack_mx", [_XD] + [_P] * 4),
+            ("moe_mx_gemm", [_XD] + [_P] * 5 + [_Z, _P]),
+            ("moe_mx_proj", [_XD] + [_P] * 4 + [_Z, _P]),
+            ("moe_check_mx_group_dims", [_XG]),
+            ("moe_mx_gate_up", [_XG] + [_P] * 8),
+            ("moe_mx_down", [_XG] + [_P] * 6),
         ):
             getattr(L, f).argtypes = args
             getattr(L, f).restype = ctypes.c_int
@@ -709,4 +778,263 @@ def moe_balance_backward(dims, logits, counts, seq_starts, dloss, dlogits, strea
         "moe_balance_backward", ctypes.byref(d), _buf(logits, "logits", d.T * d.E, T.f32, dev),
         _buf(counts, "counts", d.n_seq * d.E, T.i32, dev), _buf(seq_starts, "seq_starts", d.n_seq + 1, T.i32, dev),
         _buf(dloss, "dloss", 1, T.f32, dev), _buf(dlogits, "dlogits", d.T * d.E, T.f32, dev), _on(stream, T, dev),
+    )
+
+
+# ---------------------------------------------------------------- many rows: top-k
+
+
+def gate_dims_from(cfg) -> MoeGateDims:
+    """MoeGateDims from an object or dict with the moe_gate_dims field names."""
+    get = cfg.get if isinstance(cfg, dict) else (lambda k, dflt=None: getattr(cfg, k, dflt))
+    return MoeGateDims(
+        T=get("T"), E=get("E"), topk=get("topk"), score=get("score", MOE_SCORE_SIGMOID), renorm=get("renorm", 1),
+        bias_mode=get("bias_mode", 0),
+    )
+
+
+def _gd(dims) -> MoeGateDims:
+    return dims if isinstance(dims, MoeGateDims) else gate_dims_from(dims)
+
+
+def moe_check_gate_dims(dims) -> int:
+    return lib().moe_check_gate_dims(ctypes.byref(_gd(dims)))
+
+
+def moe_gate(dims, logits, bias, topk_ids, topk_w, stream=None) -> None:
+    """Top-k of the rows' logits and the routing weights (``bias``: None, or what
+    steers the selection under bias_mode 1)."""
+    d, T = _gd(dims), _t()
+    dev = T.device()
+    _call(
+        "moe_gate", ctypes.byref(d), _buf(logits, "logits", d.T * d.E, T.f32, dev), _buf(bias, "bias", d.E, T.f32, dev),
+        _buf(topk_ids, "topk_ids", d.T * d.topk, T.i32, dev), _buf(topk_w, "topk_w", d.T * d.topk, T.f32, dev),
+        _on(stream, T, dev),
+    )
+
+
+def moe_gate_backward(dims, logits, topk_ids, dtopk_w, dadd, dlogits, stream=None) -> None:
+    """``dadd``: None, or a gradient of the logits that is added (it may be ``dlogits``)."""
+    d, T = _gd(dims), _t()
+    dev = T.device()
+    _call(
+        "moe_gate_backward", ctypes.byref(d), _buf(logits, "logits", d.T * d.E, T.f32, dev),
+        _buf(topk_ids, "topk_ids", d.T * d.topk, T.i32, dev), _buf(dtopk_w, "dtopk_w", d.T * d.topk, T.f32, dev),
+        _buf(dadd, "dadd", d.T * d.E, T.f32, dev), _buf(dlogits, "dlogits", d.T * d.E, T.f32, dev),
+        _on(stream, T, dev),
+    )
+
+
+# ---------------------------------------------------------------- many rows: sorted by expert and back
+
+
+def rows_dims_from(cfg) -> MoeRowsDims:
+    """MoeRowsDims from an object or dict with the moe_rows_dims field names."""
+    get = cfg.get if isinstance(cfg, dict) else (lambda k, dflt=None: getattr(cfg, k, dflt))
+    return MoeRowsDims(
+        T=get("T"), E=get("E"), topk=get("topk"), n_local=get("n_local"), local_base=get("local_base", 0),
+        d=get("d", 1), tok_type=get("tok_type", MOE_BF16), row_type=get("row_type", MOE_BF16),
+    )
+
+
+def _rd(dims) -> MoeRowsDims:
+    return dims if isinstance(dims, MoeRowsDims) else rows_dims_from(dims)
+
+
+def moe_check_rows_dims(dims) -> int:
+    return lib().moe_check_rows_dims(ctypes.byref(_rd(dims)))
+
+
+def moe_sort_workspace_bytes(dims) -> int:
+    return lib().moe_sort_workspace_bytes(ctypes.byref(_rd(dims)))
+
+
+def moe_sort(dims, topk_ids, counts, offsets, rows, pick_pos, workspace, workspace_bytes=None, stream=None) -> None:
+    d, T = _rd(dims), _t()
+    dev = T.device()
+    ws, n = _workspace(workspace, workspace_bytes, T, dev)
+    picks = d.T * d.topk
+    _call(
+        "moe_sort", ctypes.byref(d), _buf(topk_ids, "topk_ids", picks, T.i32, dev),
+        _buf(counts, "counts", d.n_local, T.i32, dev), _buf(offsets, "offsets", d.n_local + 1, T.i32, dev),
+        _buf(rows, "rows", picks, T.i32, dev), _buf(pick_pos, "pick_pos", picks, T.i32, dev), ws, n,
+        _on(stream, T, dev),
+    )
+
+
+def moe_dispatch(dims, x, pick_pos, xs, stream=None) -> None:
+    """x [T, d] -> xs [T * topk, d], the picks' rows sorted by expert."""
+    d, T = _rd(dims), _t()
+    dev = T.device()
+    picks = d.T * d.topk
+    _call(
+        "moe_dispatch", ctypes.byref(d), _buf(x, "x", d.T * d.d, T.rows.get(d.tok_type), dev),
+        _buf(pick_pos, "pick_pos", picks, T.i32, dev), _buf(xs, "xs", picks * d.d, T.rows.get(d.row_type), dev),
+        _on(stream, T, dev),
+    )
+
+
+def moe_return(dims, y, topk_w, pick_pos, out, stream=None) -> None:
+    """The weighted sums of sorted rows (``topk_w`` None: plain sums, moe_dispatch's gradient)."""
+    d, T = _rd(dims), _t()
+    dev = T.device()
+    picks = d.T * d.topk
+    _call(
+        "moe_return", ctypes.byref(d), _buf(y, "y", picks * d.d, T.rows.get(d.row_type), dev),
+        _buf(topk_w, "topk_w", picks, T.f32, dev), _buf(pick_pos, "pick_pos", picks, T.i32, dev),
+        _buf(out, "out", d.T * d.d, T.rows.get(d.tok_type), dev), _on(stream, T, dev),
+    )
+
+
+def moe_return_backward(dims, dout, y, topk_w, pick_pos, dy, dtopk_w, stream=None) -> None:
+    d, T = _rd(dims), _t()
+    dev = T.device()
+    picks = d.T * d.topk
+    row = T.rows.get(d.row_type)
+    _call(
+        "moe_return_backward", ctypes.byref(d), _buf(dout, "dout", d.T * d.d, T.rows.get(d.tok_type), dev),
+        _buf(y, "y", picks * d.d, row, dev), _buf(topk_w, "topk_w", picks, T.f32, dev),
+        _buf(pick_pos, "pick_pos", picks, T.i32, dev), _buf(dy, "dy", picks * d.d, row, dev),
+        _buf(dtopk_w, "dtopk_w", picks, T.f32, dev), _on(stream, T, dev),
+    )
+
+
+# ---------------------------------------------------------------- many rows: MXFP4
+
+
+def mx_dims_from(cfg) -> MoeMxDims:
+    """MoeMxDims from an object or dict with the moe_mx_dims field names."""
+    get = cfg.get if isinstance(cfg, dict) else (lambda k, dflt=None: getattr(cfg, k, dflt))
+    return MoeMxDims(
+        M=get("M", 1), N=get("N", 1), K=get("K"), in_type=get("in_type", MOE_BF16), out_type=get("out_type", MOE_BF16),
+    )
+
+
+def _xd(dims) -> MoeMxDims:
+    return dims if isinstance(dims, MoeMxDims) else mx_dims_from(dims)
+
+
+def moe_check_mx_dims(dims) -> int:
+    return lib().moe_check_mx_dims(ctypes.byref(_xd(dims)))
+
+
+def moe_packed_mx_bytes(dims) -> int:
+    return lib().moe_packed_mx_bytes(ctypes.byref(_xd(dims)))
+
+
+def moe_mx_gemm_workspace_bytes(dims) -> int:
+    return lib().moe_mx_gemm_workspace_bytes(ctypes.byref(_xd(dims)))
+
+
+def moe_mx_proj_workspace_bytes(dims) -> int:
+    return lib().moe_mx_proj_workspace_bytes(ctypes.byref(_xd(dims)))
+
+
+def moe_mx_quant(dims, x, q, scales, stream=None) -> None:
+    """x [M, K] -> q [M, Kp / 2] uint8 (two codes a byte), scales [M, Kp / 32] uint8."""
+    d, T = _xd(dims), _t()
+    dev = T.device()
+    kc = -(-d.K // 128)
+    _call(
+        "moe_mx_quant", ctypes.byref(d), _buf(x, "x", d.M * d.K, T.rows.get(d.in_type), dev),
+        _buf(q, "q", d.M * kc * 64, T.bytes, dev), _buf(scales, "scales", d.M * kc * 4, T.bytes, dev),
+        _on(stream, T, dev),
+    )
+
+
+def moe_mx_dequant(dims, q, scales, x, stream=None) -> None:
+    """The values of MXFP4 rows: x [M, K] of dims.out_type."""
+    d, T = _xd(dims), _t()
+    dev = T.device()
+    kc = -(-d.K // 128)
+    _call(
+        "moe_mx_dequant", ctypes.byref(d), _buf(q, "q", d.M * kc * 64, T.bytes, dev),
+        _buf(scales, "scales", d.M * kc * 4, T.bytes, dev), _buf(x, "x", d.M * d.K, T.rows.get(d.out_type), dev),
+        _on(stream, T, dev),
+    )
+
+
+def _mx_bytes(N: int, K: int) -> int:
+    """Packed bytes of one [N, K] matrix: 64 x 128 tiles of 4352 bytes."""
+    return -(-N // 64) * -(-K // 128) * 4352
+
+
+def moe_pack_mx(dims, q, scales, packed, stream=None) -> None:
+    d, T = _xd(dims), _t()
+    dev = T.device()
+    kc = -(-d.K // 128)
+    _call(
+        "moe_pack_mx", ctypes.byref(d), _buf(q, "q", d.N * kc * 64, T.bytes, dev),
+        _buf(scales, "scales", d.N * kc * 4, T.bytes, dev), _buf(packed, "packed", _mx_bytes(d.N, d.K), T.bytes, dev),
+        _on(stream, T, dev),
+    )
+
+
+def moe_mx_gemm(dims, xq, xs, w_packed, out, workspace, workspace_bytes=None, stream=None) -> None:
+    d, T = _xd(dims), _t()
+    dev = T.device()
+    kc = -(-d.K // 128)
+    ws, n = _workspace(workspace, workspace_bytes, T, dev)
+    _call(
+        "moe_mx_gemm", ctypes.byref(d), _buf(xq, "xq", d.M * kc * 64, T.bytes, dev),
+        _buf(xs, "xs", d.M * kc * 4, T.bytes, dev), _buf(w_packed, "w_packed", _mx_bytes(d.N, d.K), T.bytes, dev),
+        _buf(out, "out", d.M * d.N, T.rows.get(d.out_type), dev), ws, n, _on(stream, T, dev),
+    )
+
+
+def moe_mx_proj(dims, x, w_packed, out, workspace, workspace_bytes=None, stream=None) -> None:
+    """moe_mx_quant of x and moe_mx_gemm in one call."""
+    d, T = _xd(dims), _t()
+    dev = T.device()
+    ws, n = _workspace(workspace, workspace_bytes, T, dev)
+    _call(
+        "moe_mx_proj", ctypes.byref(d), _buf(x, "x", d.M * d.K, T.rows.get(d.in_type), dev),
+        _buf(w_packed, "w_packed", _mx_bytes(d.N, d.K), T.bytes, dev),
+        _buf(out, "out", d.M * d.N, T.rows.get(d.out_type), dev), ws, n, _on(stream, T, dev),
+    )
+
+
+def mx_group_dims_from(cfg) -> MoeMxGroupDims:
+    """MoeMxGroupDims from an object or dict with the moe_mx_group_dims field names."""
+    get = cfg.get if isinstance(cfg, dict) else (lambda k, dflt=None: getattr(cfg, k, dflt))
+    return MoeMxGroupDims(
+        T=get("T"), E=get("E"), topk=get("topk"), n_local=get("n_local"), d=get("d"), I=get("I"),
+        h_type=get("h_type", MOE_MXFP4), out_type=get("out_type", MOE_BF16),
+    )
+
+
+def _xg(dims) -> MoeMxGroupDims:
+    return dims if isinstance(dims, MoeMxGroupDims) else mx_group_dims_from(dims)
+
+
+def moe_check_mx_group_dims(dims) -> int:
+    return lib().moe_check_mx_group_dims(ctypes.byref(_xg(dims)))
+
+
+def moe_mx_gate_up(dims, xq, xs, offsets, rows, w13_packed, h, hs=None, stream=None) -> None:
+    """gate_up with SwiGLU of sorted rows: h bf16 [T * topk, I], or (h_type MOE_MXFP4)
+    codes [T * topk, I / 2] with scale bytes hs [T * topk, I / 32]."""
+    d, T = _xg(dims), _t()
+    dev = T.device()
+    picks, mx = d.T * d.topk, d.h_type == MOE_MXFP4
+    _call(
+        "moe_mx_gate_up", ctypes.byref(d), _buf(xq, "xq", d.T * d.d // 2, T.bytes, dev),
+        _buf(xs, "xs", d.T * d.d // 32, T.bytes, dev), _buf(offsets, "offsets", d.n_local + 1, T.i32, dev),
+        _buf(rows, "rows", picks, T.i32, dev),
+        _buf(w13_packed, "w13_packed", d.n_local * _mx_bytes(2 * d.I, d.d), T.bytes, dev),
+        _buf(h, "h", picks * d.I // 2 if mx else picks * d.I, T.bytes if mx else T.bf16, dev),
+        _buf(hs, "hs", picks * d.I // 32 if mx else 0, T.bytes, dev), _on(stream, T, dev),
+    )
+
+
+def moe_mx_down(dims, hq, hs, offsets, w2_packed, y, stream=None) -> None:
+    """down of sorted MXFP4 rows: y [T * topk, d] of dims.out_type."""
+    d, T = _xg(dims), _t()
+    dev = T.device()
+    picks = d.T * d.topk
+    _call(
+        "moe_mx_down", ctypes.byref(d), _buf(hq, "hq", picks * d.I // 2, T.bytes, dev),
+        _buf(hs, "hs", picks * d.I // 32, T.bytes, dev), _buf(offsets, "offsets", d.n_local + 1, T.i32, dev),
+        _buf(w2_packed, "w2_packed", d.n_local * _mx_bytes(d.d, d.I), T.bytes, dev),
+        _buf(y, "y", picks * d.d, T.rows.get(d.out_type), dev), _on(stream, T, dev),
     )

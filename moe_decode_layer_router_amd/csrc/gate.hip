@@ -1,0 +1,325 @@
+// gate.hip -- top-k of many rows' router logits with the routing weights, and
+// the weights' gradient back to the logits (moe_gate, moe_gate_backward).
+//
+// With l the row's logits, P its picks and g the gradient of their weights:
+//   sigmoid         w_s = s(l_s)                 dl_s = g_s w_s (1 - s(l_s))
+//   sigmoid, renorm w_s = s(l_s) / sum_P s(l)    dl_s = w_s (1 - s(l_s)) (g_s - sum_P g w)
+//   softmax         w_s = p_s over all experts   dl_e = p_e (sum of g over picks of e - sum_P g w)
+//   softmax, renorm w_s = p_s over the picks     dl_s = w_s (g_s - sum_P g w)
+// Scores are taken relative to the largest where that keeps them from vanishing:
+// s(l) e^-m with m = min(max l, 0) is exp(min(l, 0) - m) / (1 + exp(-|l|)).
+//
+// Sixteen lanes hold a row (lanes16.h), four rows a wave. The forward orders the
+// keys as integers, takes the largest in each of topk rounds (a maximum over the
+// row, the lowest column that has it, that column struck out), and lane s keeps
+// pick s. The backward fills the row in LDS (zeros, or softmax's dense part), adds
+// the picks' terms there and stores it whole.
+#include <type_traits>
+
+#include "common.h"
+#include "host.h"
+#include "lanes16.h"
+
+namespace moeblk {
+namespace {
+
+constexpr int kGateRows = 16;  // rows a workgroup of 256 threads holds at a time
+constexpr int kMaxE = 256;
+
+// exp(x) to about an ulp: the argument's product with log2(e) in two parts (the
+// hardware's exp2 alone is off by |x| 2^-24)
+__device__ __forceinline__ float exp_near(float x) {
+  constexpr float kHi = 1.44269504088896341f, kLo = 1.92596299112661746887e-8f;
+  const float t = x * kHi;
+  const float r = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  // an infinite or NaN argument has no second part
+  return __builtin_fabsf(t) <= 1e30f ? __builtin_fmaf(e, r * 0.693147180559945309f, e) : e;
+}
+
+// An order of fp32 keys as integers: NaN above all (whatever its sign), then as
+// floats (-0 = +0); kNever for -inf, which is never picked.
+constexpr uint32_t kNever = 0;
+__device__ __forceinline__ uint32_t order_key(float f) {
+  if (f != f) return 0xffffffffu;
+  if (f == -INFINITY) return kNever;
+  const uint32_t u = __float_as_uint(f + 0.0f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+  return static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(v), kCtrl, 0xf, 0xf, false));
+}
+__device__ __forceinline__ uint32_t row_max_u(uint32_t v) {
+  v = max(v, dpp_u<0xb1>(v));
+  v = max(v, dpp_u<0x4e>(v));
+  v = max(v, dpp_u<0x141>(v));
+  return max(v, dpp_u<0x140>(v));
+}
+__device__ __forceinline__ uint32_t row_min_u(uint32_t v) {
+  v = min(v, dpp_u<0xb1>(v));
+  v = min(v, dpp_u<0x4e>(v));
+  v = min(v, dpp_u<0x141>(v));
+  return min(v, dpp_u<0x140>(v));
+}
+
+struct GateArgs {
+  const float *logits, *bias;  // bias: only what steers the selection
+  int32_t* ids;
+  float* w;
+  int T, E, topk, score, renorm;
+};
+
+// a row's largest logit (0 if there is none) and its sum of exp(l - m)
+template <int kNI>
+__device__ __forceinline__ void softmax_row(const Row<kNI>& l, float& m, float& total, Row<kNI>* p) {
+  m = l.v[0];
+#pragma unroll
+  for (int i = 1; i < 4 * kNI; ++i) m = fmaxf(m, l.v[i]);
+  m = row_max(m);
+  m = m == -INFINITY ? 0.0f : m;
+  total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4 * kNI; ++i) {
+    const float e = exp_near(l.v[i] - m);
+    if (p) p->v[i] = e;
+    total += e;
+  }
+  total = row_sum(total);
+}
+
+// Lane s of a row: pick s's logit v (`on`: there is one). Its weight, and 1 -
+// sigmoid (1 for softmax) for the gradient; m, total: of the whole row, where
+// the weights are softmax's over all experts.
+__device__ __forceinline__ float pick_weight(float v, bool on, int score, int renorm, float m,
+                                             float total, float& slope) {
+  float a;
+  slope = 1.0f;
+  if (score == MOE_SCORE_SIGMOID) {
+    const float top = renorm ? row_max(on ? v : -INFINITY) : 0.0f;
+    m = top == -INFINITY ? 0.0f : fminf(top, 0.0f);
+    const float r = 1.0f / (1.0f + exp_near(-fabsf(v)));
+    a = exp_near(fminf(v, 0.0f) - m) * r;
+    if (v != v) a = v;  // fminf drops a NaN
+    slope = (v >= 0.0f ? exp_near(-v) : 1.0f) * r;
+    total = 1.0f;
+  } else {
+    if (renorm) {
+      m = row_max(on ? v : -INFINITY);
+      m = m == -INFINITY ? 0.0f : m;
+    }
+    a = exp_near(v - m);
+  }
+  a = on ? a : 0.0f;
+  if (renorm) total = row_sum(a);
+  return total == 0.0f ? 0.0f : a / total;
+}
+
+template <int kNI>
+__global__ __launch_bounds__(256) void gate_kernel(GateArgs a) {
+  const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int E = a.E;
+  Row<kNI> bias;
+#pragma unroll
+  for (int i = 0; i < 4 * kNI; ++i) bias.v[i] = 0.0f;
+  if (a.bias) load_row<kNI>(a.bias, 0, E, j, bias);
+  const int step = kGateRows * gridDim.x;
+  int row = blockIdx.x * kGateRows + group;
+  Row<kNI> next;
+  load_row<kNI>(a.logits, min(row, a.T - 1), E, j, next);
+  // the lanes of a row stay together, and so do the four rows of a wave (the loads
+  // past the last row are of the last row)
+  for (int base = blockIdx.x * kGateRows; base < a.T; base += step, row += step) {
+    const Row<kNI> l = next;
+    load_row<kNI>(a.logits, min(row + step, a.T - 1), E, j, next);
+    uint32_t key[4 * kNI];
+#pragma unroll
+    for (int i = 0; i < 4 * kNI; ++i) key[i] = order_key(a.bias ? l.v[i] + bias.v[i] : l.v[i]);
+    int id = -1;
+    for (int s = 0; s < a.topk; ++s) {
+      uint32_t m = key[0];
+#pragma unroll
+      for (int i = 1; i < 4 * kNI; ++i) m = max(m, key[i]);
+      m = row_max_u(m);
+      uint32_t col = 0xffffu;  // lowest column with the maximum: 64 i + c ascends with the index
+#pragma unroll
+      for (int i = 4 * kNI - 1; i >= 0; --i)
+        col = key[i] == m ? static_cast<uint32_t>((i >> 2) * 64 + (i & 3)) : col;
+      const uint32_t e = row_min_u(col == 0xffffu ? col : col + 4 * j);
+#pragma unroll
+      for (int i = 0; i < 4 * kNI; ++i)
+        key[i] = e == static_cast<uint32_t>((i >> 2) * 64 + 4 * j + (i & 3)) ? kNever : key[i];
+      if (j == s) id = m == kNever ? -1 : static_cast<int>(e);
+    }
+    float m = 0.0f, total = 1.0f;
+    if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) softmax_row<kNI>(l, m, total, nullptr);
+    const bool on = id >= 0 && row < a.T;
+    const float v = on ? a.logits[static_cast<size_t>(row) * E + id] : -INFINITY;
+    float slope;
+    const float w = pick_weight(v, on, a.score, a.renorm, m, total, slope);
+    if (j < a.topk && row < a.T) {
+      const size_t at = static_cast<size_t>(row) * a.topk + j;
+      a.ids[at] = id;
+      a.w[at] = w;
+    }
+  }
+}
+
+// LDS that lanes of one wave hand to each other: its accesses stay in order, in the
+// code as well
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+struct GateBackwardArgs {
+  const float* logits;
+  const int32_t* ids;
+  const float *dw, *dadd;
+  float* dlogits;
+  int T, E, topk, score, renorm;
+};
+
+template <int kNI, bool kDense>
+__global__ __launch_bounds__(256) void gate_backward_kernel(GateBackwardArgs a) {
+  __shared__ __attribute__((aligned(16))) float rows[kGateRows][64 * kNI];
+  const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int E = a.E, step = kGateRows * gridDim.x;
+  float* mine = rows[group];
+  Row<kNI> next;
+  int next_id = -1;
+  float next_dw = 0.0f;
+  const auto load = [&](int row) {
+    next_id = -1;
+    if (row < a.T) {
+      if (j < a.topk) {
+        next_id = a.ids[static_cast<size_t>(row) * a.topk + j];
+        next_dw = a.dw[static_cast<size_t>(row) * a.topk + j];
+      }
+      if constexpr (kDense) load_row<kNI>(a.logits, row, E, j, next);
+    }
+  };
+  int row = blockIdx.x * kGateRows + group;
+  load(row);
+  for (int base = blockIdx.x * kGateRows; base < a.T; base += step, row += step) {
+    const int id = next_id;
+    const float dw = next_dw;
+    const Row<kNI> l = next;
+    load(row + step);
+    const bool in = row < a.T, on = id >= 0 && id < E;
+    const float v = on ? a.logits[static_cast<size_t>(row) * E + id] : -INFINITY;
+    float m = 0.0f, total = 1.0f;
+    Row<kNI> p;
+    if constexpr (kDense) softmax_row<kNI>(l, m, total, &p);
+    float slope;
+    const float w = pick_weight(v, on, a.score, a.renorm, m, total, slope);
+    const float g = on ? dw : 0.0f;
+    const float mean = kDense || a.renorm ? row_sum(on ? g * w : 0.0f) : 0.0f;
+    // the row in LDS: its 16 lanes are of one wave
+#pragma unroll
+    for (int i = 0; i < kNI; ++i) {
+      f32x4_t q = {0, 0, 0, 0};
+      if constexpr (kDense) {
+        const float scale = total == 0.0f ? 0.0f : -mean / total;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) q[c] = p.v[4 * i + c] * scale;
+      }
+      *reinterpret_cast<f32x4_t*>(mine + 64 * i + 4 * j) = q;
+    }
+    wave_sync();
+    if (on) atomicAdd(&mine[id], kDense ? w * g : w * slope * (g - mean));  // the same id twice adds up
+    wave_sync();
+    if (in) {
+      const size_t at = static_cast<size_t>(row) * E;
+#pragma unroll
+      for (int i = 0; i < kNI; ++i) {
+        const int e = 64 * i + 4 * j;
+        f32x4_t q = *reinterpret_cast<const f32x4_t*>(mine + e);
+        if (e + 4 <= E) {
+          if (a.dadd) q += *reinterpret_cast<const f32x4_any_t*>(a.dadd + at + e);
+          *reinterpret_cast<f32x4_any_t*>(a.dlogits + at + e) = q;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 3; ++c)
+            if (e + c < E) a.dlogits[at + e + c] = a.dadd ? q[c] + a.dadd[at + e + c] : q[c];
+        }
+      }
+    }
+    wave_sync();
+  }
+}
+
+// enough workgroups to fill the CUs several times over
+unsigned gate_grid(int T) {
+  const int n = (T + kGateRows - 1) / kGateRows;
+  return static_cast<unsigned>(n < 2048 ? n : 2048);
+}
+
+template <typename F>
+void for_width(int E, F f) {
+  if (E <= 64) f(std::integral_constant<int, 1>());
+  else if (E <= 128) f(std::integral_constant<int, 2>());
+  else f(std::integral_constant<int, 4>());
+}
+
+}  // namespace
+
+int check_gate_dims(const moe_gate_dims* d) {
+  MOE_REQUIRE(d != nullptr, MOE_ERR_NULL);
+  MOE_REQUIRE(d->T >= 1 && d->T <= 1 << 22, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->E >= 1 && d->E <= kMaxE, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->topk >= 1 && d->topk <= 8 && d->topk <= d->E, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->score == MOE_SCORE_SIGMOID || d->score == MOE_SCORE_SOFTMAX, MOE_ERR_UNSUPPORTED);
+  MOE_REQUIRE(d->renorm == 0 || d->renorm == 1, MOE_ERR_UNSUPPORTED);
+  MOE_REQUIRE(d->bias_mode == 0 || d->bias_mode == 1, MOE_ERR_UNSUPPORTED);
+  return MOE_OK;
+}
+
+}  // namespace moeblk
+
+using namespace moeblk;
+
+extern "C" {
+
+int moe_check_gate_dims(const moe_gate_dims* dims) { return check_gate_dims(dims); }
+
+int moe_gate(const moe_gate_dims* dims, const float* logits, const float* bias, int32_t* topk_ids,
+             float* topk_w, hipStream_t stream) {
+  const int rc = check_gate_dims(dims);
+  if (rc) return rc;
+  MOE_REQUIRE(logits && topk_ids && topk_w, MOE_ERR_NULL);
+  MOE_REQUIRE(aligned16(logits) && aligned16(bias) && aligned16(topk_ids) && aligned16(topk_w),
+              MOE_ERR_ALIGN);
+  const GateArgs a = {logits,  dims->bias_mode == 1 ? bias : nullptr, topk_ids, topk_w,
+                      dims->T, dims->E, dims->topk, dims->score, dims->renorm};
+  for_width(dims->E, [&](auto ni) {
+    gate_kernel<decltype(ni)::value><<<gate_grid(dims->T), 256, 0, stream>>>(a);
+  });
+  return launch_status();
+}
+
+int moe_gate_backward(const moe_gate_dims* dims, const float* logits, const int32_t* topk_ids,
+                      const float* dtopk_w, const float* dadd, float* dlogits,
+                      hipStream_t stream) {
+  const int rc = check_gate_dims(dims);
+  if (rc) return rc;
+  MOE_REQUIRE(logits && topk_ids && dtopk_w && dlogits, MOE_ERR_NULL);
+  MOE_REQUIRE(aligned16(logits) && aligned16(topk_ids) && aligned16(dtopk_w) && aligned16(dadd) &&
+                  aligned16(dlogits),
+              MOE_ERR_ALIGN);
+  const GateBackwardArgs a = {logits,  topk_ids, dtopk_w,    dadd,        dlogits,
+                              dims->T, dims->E,  dims->topk, dims->score, dims->renorm};
+  const bool dense = dims->score == MOE_SCORE_SOFTMAX && !dims->renorm;
+  for_width(dims->E, [&](auto ni) {
+    constexpr int kNI = decltype(ni)::value;
+    if (dense)
+      gate_backward_kernel<kNI, true><<<gate_grid(dims->T), 256, 0, stream>>>(a);
+    else
+      gate_backward_kernel<kNI, false><<<gate_grid(dims->T), 256, 0, stream>>>(a);
+  });
+  return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,392 @@
+// mx_group.hip -- the experts' MXFP4 products of many rows: gate_up with SwiGLU from
+// the tokens' quantised rows (moe_mx_gate_up), and down (moe_mx_down).
+//
+// The rows are sorted by expert (moe_sort): expert e has rows offsets[e] ..
+// offsets[e + 1] - 1, as the device knows; the host sizes the grid for any split of
+// the picks, and a workgroup finds its tile from the offsets or ends. The weights are
+// those that moe_pack_mxfp4 lays out for the decode path.
+//
+// In gate_up a lane's four outputs of a row tile are (gate i, gate i + 1, up i,
+// up i + 1) (common.h), so SwiGLU needs no exchange; a row block of 64 weight rows is
+// 32 intermediates, one MX block of the result, whose 32 values lie in four lanes: the
+// next product's quantisation is two exchanges away.
+#include <type_traits>
+
+#include "host.h"
+#include "mx_dev.h"
+#include "mx_rows.h"
+#include "mx_tile.h"
+
+namespace moeblk {
+namespace {
+
+constexpr int kMaxGroups = 32;
+
+struct MxGroupArgs {
+  const uint8_t *xq, *xs, *w;
+  const int32_t *offsets, *rows;  // rows: gate_up's row -> token, NULL: the rows themselves
+  void* out;
+  uint8_t* hs;  // scale bytes of an MXFP4 result
+  int T, R, n, N, Kc;
+  int type;  // MOE_BF16, MOE_FP32 or MOE_MXFP4
+  size_t w_bytes;  // an expert's
+};
+
+struct Group {
+  int e, first, count, tile;  // expert, its first row and rows; the tile within it (-1: none)
+};
+
+// Tile `t` of all experts' (tiles_n a group of kBM rows). Lane i holds expert i; offsets
+// outside the rows are taken as the nearer end.
+template <int kBM>
+__device__ __forceinline__ Group find_group(const MxGroupArgs& a, int b, int tiles_n) {
+  const int lane = threadIdx.x & 63;
+  const int o = lane <= a.n ? min(max(a.offsets[lane], 0), a.R) : 0;
+  const int next = __shfl_down(o, 1, kWave);
+  const int count = lane < a.n ? max(next - o, 0) : 0;
+  const int tiles = (count + kBM - 1) / kBM * tiles_n;
+  int incl = tiles;
+#pragma unroll
+  for (int s = 1; s < kMaxGroups; s <<= 1) {
+    const int v = __shfl_up(incl, s, kWave);
+    if (lane >= s) incl += v;
+  }
+  const int total = __builtin_amdgcn_readlane(incl, kMaxGroups - 1);
+  Group g;
+  const int t = mx_xcd_tile(b, total);
+  if (t < 0) {
+    g.e = g.first = g.count = 0;
+    g.tile = -1;
+    return g;
+  }
+  const uint64_t m = __ballot(t < incl && lane < kMaxGroups);
+  g.e = __builtin_ctzll(m);
+  g.first = __builtin_amdgcn_readlane(o, g.e);
+  g.count = __builtin_amdgcn_readlane(count, g.e);
+  g.tile = t - __builtin_amdgcn_readlane(incl - tiles, g.e);
+  return g;
+}
+
+// ---------------------------------------------------------------- many rows an expert
+
+template <int kRT, int kTT, int kWN, int kWM, int kStages, bool kGateUp>
+__global__ __launch_bounds__(64 * kWN * kWM, kRT * kTT > 32 ? 1 : 2) void mx_group_tile_kernel(
+    MxGroupArgs a) {
+  constexpr int BN = 16 * kRT * kWN, BM = 16 * kTT * kWM;
+  __shared__ __attribute__((aligned(128))) uint8_t lds[mx_tile_lds<kRT, kTT, kWN, kWM, kStages>()];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int m16 = lane & 15, g = lane >> 4;
+  const int wn = wave % kWN, wm = wave / kWN;
+  const int tiles_n = (a.N + BN - 1) / BN;
+  const Group gr = find_group<BM>(a, blockIdx.x, tiles_n);
+  if (gr.tile < 0) return;
+  int tn, tm;
+  mx_tile_at(gr.tile, tiles_n, (gr.count + BM - 1) / BM, tn, tm);
+  const int first = gr.first + tm * BM, rows = min(BM, gr.count - tm * BM);
+  MxTile p;
+  p.w = a.w + gr.e * a.w_bytes;
+  p.rb0 = tn * (BN / 64);
+  p.row_blocks = a.N / kRowsPerBlock;
+  const size_t base = kGateUp ? 0 : first;
+  const uint32_t readable = kGateUp ? a.T : rows;
+  p.xq = a.xq + base * a.Kc * 64;
+  p.xs = a.xs + base * a.Kc * 4;
+  p.xq_bytes = readable * a.Kc * 64u;
+  p.xs_bytes = readable * a.Kc * 4u;
+  p.Kc = a.Kc;
+  p.c0 = 0;
+  p.c1 = a.Kc;
+  f32x4_t acc[kRT][kTT];
+  mx_tile_body<kRT, kTT, kWN, kWM, kStages>(
+      p,
+      [&](int i) {
+        i = min(i, rows - 1);
+        if constexpr (kGateUp) return min(max(a.rows[first + i], 0), a.T - 1);
+        return i;
+      },
+      lds, acc);
+  const int m0 = wm * 16 * kTT;  // of this wave
+  if constexpr (kGateUp) {
+    const int I = a.N / 2, i0 = (p.rb0 + wn * (kRT / 4)) * 32;  // first intermediate of this wave
+#pragma unroll
+    for (int r = 0; r < kRT; ++r)
+#pragma unroll
+      for (int t = 0; t < kTT; ++t) {
+        acc[r][t][0] = mx_swiglu(acc[r][t][0], acc[r][t][2]);
+        acc[r][t][1] = mx_swiglu(acc[r][t][1], acc[r][t][3]);
+      }
+    if (a.type == MOE_BF16) {
+      mx_store_bf16<kTT, 8 * kRT>(
+          lds,
+          [&](int t, uint8_t* o) {
+#pragma unroll
+            for (int r = 0; r < kRT; ++r)
+              *reinterpret_cast<uint32_t*>(o + (r >> 2) * 64 + (r & 3) * 16 + 4 * g) =
+                  pack_bf16x2(acc[r][t][0], acc[r][t][1]);
+          },
+          [&](int row) -> uint16_t* {
+            return m0 + row < rows
+                       ? static_cast<uint16_t*>(a.out) + static_cast<size_t>(first + m0 + row) * I + i0
+                       : nullptr;
+          },
+          I - i0);
+      return;
+    }
+    // MXFP4: a block's codes meet in LDS, 16 bytes a row
+    constexpr int kB = kRT / 4;
+    uint8_t* o = lds + wave * (16 * kTT * kB * 16);
+#pragma unroll
+    for (int t = 0; t < kTT; ++t) {
+      const int row = m0 + t * 16 + m16;
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          m = max(m, __float_as_uint(acc[4 * b + r][t][0]) & 0x7fffffffu);
+          m = max(m, __float_as_uint(acc[4 * b + r][t][1]) & 0x7fffffffu);
+        }
+        m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16, kWave)));
+        m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32, kWave)));
+        const uint32_t byte = mx_scale_byte(m);
+        const float s = e8m0_scale(byte);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = acc[4 * b + (i >> 1)][t][i & 1];
+        const uint32_t q = mx_codes_or_zero(mx_codes(v, s), byte);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          o[((t * 16 + m16) * kB + b) * 16 + 4 * r + g] = static_cast<uint8_t>(q >> (8 * r));
+        if (g == 0 && row < rows && i0 + 32 * b < I)
+          a.hs[static_cast<size_t>(first + row) * (I / 32) + i0 / 32 + b] = static_cast<uint8_t>(byte);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < (16 * kTT * kB + 63) / 64; ++i) {
+      const int at = i * 64 + lane, row = m0 + at / kB, b = at % kB;
+      if (at < 16 * kTT * kB && row < rows && i0 + 32 * b < I)
+        *reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(a.out) +
+                                    static_cast<size_t>(first + row) * (I / 2) + i0 / 2 + 16 * b) =
+            *reinterpret_cast<const u32x4_t*>(o + at * 16);
+    }
+  } else {
+    const int n0 = tn * BN + wn * 16 * kRT;
+    if (a.type == MOE_BF16) {
+      mx_store_bf16<kTT, 16 * kRT>(
+          lds,
+          [&](int t, uint8_t* o) {
+#pragma unroll
+            for (int r = 0; r < kRT; ++r)
+              *reinterpret_cast<u32x2_t*>(o + r * 32 + 8 * g) =
+                  u32x2_t{pack_bf16x2(acc[r][t][0], acc[r][t][1]),
+                          pack_bf16x2(acc[r][t][2], acc[r][t][3])};
+          },
+          [&](int row) -> uint16_t* {
+            return m0 + row < rows
+                       ? static_cast<uint16_t*>(a.out) + static_cast<size_t>(first + m0 + row) * a.N + n0
+                       : nullptr;
+          },
+          a.N - n0);
+      return;
+    }
+#pragma unroll
+    for (int t = 0; t < kTT; ++t) {
+      const int row = m0 + t * 16 + m16;
+#pragma unroll
+      for (int r = 0; r < kRT; ++r) {
+        const int n = n0 + r * 16 + 4 * g;
+        if (row < rows)
+          store4<true>(a.out, static_cast<size_t>(first + row) * a.N + n, a.N - n, acc[r][t], false);
+        __builtin_amdgcn_sched_barrier(0);  // one tile's addresses at a time
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- few rows an expert
+//
+// A workgroup takes one row block and up to 64 rows of an expert.
+constexpr int kFewRows = 64, kFewWaves = 8;
+
+template <int kTT, bool kGateUp>
+__device__ __forceinline__ void few_rows(const MxGroupArgs& a, const Group& gr, int rb, int m0, f32x4_t* red) {
+  constexpr int kEach = (4 * kTT + kFewWaves - 1) / kFewWaves;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int m16 = lane & 15, g = lane >> 4;
+  const MxRowsTile p = {a.w + gr.e * a.w_bytes, 4 * rb, a.Kc, 0, a.Kc, m0, gr.count};
+  f32x4_t sum[kEach];
+  mx_rows_body<4, kTT, kFewWaves, 2, kMxRowsQ>(
+      p, nullptr, 0, a.xq, a.xs,
+      [&](int i) {
+        if constexpr (kGateUp) return min(max(a.rows[gr.first + i], 0), a.T - 1);
+        return gr.first + i;
+      },
+      red, sum);
+  if constexpr (!kGateUp) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = e * kFewWaves + wave, row = m0 + (i % kTT) * 16 + m16;
+      const int n = (4 * rb + i / kTT) * 16 + 4 * g;
+      if (row < gr.count && i < 4 * kTT)
+        store4<true>(a.out, static_cast<size_t>(gr.first + row) * a.N + n, a.N - n, sum[e],
+                     a.type == MOE_BF16);
+    }
+  } else {
+    // the 32 intermediates of a row meet in LDS; then 4 threads a row, 8 values each
+    constexpr int kPitch = 36;
+    float* h = reinterpret_cast<float*>(red);
+    __syncthreads();  // the sums have been read
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = e * kFewWaves + wave;
+      if (i < 4 * kTT) {
+        float* to = h + ((i % kTT) * 16 + m16) * kPitch + 8 * (i / kTT) + 2 * g;
+        to[0] = mx_swiglu(sum[e][0], sum[e][2]);
+        to[1] = mx_swiglu(sum[e][1], sum[e][3]);
+      }
+    }
+    __syncthreads();
+    const int row = threadIdx.x >> 2, j = threadIdx.x & 3, I = a.N / 2;
+    if (row >= 16 * kTT || m0 + row >= gr.count) return;  // all four threads of a row
+    const float* from = h + row * kPitch + 8 * j;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = from[i];
+    const size_t at = static_cast<size_t>(gr.first + m0 + row);
+    if (a.type == MOE_BF16) {
+      u32x4_t q;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + at * I + 32 * rb + 8 * j) = q;
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+      m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 1, kWave)));
+      m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 2, kWave)));
+      const uint32_t byte = mx_scale_byte(m);
+      const uint32_t q = mx_codes_or_zero(mx_codes(v, e8m0_scale(byte)), byte);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + at * (I / 2) + 16 * rb + 4 * j) = q;
+      if (j == 0) a.hs[at * (I / 32) + rb] = static_cast<uint8_t>(byte);
+    }
+  }
+}
+
+template <bool kGateUp>
+__global__ __launch_bounds__(64 * kFewWaves) void mx_group_few_kernel(MxGroupArgs a) {
+  __shared__ f32x4_t red[kFewWaves * kFewWaves * 64];
+  const int blocks = a.N / kRowsPerBlock;
+  const Group gr = find_group<kFewRows>(a, blockIdx.x, blocks);
+  if (gr.tile < 0) return;
+  const int tiles_m = (gr.count + kFewRows - 1) / kFewRows;
+  const int rb = gr.tile / tiles_m, m0 = gr.tile % tiles_m * kFewRows;
+  const int left = gr.count - m0;
+  if (left <= 16)
+    few_rows<1, kGateUp>(a, gr, rb, m0, red);
+  else if (left <= 32)
+    few_rows<2, kGateUp>(a, gr, rb, m0, red);
+  else
+    few_rows<4, kGateUp>(a, gr, rb, m0, red);
+}
+
+// ---------------------------------------------------------------- host
+
+// most tiles of kBM rows that R rows of n experts can make
+inline int64_t max_tiles(int64_t R, int n, int bm) {
+  const int64_t groups = n < R ? n : R;
+  return (R - groups) / bm + groups;
+}
+
+// Rows an expert has on average decide: one kernel serves every expert of a call.
+template <bool kGateUp>
+void launch_group(const moe_mx_group_dims& m, const MxGroupArgs& a, hipStream_t stream) {
+  const int64_t per = static_cast<int64_t>(m.T) * m.topk / m.E;
+  if (per <= 64) {
+    const int64_t grid = max_tiles(a.R, a.n, kFewRows) * (a.N / kRowsPerBlock);
+    mx_group_few_kernel<kGateUp><<<static_cast<unsigned>(grid), 64 * kFewWaves, 0, stream>>>(a);
+  } else {
+    const int64_t grid = max_tiles(a.R, a.n, 128) * ((a.N + 255) / 256);
+    mx_group_tile_kernel<8, 4, 2, 2, 3, kGateUp><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
+  }
+}
+
+}  // namespace
+
+int check_mx_group_dims(const moe_mx_group_dims* d) {
+  MOE_REQUIRE(d != nullptr, MOE_ERR_NULL);
+  MOE_REQUIRE(d->T >= 1 && d->T <= 262144, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->E >= 1 && d->E <= 256, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->topk >= 1 && d->topk <= 8 && d->topk <= d->E, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->n_local >= 1 && d->n_local <= kMaxGroups && d->n_local <= d->E, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->d >= 128 && d->d <= 16384 && d->d % 128 == 0, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->I >= 128 && d->I <= 8192 && d->I % 128 == 0, MOE_ERR_SHAPE);
+  MOE_REQUIRE(d->h_type == MOE_BF16 || d->h_type == MOE_MXFP4, MOE_ERR_UNSUPPORTED);
+  MOE_REQUIRE(d->out_type == MOE_BF16 || d->out_type == MOE_FP32, MOE_ERR_UNSUPPORTED);
+  return MOE_OK;
+}
+
+}  // namespace moeblk
+
+using namespace moeblk;
+
+extern "C" {
+
+int moe_check_mx_group_dims(const moe_mx_group_dims* dims) { return check_mx_group_dims(dims); }
+
+int moe_mx_gate_up(const moe_mx_group_dims* dims, const void* xq, const void* xs,
+                   const int32_t* offsets, const int32_t* rows, const void* w13_packed, void* h,
+                   void* hs, hipStream_t stream) {
+  const int rc = check_mx_group_dims(dims);
+  if (rc) return rc;
+  MOE_REQUIRE(xq && xs && offsets && rows && w13_packed && h, MOE_ERR_NULL);
+  MOE_REQUIRE(hs || dims->h_type != MOE_MXFP4, MOE_ERR_NULL);
+  MOE_REQUIRE(aligned16(xq) && aligned16(xs) && aligned16(offsets) && aligned16(rows) &&
+                  aligned16(w13_packed) && aligned16(h) && aligned16(hs),
+              MOE_ERR_ALIGN);
+  const int N = 2 * dims->I;
+  const MxGroupArgs a = {static_cast<const uint8_t*>(xq),
+                         static_cast<const uint8_t*>(xs),
+                         static_cast<const uint8_t*>(w13_packed),
+                         offsets,
+                         rows,
+                         h,
+                         static_cast<uint8_t*>(hs),
+                         dims->T,
+                         dims->T * dims->topk,
+                         dims->n_local,
+                         N,
+                         mx_chunks(dims->d),
+                         dims->h_type,
+                         mx_packed_bytes(N, dims->d)};
+  launch_group<true>(*dims, a, stream);
+  return launch_status();
+}
+
+int moe_mx_down(const moe_mx_group_dims* dims, const void* hq, const void* hs,
+                const int32_t* offsets, const void* w2_packed, void* y, hipStream_t stream) {
+  const int rc = check_mx_group_dims(dims);
+  if (rc) return rc;
+  MOE_REQUIRE(hq && hs && offsets && w2_packed && y, MOE_ERR_NULL);
+  MOE_REQUIRE(aligned16(hq) && aligned16(hs) && aligned16(offsets) && aligned16(w2_packed) &&
+                  aligned16(y),
+              MOE_ERR_ALIGN);
+  const MxGroupArgs a = {static_cast<const uint8_t*>(hq),
+                         static_cast<const uint8_t*>(hs),
+                         static_cast<const uint8_t*>(w2_packed),
+                         offsets,
+                         nullptr,
+                         y,
+                         nullptr,
+                         dims->T,
+                         dims->T * dims->topk,
+                         dims->n_local,
+                         dims->d,
+                         mx_chunks(dims->I),
+                         dims->out_type,
+                         mx_packed_bytes(dims->d, dims->I)};
+  launch_group<false>(*dims, a, stream);
+  return launch_status();
+}
+
+}  // extern "C"

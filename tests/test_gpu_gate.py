@@ -1,0 +1,218 @@
+"""GPU parity of moe_gate and moe_gate_backward against the 64-bit references of
+tests/_ref_many.py (which derives the tolerances)."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import moe_decode_layer_router_amd as mb  # noqa: E402
+from tests import _ref_many as rm  # noqa: E402
+from tests.gpu_util import to_np  # noqa: E402
+
+SCORES = {"sigmoid": mb.MOE_SCORE_SIGMOID, "softmax": mb.MOE_SCORE_SOFTMAX}
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _logits(T, E, seed, spread=1.5):
+    r = np.random.default_rng([seed, T, E])
+    l = (r.standard_normal((T, E)) * spread + 0.5 * r.standard_normal((1, E))).astype(np.float32)
+    l[::5] = np.round(l[::5] * 2) / 2  # equal logits
+    return l
+
+
+def _dims(T, E, k, score, renorm, bias_mode=0):
+    return mb.gate_dims_from(dict(T=T, E=E, topk=k, score=SCORES[score], renorm=renorm, bias_mode=bias_mode))
+
+
+def _run(l, k, score, renorm, bias=None, bias_mode=None):
+    T, E = l.shape
+    d = _dims(T, E, k, score, renorm, (bias is not None) if bias_mode is None else bias_mode)
+    ids = torch.full((T + 1, k), 77, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 1, k), 77.0, device="cuda")
+    mb.moe_gate(d, torch.from_numpy(l).cuda(), None if bias is None else torch.from_numpy(bias).cuda(), ids, w)
+    torch.cuda.synchronize()
+    ids, w = to_np(ids), to_np(w)
+    assert (ids[T] == 77).all() and (w[T] == 77).all(), "wrote behind its outputs"
+    return ids[:T], w[:T].astype(np.float64)
+
+
+def _check(l, k, score, renorm, bias=None):
+    ids, w = _run(l, k, score, renorm, bias)
+    rids, rw = rm.gate(l, bias, k, score, renorm)
+    assert np.array_equal(ids, rids)
+    assert np.array_equal(np.isnan(w), np.isnan(rw))
+    tol = rm.gate_rel(l) * np.abs(rw) + 2.0**-126
+    assert (np.abs(w - rw) <= tol)[~np.isnan(rw)].all(), np.nanmax(np.abs(w - rw) / tol)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 8), (3, 2, 2), (17, 63, 6), (16, 64, 8), (130, 65, 5), (33, 128, 8),
+                                   (77, 129, 7), (100, 255, 8), (1025, 256, 8), (5, 7, 7)])
+def test_gate(T, E, k, score, renorm):
+    l = _logits(T, E, 0)
+    _check(l, k, score, renorm)
+    _check(l, k, score, renorm, (0.5 * np.random.default_rng(1).standard_normal(E)).astype(np.float32))
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [0, 1])
+def test_gate_masks_and_extremes(score, renorm):
+    l = _logits(40, 100, 3)
+    l[0] = -np.inf  # a padded row
+    l[1, 3:] = -np.inf  # fewer experts than picks
+    l[2] = np.finfo(np.float32).min  # the type's lowest value as a mask
+    l[3, ::2] = np.finfo(np.float32).min
+    l[4] = 0.0
+    l[4, ::3] = -0.0  # equal to +0
+    l[5] = -200.0 + l[5]  # sigmoids below fp32's range
+    l[6] = 200.0 + l[6]
+    l[7, 90] = np.nan
+    l[8, 5] = -np.nan
+    l[9] = 7.25
+    l[10, 20] = np.finfo(np.float32).max
+    l[11, 1] = np.float32(1e-45)
+    l[11, 2:] = 0
+    _check(l, 8, score, renorm)
+
+
+def test_gate_infinite_logit():
+    """+inf is picked first; its sigmoid is 1."""
+    l = _logits(4, 20, 4)
+    l[1, 7] = np.inf
+    ids, w = _run(l, 3, "sigmoid", 0)
+    assert ids[1, 0] == 7 and w[1, 0] == 1.0 and np.isfinite(w).all()
+
+
+def test_gate_bias_mode_0_does_not_read_the_bias():
+    l = _logits(50, 30, 5)
+    a = _run(l, 4, "sigmoid", 1)
+    b = _run(l, 4, "sigmoid", 1, np.full(30, np.nan, np.float32), bias_mode=0)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+def test_gate_matches_moe_topk():
+    """A decode step's rows through either call."""
+    S, E, k = 128, 256, 8
+    l = _logits(S, E, 6)
+    bias = (0.3 * np.random.default_rng(7).standard_normal(E)).astype(np.float32)
+    td = mb.dims_from(dict(S=S, d=4096, E=E, topk=k, n_local=32, local_base=0, I=2048, renorm=1, eps=1e-6, shared_I=0,
+                           bias_mode=1))
+    ids = torch.empty((S, k), dtype=torch.int32, device="cuda")
+    w = torch.empty((S, k), device="cuda")
+    mb.moe_topk(td, torch.from_numpy(l).cuda(), torch.from_numpy(bias).cuda(), ids, w)
+    gids, gw = _run(l, k, "sigmoid", 1, bias)
+    assert np.array_equal(gids, to_np(ids))
+    assert np.allclose(gw, to_np(w), rtol=2e-6, atol=0)
+
+
+def _grad(l, ids, g, score, renorm, dadd=None, in_place=False):
+    T, E = l.shape
+    d = _dims(T, E, ids.shape[1], score, renorm)
+    out = torch.full((T + 1, E), 77.0, device="cuda")
+    add = None
+    if dadd is not None:
+        add = torch.from_numpy(dadd).cuda()
+        if in_place:
+            out[:T] = add
+            add = out
+    mb.moe_gate_backward(d, torch.from_numpy(l).cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(g).cuda(), add, out)
+    torch.cuda.synchronize()
+    out = to_np(out).astype(np.float64)
+    assert (out[T] == 77).all(), "wrote behind its output"
+    return out[:T]
+
+
+def _check_grad(l, ids, g, score, renorm, dadd=None, in_place=False):
+    got = _grad(l, ids, g, score, renorm, dadd, in_place)
+    want, mag = rm.gate_grad(l, ids, g, score, renorm)
+    tol = (rm.gate_rel(l) * 2 + 20 * rm.U24) * mag + 2.0**-120
+    if dadd is not None:
+        want = want + dadd
+        tol = tol + rm.U24 * 2 * np.abs(want)
+    assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / tol).max())
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 256, 8), (17, 63, 6), (130, 65, 5), (33, 128, 8), (100, 255, 8),
+                                   (1000, 256, 8)])
+def test_gate_backward(T, E, k, score, renorm):
+    l = _logits(T, E, 10)
+    r = np.random.default_rng(11)
+    ids, _ = rm.gate(l, None, k, score, renorm)
+    g = r.standard_normal((T, k)).astype(np.float32)
+    _check_grad(l, ids, g, score, renorm)
+    dadd = r.standard_normal((T, E)).astype(np.float32)
+    _check_grad(l, ids, g, score, renorm, dadd)
+    _check_grad(l, ids, g, score, renorm, dadd, in_place=True)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [0, 1])
+def test_gate_backward_masks_and_odd_picks(score, renorm):
+    """Padded rows and places (their gradients NaN), ids outside the experts, an expert
+    picked twice, picks that are not the largest, masked logits."""
+    l = _logits(12, 70, 12)
+    l[0] = -np.inf
+    l[1, 2:] = -np.inf
+    l[2] = -150.0 + l[2]
+    l[3] = np.finfo(np.float32).min
+    ids, _ = rm.gate(l, None, 6, score, renorm)
+    g = np.random.default_rng(13).standard_normal((12, 6)).astype(np.float32)
+    ids[4, 1] = ids[4, 0]
+    ids[5] = [3, 3, 3, 9, 9, 3]
+    ids[6] = [-1, 5, 70, 6, -2**31, 2**31 - 1]
+    ids[7] = -1
+    ids[8] = [69, 60, 50, 40, 30, 0]
+    g[(ids < 0) | (ids >= 70)] = np.nan
+    _check_grad(l, ids, g, score, renorm)
+
+
+def test_gate_backward_against_differences():
+    """The kernel's gradient against central differences of the reference's weights."""
+    l = _logits(6, 20, 14)
+    g = np.random.default_rng(15).standard_normal((6, 4)).astype(np.float32)
+    for score in SCORES:
+        for renorm in (0, 1):
+            ids, _ = rm.gate(l, None, 4, score, renorm)
+            got = _grad(l, ids, g, score, renorm)
+            h = 1e-5
+            for t in range(6):
+                for e in range(20):
+                    f = []
+                    for sgn in (1, -1):
+                        row = l[t].astype(np.float64)
+                        row[e] += sgn * h
+                        f.append(float(rm.pick_weights(row, ids[t], score, renorm) @ g[t]))
+                    # differences to h^2 and 2^-52 / h, the kernel to some 2^-24 of terms up to about 3
+                    assert abs((f[0] - f[1]) / (2 * h) - got[t, e]) <= 1e-5
+
+
+def test_gate_large_and_deterministic():
+    """Rows behind 2^32 bytes of logits; two runs give the same bytes."""
+    T, E, k = (1 << 22), 256, 8
+    l = torch.empty((T, E), device="cuda")
+    l.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    d = _dims(T, E, k, "sigmoid", 1)
+    ids = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    w = torch.empty((T, k), device="cuda")
+    mb.moe_gate(d, l, None, ids, w)
+    tail = slice(T - 300, T)
+    rids, rw = rm.gate(to_np(l[tail]), None, k, "sigmoid", 1)
+    assert np.array_equal(to_np(ids[tail]), rids) and np.allclose(to_np(w[tail]), rw, rtol=1e-5, atol=0)
+    g = torch.randn((T, k), device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    dl = torch.empty((T, E), device="cuda")
+    mb.moe_gate_backward(d, l, ids, g, None, dl)
+    want, mag = rm.gate_grad(to_np(l[tail]), rids, to_np(g[tail]), "sigmoid", 1)
+    assert (np.abs(to_np(dl[tail]) - want) <= (rm.gate_rel(to_np(l[tail])) * 2 + 20 * rm.U24) * mag + 1e-30).all()
+    again = torch.empty_like(w)
+    mb.moe_gate(d, l, None, ids, again)
+    assert torch.equal(w, again)
