@@ -164,61 +164,41 @@ __global__ __launch_bounds__(64 * kNW) void mx_rows_kernel(MxGemmArgs a) {
   }
 }
 
-template <int kRT, int kTT, int kWN, int kWM, int kStages>
-__global__ __launch_bounds__(64 * kWN * kWM, kRT * kTT > 32 ? 1 : 2) void mx_tile_kernel(MxGemmArgs a) {
-  constexpr int BN = 16 * kRT * kWN, BM = 16 * kTT * kWM;
-  __shared__ __attribute__((aligned(128))) uint8_t lds[mx_tile_lds<kRT, kTT, kWN, kWM, kStages>()];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int m16 = lane & 15, g = lane >> 4;
-  const int wn = wave % kWN, wm = wave / kWN;
+template <int kQ, int kT, int kWN, int kWM>
+__global__ __launch_bounds__(64 * kWN * kWM, kQ * kT * kWN * kWM > 16 ? 1 : 2) void mx_tile_kernel(MxGemmArgs a) {
+  using S = MxTileShape<kQ, kT, kWN, kWM>;
+  __shared__ __attribute__((aligned(128))) uint8_t lds[S::kLds];
+  const int wave = threadIdx.x >> 6, wn = wave % kWN, wm = wave / kWN;
   const int tiles = a.tiles_n * a.tiles_m, part = blockIdx.x / tiles;
   int tn, tm;
   mx_tile_at(mx_xcd_tile(blockIdx.x - part * tiles, tiles), a.tiles_n, a.tiles_m, tn, tm);
-  const int rows = min(BM, a.M - tm * BM);
+  const int rows = min(S::BM, a.M - tm * S::BM);
   MxTile p;
   p.w = a.w;
-  p.rb0 = tn * (BN / 64);
+  p.rb0 = tn * (S::BN / 64);
   p.row_blocks = mx_row_blocks(a.N);
-  p.xq = a.xq + static_cast<size_t>(tm) * BM * a.Kc * 64;
-  p.xs = a.xs + static_cast<size_t>(tm) * BM * a.Kc * 4;
+  p.xq = a.xq + static_cast<size_t>(tm) * S::BM * a.Kc * 64;
+  p.xs = a.xs + static_cast<size_t>(tm) * S::BM * a.Kc * 4;
   p.xq_bytes = static_cast<uint32_t>(rows) * a.Kc * 64;
   p.xs_bytes = static_cast<uint32_t>(rows) * a.Kc * 4;
   p.Kc = a.Kc;
   part_range(a.Kc, a.split.parts, part, p.c0, p.c1);
-  f32x4_t acc[kRT][kTT];
-  mx_tile_body<kRT, kTT, kWN, kWM, kStages>(p, [&](int i) { return min(i, rows - 1); }, lds, acc);
-  if constexpr (kRT * kTT <= 16) {  // the larger tiles are never split
-    f32x4_t(&v)[kRT * kTT] = reinterpret_cast<f32x4_t(&)[kRT * kTT]>(acc);
+  f32x16_t acc[kQ][kT];
+  mx_tile_body<kQ, kT, kWN, kWM>(p, [&](int i) { return min(i, rows - 1); }, lds, acc);
+  if constexpr (kQ * kT <= 4) {  // the larger tiles are never split
+    f32x4_t(&v)[4 * kQ * kT] = reinterpret_cast<f32x4_t(&)[4 * kQ * kT]>(acc);
     if (!join_parts(a.split, tm * a.tiles_n + tn, part, true, v, reinterpret_cast<int*>(lds))) return;
     __syncthreads();  // everyone has read the word of LDS
   }
-  const int n0 = tn * BN + wn * 16 * kRT, m0 = tm * BM + wm * 16 * kTT;
-  if (a.out_bf16) {
-    mx_store_bf16<kTT, 16 * kRT>(
-        lds,
-        [&](int t, uint8_t* o) {
-#pragma unroll
-          for (int r = 0; r < kRT; ++r)
-            *reinterpret_cast<u32x2_t*>(o + r * 32 + 8 * g) =
-                u32x2_t{pack_bf16x2(acc[r][t][0], acc[r][t][1]), pack_bf16x2(acc[r][t][2], acc[r][t][3])};
-        },
-        [&](int row) -> uint16_t* {
-          return m0 + row < a.M ? static_cast<uint16_t*>(a.out) + static_cast<size_t>(m0 + row) * a.N + n0
-                                : nullptr;
-        },
-        a.N - n0);
-    return;
-  }
-#pragma unroll
-  for (int t = 0; t < kTT; ++t) {
-    const int token = m0 + t * 16 + m16;
-#pragma unroll
-    for (int r = 0; r < kRT; ++r) {
-      const int n = n0 + r * 16 + 4 * g;
-      if (token < a.M) store4<true>(a.out, static_cast<size_t>(token) * a.N + n, a.N - n, acc[r][t], false);
-      __builtin_amdgcn_sched_barrier(0);  // one tile's addresses at a time
-    }
-  }
+  const int n0 = tn * S::BN + wn * 32 * kQ, m0 = tm * S::BM + wm * 32 * kT;
+  const auto row_of = [&](int row, auto type) -> decltype(type)* {
+    return m0 + row < a.M ? static_cast<decltype(type)*>(a.out) + static_cast<size_t>(m0 + row) * a.N + n0
+                          : nullptr;
+  };
+  if (a.out_bf16)
+    mx_store_tile_bf16<kQ, kT>(lds, acc, [&](int row) { return row_of(row, uint16_t()); }, a.N - n0);
+  else
+    mx_store_tile_f32<kQ, kT>(acc, [&](int row) { return row_of(row, float()); }, a.N - n0);
 }
 
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -309,9 +289,9 @@ void launch_gemm(const moe_mx_dims& m, const void* x, const uint8_t* xq, const u
                                reinterpret_cast<f32x4_t*>(ws + kSplitCounterBytes)}};
   const unsigned grid = static_cast<unsigned>(p.tiles_n) * p.tiles_m * p.parts;
   if (p.form == kTile256)
-    mx_tile_kernel<8, 8, 2, 2, 4><<<grid, 256, 0, stream>>>(a);
+    mx_tile_kernel<4, 4, 2, 2><<<grid, 256, 0, stream>>>(a);
   else if (p.form == kTile128)
-    mx_tile_kernel<4, 4, 2, 2, 4><<<grid, 256, 0, stream>>>(a);
+    mx_tile_kernel<2, 2, 2, 2><<<grid, 256, 0, stream>>>(a);
   else if (!x)
     launch_few<kMxRowsQ>(a, p, grid, stream);
   else if (m.in_type == MOE_BF16)

@@ -84,6 +84,12 @@ __device__ __forceinline__ uint32_t mx_codes_bf16(const uint32_t* w, float scale
   return q;
 }
 
+// two fp32 -> bf16 in a word, to nearest even (one instruction)
+__device__ __forceinline__ uint32_t mx_bf16x2(float lo, float hi) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
+}
+
 // silu(g) u in fp32; exp(-|g|) never overflows
 __device__ __forceinline__ float mx_swiglu(float g, float u) {
   const float e = __expf(-fabsf(g));

@@ -36,15 +36,23 @@ struct Group {
   int e, first, count, tile;  // expert, its first row and rows; the tile within it (-1: none)
 };
 
+// How an expert's rows fall into tiles of kBM: the last one takes the rest, and up to
+// kOver rows more than kBM rather than leaving them a tile of their own.
+template <int kBM, int kOver>
+__device__ __forceinline__ int row_tiles(int count) {
+  const int full = count / kBM, rest = count - full * kBM;
+  return full + (rest > (full ? kOver : 0) ? 1 : 0);
+}
+
 // Tile `t` of all experts' (tiles_n a group of kBM rows). Lane i holds expert i; offsets
 // outside the rows are taken as the nearer end.
-template <int kBM>
+template <int kBM, int kOver>
 __device__ __forceinline__ Group find_group(const MxGroupArgs& a, int b, int tiles_n) {
   const int lane = threadIdx.x & 63;
   const int o = lane <= a.n ? min(max(a.offsets[lane], 0), a.R) : 0;
   const int next = __shfl_down(o, 1, kWave);
   const int count = lane < a.n ? max(next - o, 0) : 0;
-  const int tiles = (count + kBM - 1) / kBM * tiles_n;
+  const int tiles = row_tiles<kBM, kOver>(count) * tiles_n;
   int incl = tiles;
 #pragma unroll
   for (int s = 1; s < kMaxGroups; s <<= 1) {
@@ -69,23 +77,17 @@ __device__ __forceinline__ Group find_group(const MxGroupArgs& a, int b, int til
 
 // ---------------------------------------------------------------- many rows an expert
 
-template <int kRT, int kTT, int kWN, int kWM, int kStages, bool kGateUp>
-__global__ __launch_bounds__(64 * kWN * kWM, kRT * kTT > 32 ? 1 : 2) void mx_group_tile_kernel(
-    MxGroupArgs a) {
-  constexpr int BN = 16 * kRT * kWN, BM = 16 * kTT * kWM;
-  __shared__ __attribute__((aligned(128))) uint8_t lds[mx_tile_lds<kRT, kTT, kWN, kWM, kStages>()];
+// a tile of an expert's rows: `rows` of them from `first` on, up to 32 kT kWM
+template <int kQ, int kT, int kWN, int kWM, bool kGateUp>
+__device__ __forceinline__ void group_tile(const MxGroupArgs& a, const Group& gr, int tn, int first,
+                                           int rows, uint8_t* lds) {
+  using S = MxTileShape<kQ, kT, kWN, kWM>;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int m16 = lane & 15, g = lane >> 4;
+  const int m32 = lane & 31, hi = lane >> 5;
   const int wn = wave % kWN, wm = wave / kWN;
-  const int tiles_n = (a.N + BN - 1) / BN;
-  const Group gr = find_group<BM>(a, blockIdx.x, tiles_n);
-  if (gr.tile < 0) return;
-  int tn, tm;
-  mx_tile_at(gr.tile, tiles_n, (gr.count + BM - 1) / BM, tn, tm);
-  const int first = gr.first + tm * BM, rows = min(BM, gr.count - tm * BM);
   MxTile p;
   p.w = a.w + gr.e * a.w_bytes;
-  p.rb0 = tn * (BN / 64);
+  p.rb0 = tn * (S::BN / 64);
   p.row_blocks = a.N / kRowsPerBlock;
   const size_t base = kGateUp ? 0 : first;
   const uint32_t readable = kGateUp ? a.T : rows;
@@ -96,8 +98,8 @@ __global__ __launch_bounds__(64 * kWN * kWM, kRT * kTT > 32 ? 1 : 2) void mx_gro
   p.Kc = a.Kc;
   p.c0 = 0;
   p.c1 = a.Kc;
-  f32x4_t acc[kRT][kTT];
-  mx_tile_body<kRT, kTT, kWN, kWM, kStages>(
+  f32x16_t acc[kQ][kT];
+  mx_tile_body<kQ, kT, kWN, kWM>(
       p,
       [&](int i) {
         i = min(i, rows - 1);
@@ -105,108 +107,120 @@ __global__ __launch_bounds__(64 * kWN * kWM, kRT * kTT > 32 ? 1 : 2) void mx_gro
         return i;
       },
       lds, acc);
-  const int m0 = wm * 16 * kTT;  // of this wave
+  const int m0 = wm * 32 * kT;  // of this wave
+  const auto row_of = [&](int row, auto type, int width, int col) -> decltype(type)* {
+    return m0 + row < rows
+               ? static_cast<decltype(type)*>(a.out) + static_cast<size_t>(first + m0 + row) * width + col
+               : nullptr;
+  };
   if constexpr (kGateUp) {
-    const int I = a.N / 2, i0 = (p.rb0 + wn * (kRT / 4)) * 32;  // first intermediate of this wave
+    // elements 4 j .. 4 j + 3 are (gate i, gate i + 1, up i, up i + 1) of i = 16 q + 4 j + 2 hi
+    const int I = a.N / 2, i0 = (p.rb0 + wn * (kQ / 2)) * 32;  // first intermediate of this wave
 #pragma unroll
-    for (int r = 0; r < kRT; ++r)
+    for (int q = 0; q < kQ; ++q)
 #pragma unroll
-      for (int t = 0; t < kTT; ++t) {
-        acc[r][t][0] = mx_swiglu(acc[r][t][0], acc[r][t][2]);
-        acc[r][t][1] = mx_swiglu(acc[r][t][1], acc[r][t][3]);
-      }
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[q][t][4 * j] = mx_swiglu(acc[q][t][4 * j], acc[q][t][4 * j + 2]);
+          acc[q][t][4 * j + 1] = mx_swiglu(acc[q][t][4 * j + 1], acc[q][t][4 * j + 3]);
+        }
     if (a.type == MOE_BF16) {
-      mx_store_bf16<kTT, 8 * kRT>(
+      mx_store_bf16<kT, 16 * kQ>(
           lds,
           [&](int t, uint8_t* o) {
 #pragma unroll
-            for (int r = 0; r < kRT; ++r)
-              *reinterpret_cast<uint32_t*>(o + (r >> 2) * 64 + (r & 3) * 16 + 4 * g) =
-                  pack_bf16x2(acc[r][t][0], acc[r][t][1]);
+            for (int q = 0; q < kQ; ++q)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint32_t*>(o + q * 32 + j * 8 + 4 * hi) =
+                    mx_bf16x2(acc[q][t][4 * j], acc[q][t][4 * j + 1]);
           },
-          [&](int row) -> uint16_t* {
-            return m0 + row < rows
-                       ? static_cast<uint16_t*>(a.out) + static_cast<size_t>(first + m0 + row) * I + i0
-                       : nullptr;
-          },
-          I - i0);
+          [&](int row) { return row_of(row, uint16_t(), I, i0); }, I - i0);
       return;
     }
-    // MXFP4: a block's codes meet in LDS, 16 bytes a row
-    constexpr int kB = kRT / 4;
-    uint8_t* o = lds + wave * (16 * kTT * kB * 16);
+    // MXFP4: a block is two 32-row units, 16 values of a lane and 16 of lane ^ 32; its codes
+    // meet in LDS, 16 bytes a row
+    constexpr int kB = kQ / 2;
+    uint8_t* o = lds + wave * (32 * kT * kB * 16);
 #pragma unroll
-    for (int t = 0; t < kTT; ++t) {
-      const int row = m0 + t * 16 + m16;
+    for (int t = 0; t < kT; ++t) {
+      const int row = m0 + t * 32 + m32;
 #pragma unroll
       for (int b = 0; b < kB; ++b) {
+        float v[2][8];
         uint32_t m = 0;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          m = max(m, __float_as_uint(acc[4 * b + r][t][0]) & 0x7fffffffu);
-          m = max(m, __float_as_uint(acc[4 * b + r][t][1]) & 0x7fffffffu);
+        for (int i = 0; i < 16; ++i) {
+          v[i >> 3][i & 7] = acc[2 * b + (i >> 3)][t][4 * ((i & 7) >> 1) + (i & 1)];
+          m = max(m, __float_as_uint(v[i >> 3][i & 7]) & 0x7fffffffu);
         }
-        m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16, kWave)));
         m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32, kWave)));
         const uint32_t byte = mx_scale_byte(m);
         const float s = e8m0_scale(byte);
-        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = acc[4 * b + (i >> 1)][t][i & 1];
-        const uint32_t q = mx_codes_or_zero(mx_codes(v, s), byte);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t c = mx_codes_or_zero(mx_codes(v[h], s), byte);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          o[((t * 16 + m16) * kB + b) * 16 + 4 * r + g] = static_cast<uint8_t>(q >> (8 * r));
-        if (g == 0 && row < rows && i0 + 32 * b < I)
+          for (int j = 0; j < 4; ++j)
+            o[((t * 32 + m32) * kB + b) * 16 + 8 * h + 2 * j + hi] = static_cast<uint8_t>(c >> (8 * j));
+        }
+        if (hi == 0 && row < rows && i0 + 32 * b < I)
           a.hs[static_cast<size_t>(first + row) * (I / 32) + i0 / 32 + b] = static_cast<uint8_t>(byte);
       }
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < (16 * kTT * kB + 63) / 64; ++i) {
+    for (int i = 0; i < (32 * kT * kB + 63) / 64; ++i) {
       const int at = i * 64 + lane, row = m0 + at / kB, b = at % kB;
-      if (at < 16 * kTT * kB && row < rows && i0 + 32 * b < I)
+      if (at < 32 * kT * kB && row < rows && i0 + 32 * b < I)
         *reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(a.out) +
                                     static_cast<size_t>(first + row) * (I / 2) + i0 / 2 + 16 * b) =
             *reinterpret_cast<const u32x4_t*>(o + at * 16);
     }
   } else {
-    const int n0 = tn * BN + wn * 16 * kRT;
-    if (a.type == MOE_BF16) {
-      mx_store_bf16<kTT, 16 * kRT>(
-          lds,
-          [&](int t, uint8_t* o) {
-#pragma unroll
-            for (int r = 0; r < kRT; ++r)
-              *reinterpret_cast<u32x2_t*>(o + r * 32 + 8 * g) =
-                  u32x2_t{pack_bf16x2(acc[r][t][0], acc[r][t][1]),
-                          pack_bf16x2(acc[r][t][2], acc[r][t][3])};
-          },
-          [&](int row) -> uint16_t* {
-            return m0 + row < rows
-                       ? static_cast<uint16_t*>(a.out) + static_cast<size_t>(first + m0 + row) * a.N + n0
-                       : nullptr;
-          },
-          a.N - n0);
-      return;
-    }
-#pragma unroll
-    for (int t = 0; t < kTT; ++t) {
-      const int row = m0 + t * 16 + m16;
-#pragma unroll
-      for (int r = 0; r < kRT; ++r) {
-        const int n = n0 + r * 16 + 4 * g;
-        if (row < rows)
-          store4<true>(a.out, static_cast<size_t>(first + row) * a.N + n, a.N - n, acc[r][t], false);
-        __builtin_amdgcn_sched_barrier(0);  // one tile's addresses at a time
-      }
-    }
+    const int n0 = tn * S::BN + wn * 32 * kQ;
+    if (a.type == MOE_BF16)
+      mx_store_tile_bf16<kQ, kT>(lds, acc, [&](int row) { return row_of(row, uint16_t(), a.N, n0); }, a.N - n0);
+    else
+      mx_store_tile_f32<kQ, kT>(acc, [&](int row) { return row_of(row, float(), a.N, n0); }, a.N - n0);
   }
 }
 
-// ---------------------------------------------------------------- few rows an expert
+// A tile of `rows` rows runs on the narrowest instance that holds them, in steps of 32 kWM:
+// fewer MFMAs, down to where the weights' copies are its time.
+template <int kQ, int kT, int kWN, int kWM, bool kGateUp>
+__device__ __forceinline__ void group_tile_rows(const MxGroupArgs& a, const Group& gr, int tn, int first,
+                                                int rows, uint8_t* lds) {
+  if constexpr (kT > 1) {
+    if (rows <= 32 * (kT - 1) * kWM) {
+      group_tile_rows<kQ, kT - 1, kWN, kWM, kGateUp>(a, gr, tn, first, rows, lds);
+      return;
+    }
+  }
+  group_tile<kQ, kT, kWN, kWM, kGateUp>(a, gr, tn, first, rows, lds);
+}
+
+// tiles of 32 kQ kWN weight rows x kBM rows, kBM + kOver = 32 kT kWM
+template <int kQ, int kT, int kWN, int kWM, int kOver, bool kGateUp>
+__global__ __launch_bounds__(64 * kWN * kWM, 2) void mx_group_tile_kernel(MxGroupArgs a) {
+  using S = MxTileShape<kQ, kT, kWN, kWM>;
+  constexpr int kBM = S::BM - kOver;
+  __shared__ __attribute__((aligned(128))) uint8_t lds[S::kLds];
+  const int tiles_n = (a.N + S::BN - 1) / S::BN;
+  const Group gr = find_group<kBM, kOver>(a, blockIdx.x, tiles_n);
+  if (gr.tile < 0) return;
+  const int tiles_m = row_tiles<kBM, kOver>(gr.count);
+  int tn, tm;
+  mx_tile_at(gr.tile, tiles_n, tiles_m, tn, tm);
+  const int rows = tm == tiles_m - 1 ? gr.count - tm * kBM : kBM;
+  group_tile_rows<kQ, kT, kWN, kWM, kGateUp>(a, gr, tn, gr.first + tm * kBM, rows, lds);
+}
+
+// ---------------------------------------------------------------- few rows of few experts
 //
-// A workgroup takes one row block and up to 64 rows of an expert.
+// A workgroup takes one row block and up to 64 rows of an expert, weights straight into
+// registers.
 constexpr int kFewRows = 64, kFewWaves = 8;
 
 template <int kTT, bool kGateUp>
@@ -257,7 +271,7 @@ __device__ __forceinline__ void few_rows(const MxGroupArgs& a, const Group& gr, 
     if (a.type == MOE_BF16) {
       u32x4_t q;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) q[i] = mx_bf16x2(v[2 * i], v[2 * i + 1]);
       *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.out) + at * I + 32 * rb + 8 * j) = q;
     } else {
       uint32_t m = 0;
@@ -277,7 +291,7 @@ template <bool kGateUp>
 __global__ __launch_bounds__(64 * kFewWaves) void mx_group_few_kernel(MxGroupArgs a) {
   __shared__ f32x4_t red[kFewWaves * kFewWaves * 64];
   const int blocks = a.N / kRowsPerBlock;
-  const Group gr = find_group<kFewRows>(a, blockIdx.x, blocks);
+  const Group gr = find_group<kFewRows, 0>(a, blockIdx.x, blocks);
   if (gr.tile < 0) return;
   const int tiles_m = (gr.count + kFewRows - 1) / kFewRows;
   const int rb = gr.tile / tiles_m, m0 = gr.tile % tiles_m * kFewRows;
@@ -298,16 +312,28 @@ inline int64_t max_tiles(int64_t R, int n, int bm) {
   return (R - groups) / bm + groups;
 }
 
-// Rows an expert has on average decide: one kernel serves every expert of a call.
+// One kernel serves every expert of a call; which one follows from what the host knows, the
+// rows an expert has on average (evenly popular experts) and the experts that have any.
+// Measured, us, gate_up of 4096 x 2 x 2048, 32 of 256 experts held, top-8, tiles of 128 x 128 /
+// 256 x 256: 2 rows an expert 41.0 / 43.0, 32 rows 50.6 / 53.4, 94 rows 69.3 / 73.9, 128 rows
+// 90.5 / 78.5, 256 rows 138 / 112. Few rows of few experts leave most CUs without a tile of
+// 128 weight rows; the register kernel has twice the workgroups and all of their loads in
+// flight: one expert of 1 / 16 / 100 rows, tiles / registers, 10.5 / 4.9, 10.5 / 6.2, 13.0 / 12.8;
+// seven experts of one row 14.3 / 16.6.
 template <bool kGateUp>
 void launch_group(const moe_mx_group_dims& m, const MxGroupArgs& a, hipStream_t stream) {
+  const int64_t picks = static_cast<int64_t>(m.T) * m.topk * m.n_local / m.E;  // that are local
   const int64_t per = static_cast<int64_t>(m.T) * m.topk / m.E;
-  if (per <= 64) {
+  const int64_t active = picks < 1 ? 1 : picks < m.n_local ? picks : m.n_local;
+  if (per <= kFewRows && active * (a.N / 128) <= 128) {
     const int64_t grid = max_tiles(a.R, a.n, kFewRows) * (a.N / kRowsPerBlock);
     mx_group_few_kernel<kGateUp><<<static_cast<unsigned>(grid), 64 * kFewWaves, 0, stream>>>(a);
+  } else if (per <= 96) {
+    const int64_t grid = max_tiles(a.R, a.n, 128) * (a.N / 128);
+    mx_group_tile_kernel<2, 2, 2, 2, 0, kGateUp><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
   } else {
-    const int64_t grid = max_tiles(a.R, a.n, 128) * ((a.N + 255) / 256);
-    mx_group_tile_kernel<8, 4, 2, 2, 3, kGateUp><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
+    const int64_t grid = max_tiles(a.R, a.n, 256) * ((a.N + 255) / 256);
+    mx_group_tile_kernel<2, 5, 4, 2, 64, kGateUp><<<static_cast<unsigned>(grid), 512, 0, stream>>>(a);
   }
 }
 

@@ -1,30 +1,43 @@
 // mx_tile.h -- the MXFP4 product of many rows, tiled through LDS (device code).
 //
-// A workgroup of kWN x kWM waves takes 16 kRT kWN weight rows x 16 kTT kWM rows
-// (tokens) and steps through the 128-K chunks; a wave holds kRT x kTT accumulator
-// tiles, to which the scaled MFMA adds a chunk's products directly. Both operands and
-// their scales are copied to LDS by direct loads (no registers), kStages steps in a
-// ring.
+// A workgroup of kWN x kWM waves takes 32 kQ kWN weight rows x 32 kT kWM rows
+// (tokens) and steps through the 128-K chunks; a wave holds kQ x kT accumulators of
+// 32 x 32, to which the 32x32x64 scaled MFMA adds half a chunk's products directly (alone,
+// with one wave a SIMD, it reached 6.4 PFLOP/s on random codes, the 16x16x128 one 4.5).
 //
-// Step k's unit (r, t) is one MFMA of row tile r and token tile t. The weight operand of
-// row tile r + 1 is read from LDS during row tile r; the tokens' operands stay in
-// registers for the step and are replaced by step k + 1's in the last row tile, each
-// behind its last use. One barrier a step, in front of the last row tile but one: each
-// wave has waited for its own copies of step k + 1, so behind it all of them have
-// landed, and every wave is done with step k - 1's buffer. The copies of step
-// k + kStages - 1 go there.
+// Both operands and their scales are copied to LDS by direct loads (no registers). What a
+// copy costs is the cache lines it touches, about 3.7 cycles each, whole or not (8192 x
+// 4096 x 7168 on 256 x 256 tiles, copies alone: 101 us with the tokens' scales fetched
+// chunk by chunk, 64 lines a load, and 64 bytes of a token row at a time; 69 without the
+// scales). So weights come as packed, 1 KiB pieces of 8 lines, in a ring of kWRing chunks;
+// token rows by whole lines, two chunks at once, and their scales four chunks at once, in
+// rings of two.
 //
-// Weights are copied as packed (1 KiB pieces, read back contiguously; the scales of a
-// row block are a word a lane). Of the tokens a 1 KiB piece is 16 rows' 64 bytes of the
-// chunk, the 16-byte blocks of row m permuted by block ^ (m / 2 % 4), so that the reads
-// of 8 rows at one block fall on different banks.
+// A step is one chunk: 2 kQ units of kT MFMAs, unit (h, q) being half h of the chunk and
+// 32 weight rows. Its weight operand is read from LDS two units ahead; the tokens'
+// operands of a step stay in registers, replaced by the next step's in the last two units.
+// One barrier a step, in front of those: each wave has waited for its own copies of step
+// k + 1, so behind it all of them have landed, and every wave is done with step k - 1's
+// weights and holds step k's tokens. The copies that replace those (a batch) go out from
+// there to the next barrier, one to two steps before they are needed.
+//
+// Lane (row or token l % 32, MX block l / 32 of the half). The 16-byte blocks of token
+// row m are permuted by block ^ (m / 2 % 8), so that the reads of 16 rows at one block fall
+// on different banks. Of a weight row block's scale words (a byte a row tile of 16) the
+// lane's own two bytes are shifted to places 0 and 2; so are those of a token's word (a byte a
+// block).
 #pragma once
+
+#include <type_traits>
 
 #include "mx_dev.h"
 
 namespace moeblk {
 
 typedef __attribute__((address_space(3))) void* mx_lptr_t;
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+constexpr int kWRing = 4, kXRing = 2;
 
 struct MxTile {
   const uint8_t* w;        // the matrix' tiles
@@ -41,21 +54,47 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt(0x0f70 | (n & 15) | ((n >> 4) << 14));
 }
 
-// row_of(i) gives the row (from p.xq) of the tile's token i, i < 16 kTT kWM
-template <int kRT, int kTT, int kWN, int kWM, int kStages, typename F>
+// D[32x32] += A[32x64] B[64x32]: scales from byte kA of sa, byte kB of sb. D: lane's
+// column l % 32, element i in row 8 (i / 4) + 4 (l / 32) + i % 4.
+template <int kA, int kB>
+__device__ __forceinline__ f32x16_t mfma_mx32(u32x4_t a, u32x4_t b, f32x16_t c, uint32_t sa, uint32_t sb) {
+  const i32x8_t a8 = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8_t b8 = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, kA, (int)sa, kB, (int)sb);
+}
+
+// q, h: compile-time after unrolling
+__device__ __forceinline__ f32x16_t mfma_mx32_at(int q, int h, u32x4_t a, u32x4_t b, f32x16_t c,
+                                                 uint32_t sa, uint32_t sb) {
+  if (q & 1) return h ? mfma_mx32<2, 2>(a, b, c, sa, sb) : mfma_mx32<2, 0>(a, b, c, sa, sb);
+  return h ? mfma_mx32<0, 2>(a, b, c, sa, sb) : mfma_mx32<0, 0>(a, b, c, sa, sb);
+}
+
+template <int kQ, int kT, int kWN, int kWM>
+struct MxTileShape {
+  static constexpr int kWaves = kWN * kWM;
+  static constexpr int BN = 32 * kQ * kWN, BM = 32 * kT * kWM;
+  static constexpr int kWBuf = BN * 68, kXBuf = BM * 128, kSBuf = BM * 16;  // bytes
+  static constexpr int kXAt = kWRing * kWBuf, kSAt = kXAt + kXRing * kXBuf;
+  static constexpr int kLds = kSAt + kXRing * kSBuf + 1024;
+  static_assert(kQ % 2 == 0, "whole row blocks a wave");
+  static_assert(BN / 16 % kWaves == 0 && BM / 8 % kWaves == 0, "whole pieces a wave");
+  static_assert(kLds <= 160 * 1024, "LDS");
+  // what the outputs pass through behind the last step
+  static_assert(kWaves * 32 * (32 * kQ * 2 + 16) <= kLds && kWaves * 32 * kT * (kQ / 2) * 16 <= kLds, "LDS");
+};
+
+// row_of(i) gives the row (from p.xq) of the tile's token i
+template <int kQ, int kT, int kWN, int kWM, typename F>
 __device__ __forceinline__ void mx_tile_body(const MxTile& p, F row_of, uint8_t* lds,
-                                             f32x4_t (&acc)[kRT][kTT]) {
-  constexpr int kWaves = kWN * kWM;
-  constexpr int BN = 16 * kRT * kWN, BM = 16 * kTT * kWM;
-  constexpr int kW = BN / 16 / kWaves, kX = BM / 16 / kWaves;  // 1 KiB pieces a wave copies
+                                             f32x16_t (&acc)[kQ][kT]) {
+  using S = MxTileShape<kQ, kT, kWN, kWM>;
+  constexpr int kWaves = S::kWaves, BN = S::BN, BM = S::BM;
+  constexpr int kW = BN / 16 / kWaves, kX = BM / 8 / kWaves;  // 1 KiB pieces a wave copies
   constexpr int kSW = (BN / 64 + kWaves - 1) / kWaves, kSX = (BM / 64 + kWaves - 1) / kWaves;
-  static_assert(BN / 16 % kWaves == 0 && BM / 16 % kWaves == 0, "whole pieces a wave");
-  static_assert(kRT % 4 == 0, "whole row blocks a wave");
-  constexpr int kLoads = kW + kX + kSW + kSX;
-  constexpr int kXAt = BN * 64, kSWAt = kXAt + BM * 64, kSXAt = kSWAt + BN * 4;
-  constexpr int kStage = kSXAt + BM * 4;  // bytes
+  constexpr int kUnits = 2 * kQ;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int m16 = lane & 15, g = lane >> 4;
+  const int m32 = lane & 31, hi = lane >> 5;
   const int wn = wave % kWN, wm = wave / kWN;
   const int Kc = p.Kc;
 
@@ -71,128 +110,192 @@ __device__ __forceinline__ void mx_tile_body(const MxTile& p, F row_of, uint8_t*
       const_cast<uint8_t*>(p.xs), 0, static_cast<int>(p.xs_bytes), 0x00020000);
   uint32_t xoff[kX], soff[kSX];
 #pragma unroll
-  for (int i = 0; i < kX; ++i) {
-    const int m = lane >> 2;
-    xoff[i] = static_cast<uint32_t>(row_of(16 * (wave + i * kWaves) + m)) * (Kc * 64u) +
-              ((lane & 3) ^ ((m >> 1) & 3)) * 16;
+  for (int i = 0; i < kX; ++i) {  // a piece: 8 rows' 128 bytes
+    const int m = lane >> 3;
+    xoff[i] = static_cast<uint32_t>(row_of(8 * (wave + i * kWaves) + m)) * (Kc * 64u) +
+              ((lane & 7) ^ (4 * ((wave + i * kWaves) & 1) + (m >> 1))) * 16;
   }
 #pragma unroll
-  for (int i = 0; i < kSX; ++i)  // with fewer pieces than waves some copy the same ones
-    soff[i] = static_cast<uint32_t>(row_of(64 * ((wave + i * kWaves) % (BM / 64)) + lane)) * (Kc * 4u);
-  // copy i < kLoads of chunk c into buffer s; `past`: 0, or an offset behind every buffer
-  const auto copy = [&](int i, int c, int s, uint32_t past) {
-    uint8_t* to = lds + s * kStage;
+  for (int i = 0; i < kSX; ++i)
+    soff[i] = static_cast<uint32_t>(row_of(64 * min(wave + i * kWaves, BM / 64 - 1) + lane)) * (Kc * 4u);
+  // Copies of weight chunk k, of token unit u (chunks 2 u, 2 u + 1), of scale unit v (chunks
+  // 4 v .. 4 v + 3), all counted from p.c0; behind the last chunk they read nothing (an offset
+  // behind every buffer) or what is not used.
+  constexpr uint32_t kPast = 1u << 31;
+  const int n = p.c1 - p.c0;
+  const auto copy_w = [&](int i, int k) {
+    uint8_t* to = lds + (k & (kWRing - 1)) * S::kWBuf;
+    const uint32_t past = k < n ? 0u : kPast;
+    const int c = min(p.c0 + k, Kc - 1);
     if (i < kW) {
-      const int q = wave + i * kWaves;  // piece: row tile q
+      const int q = wave + i * kWaves;  // piece: row tile of 16
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           wr, (mx_lptr_t)(to + q * 1024), 16, (lane * 16) | past,
           (min(q >> 2, blocks - 1) * Kc + c) * kMxTileBytes + (q & 3) * 1024, 0, 0);
-    } else if (i < kW + kX) {
-      const int q = wave + (i - kW) * kWaves;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (mx_lptr_t)(to + kXAt + q * 1024), 16,
-                                               xoff[i - kW] | past, c * 64, 0, 0);
-    } else if (i < kW + kX + kSW) {
-      const int q = (wave + (i - kW - kX) * kWaves) % (BN / 64);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          wr, (mx_lptr_t)(to + kSWAt + q * 256), 4, (lane * 4) | past,
-          (min(q, blocks - 1) * Kc + c) * kMxTileBytes + 4096, 0, 0);
     } else {
-      const int q = (wave + (i - kW - kX - kSW) * kWaves) % (BM / 64);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (mx_lptr_t)(to + kSXAt + q * 256), 4,
-                                               soff[i - kW - kX - kSW] | past, c * 4, 0, 0);
+      const int q = (wave + (i - kW) * kWaves) % (BN / 64);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (mx_lptr_t)(to + BN * 64 + q * 256), 4,
+                                               (lane * 4) | past,
+                                               (min(q, blocks - 1) * Kc + c) * kMxTileBytes + 4096, 0, 0);
     }
   };
-
-  // operand reads
-  const uint8_t* lw = lds + wn * kRT * 1024 + lane * 16;
-  const uint8_t* lsw = lds + kSWAt + wn * kRT * 64 + lane * 4;
-  const uint8_t* lx = lds + kXAt + wm * kTT * 1024 + m16 * 64 + ((g ^ ((m16 >> 1) & 3)) * 16);
-  const uint8_t* lsx = lds + kSXAt + (wm * kTT * 16 + m16) * 4 + g;
-  const auto read_w = [&](int s, int r) {
-    return *reinterpret_cast<const u32x4_t*>(lw + s * kStage + r * 1024);
+  const auto copy_x = [&](int i, int u) {
+    const uint32_t past = 2 * u < n ? 0u : kPast;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        xr, (mx_lptr_t)(lds + S::kXAt + (u & 1) * S::kXBuf + (wave + i * kWaves) * 1024), 16,
+        xoff[i] | past, (p.c0 + 2 * u) * 64, 0, 0);
   };
-  const auto read_sw = [&](int s, int r) {  // of row tiles r .. r + 3
-    return *reinterpret_cast<const uint32_t*>(lsw + s * kStage + r * 64);
-  };
-  const auto read_x = [&](int s, int t) {
-    return *reinterpret_cast<const u32x4_t*>(lx + s * kStage + t * 1024);
-  };
-  const auto read_sx = [&](int s, int t) {
-    return static_cast<uint32_t>(lsx[s * kStage + t * 64]);
+  const auto copy_s = [&](int i, int v, bool real = true) {  // !real: reads nothing
+    const int q = wave + i * kWaves;
+    real = real && q < BM / 64;  // with fewer pieces than waves some have none
+    const uint32_t past = 4 * v < n && real ? 0u : kPast;
+    const int at = real ? (v & 1) * S::kSBuf + q * 1024 : kXRing * S::kSBuf;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (mx_lptr_t)(lds + S::kSAt + at), 16, soff[i] | past,
+                                             (p.c0 + 4 * v) * 4, 0, 0);
   };
 
-#pragma unroll
-  for (int r = 0; r < kRT; ++r)
-#pragma unroll
-    for (int t = 0; t < kTT; ++t) acc[r][t] = f32x4_t{0, 0, 0, 0};
+  // operand reads of step k
+  const int wl = (m32 >> 4) * 1024 + (hi * 16 + (m32 & 15)) * 16;
+  const uint8_t* lw = lds + wn * kQ * 2048 + wl;
+  const uint8_t* lsw = lds + BN * 64 + wn * kQ * 128 + (hi * 16 + (m32 & 15)) * 4;
+  const int swsh = (m32 >> 4) * 8;
+  const auto read_w = [&](int k, int unit) {  // half unit / kQ, 32 rows unit % kQ
+    return *reinterpret_cast<const u32x4_t*>(lw + (k & (kWRing - 1)) * S::kWBuf + unit % kQ * 2048 +
+                                             unit / kQ * 512);
+  };
+  const auto read_sw = [&](int k, int unit) {  // of units unit, unit + 1: a row block
+    return *reinterpret_cast<const uint32_t*>(lsw + (k & (kWRing - 1)) * S::kWBuf + unit % kQ * 128 +
+                                              unit / kQ * 128);
+  };
+  const int row = wm * kT * 32 + m32;
+  const uint8_t* lx = lds + S::kXAt + row * 128;
+  const uint8_t* lsx = lds + S::kSAt + row * 16;
+  const auto read_x = [&](int k, int h, int t) {
+    const int block = 4 * (k & 1) + 2 * h + hi;
+    return *reinterpret_cast<const u32x4_t*>(lx + ((k >> 1) & 1) * S::kXBuf + t * 4096 +
+                                             (block ^ ((row >> 1) & 7)) * 16);
+  };
+  const auto read_sx = [&](int k, int t) {  // of chunks k, k + 1 (k even): a word each
+    return *reinterpret_cast<const u32x2_t*>(lsx + ((k >> 2) & 1) * S::kSBuf + t * 512 + (k & 2) * 4);
+  };
 
-  constexpr uint32_t kPast = 1u << 31;  // behind every buffer: such a copy reads nothing
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    const int c = p.c0 + s;
+  for (int q = 0; q < kQ; ++q)
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) copy(i, min(c, p.c1 - 1), s, c < p.c1 ? 0u : kPast);
-  }
-  wait_loads<(kStages - 2) * kLoads>();
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[q][t][i] = 0.0f;
+
+  // Order of the copies, oldest first: what the first step needs, then what each
+  // barrier's batch brings: at step k's weights k + 3, at odd steps token unit (k + 3) / 2,
+  // at every fourth (k % 4 = 3) scale unit (k + 5) / 4, and a copy that reads nothing at the
+  // odd ones between, so that the steps are one piece of code without branches (which the
+  // compiler would move MFMAs across). The two batches in front of step 0 are those of steps
+  // -2 and -1.
+#pragma unroll
+  for (int i = 0; i < kSX; ++i) copy_s(i, 0);
+#pragma unroll
+  for (int i = 0; i < kX; ++i) copy_x(i, 0);
+#pragma unroll
+  for (int i = 0; i < kW + kSW; ++i) copy_w(i, 0);
+  // Loads of a batch (an odd step's has the tokens' ones, in front). They go along with the
+  // kSlots MFMAs up to the next barrier: all at once, right behind a barrier, they queue and
+  // hold up the waves that issue them (8192 x 4096 x 7168: 119.6 us, spread 115.5).
+  constexpr int kEven = kW + kSW, kOddLoads = kX + kSX + kEven;
+  constexpr int kSlots = kUnits * kT;
+  const auto batch = [&](int k, auto odd, int slot) {
+    constexpr bool kOdd = decltype(odd)::value;
+    constexpr int kN = kOdd ? kOddLoads : kEven;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      if (i * kSlots / kN != slot) continue;
+      const int j = kOdd ? i - kX - kSX : i;
+      if (j >= 0)
+        copy_w(j, k + 3);
+      else if (i < kSX)
+        copy_s(i, (k + 5) >> 2, (k & 3) == 3);
+      else
+        copy_x(i - kSX, (k + 3) >> 1);
+    }
+  };
+  const std::true_type odd_step;
+  const std::false_type even_step;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) batch(-2, even_step, i);
+  // the rest of batch -1 goes along with step 0, like any other's with the step behind it
+  constexpr int kHead = 2 * kT;  // slots in front of the step's end
+  constexpr int kHeadLoads = (kHead * kOddLoads + kSlots - 1) / kSlots;
+#pragma unroll
+  for (int i = 0; i < kHead; ++i) batch(-1, odd_step, i);
+  wait_loads<kEven + kHeadLoads>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  u32x4_t w[2], x[kTT];
-  uint32_t sw[2], sw_next, sx[kTT];
+  u32x4_t w[4], x[2][kT];
+  uint32_t sw = 0, sw_raw, sx[kT];
+  u32x2_t sx_raw[kT];
   w[0] = read_w(0, 0);
-  sw[0] = read_sw(0, 0);
+  w[1] = read_w(0, 1);
+  sw_raw = read_sw(0, 0);
 #pragma unroll
-  for (int t = 0; t < kTT; ++t) {
-    x[t] = read_x(0, t);
-    sx[t] = read_sx(0, t);
+  for (int t = 0; t < kT; ++t) {
+    x[0][t] = read_x(0, 0, t);
+    x[1][t] = read_x(0, 1, t);
+    sx_raw[t] = read_sx(0, t);
   }
-  int s = 0;
-  for (int c = p.c0; c < p.c1; ++c) {
-    const int s1 = s + 1 == kStages ? 0 : s + 1, s3 = s == 0 ? kStages - 1 : s - 1;
-    const int cn = c + kStages - 1;
-    const uint32_t past = cn < p.c1 ? 0u : kPast;
+
+  // one step; kOdd: k is odd
+  const auto step = [&](int k, auto odd) {
+    constexpr bool kOdd = decltype(odd)::value;
 #pragma unroll
-    for (int r = 0; r < kRT; ++r) {
-      if (r == kRT - 2) {  // step c + 1 has landed, step c - 1's buffer is free
+    for (int u = 0; u < kUnits; ++u) {
+      if (u == kUnits - 2) {
+        // all but the batch of step k - 1 have landed: that is weights, tokens and scales of
+        // step k + 1
         asm volatile("" ::: "memory");
-        wait_loads<(kStages - 3) * kLoads>();
+        // with two units a half the step's second tokens are not in use yet: wait for them,
+        // since others may replace them behind the barrier
+        if constexpr (kQ == 2) __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+        wait_loads<kOdd ? kEven : kOddLoads>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
       }
-      __builtin_amdgcn_sched_barrier(0);
+      constexpr int kLast = kUnits - 1;
+      // operands two units ahead
+      const int un = u + 2 < kUnits ? u + 2 : u + 2 - kUnits;
+      const int kn = u + 2 < kUnits ? k : k + 1;
+      if ((u & 1) == 0) sw = sw_raw >> swsh;
 #pragma unroll
-      for (int t = 0; t < kTT; ++t) {
-        acc[r][t] = mfma_mx_row(r, w[r & 1], x[t], acc[r][t], sw[(r >> 2) & 1], sx[t]);
-        if (t == 0 && r + 1 < kRT) {
-          w[(r + 1) & 1] = read_w(s, r + 1);
-          if ((r + 1) % 4 == 0) sw[((r + 1) >> 2) & 1] = read_sw(s, r + 1);
+      for (int t = 0; t < kT; ++t) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (u == 0) sx[t] = sx_raw[t][kOdd] >> (8 * hi);
+        acc[u % kQ][t] = mfma_mx32_at(u, u / kQ, w[u & 3], x[u / kQ][t], acc[u % kQ][t], sw, sx[t]);
+        if (t == 0) {
+          w[(u + 2) & 3] = read_w(kn, un);
+          if ((u & 1) == 0) sw_raw = read_sw(kn, un);
         }
-        if (r == kRT - 1) {  // the next step's first operands
-          x[t] = read_x(s1, t);
-          sx[t] = read_sx(s1, t);
-          if (t == 0) {
-            w[0] = read_w(s1, 0);
-            sw_next = read_sw(s1, 0);
-          }
+        if (u == kLast - 1) {
+          x[0][t] = read_x(k + 1, 0, t);
+          if constexpr (kOdd) sx_raw[t] = read_sx(k + 1, t);
         }
-        const int u = (r - (kRT - 2)) * kTT + t;  // the copies go along with the last two row tiles
-        if (u >= 0) {
-#pragma unroll
-          for (int i = 0; i < kLoads; ++i)
-            if (i * (2 * kTT) / kLoads == u) copy(i, min(cn, p.c1 - 1), s3, past);
+        if (u == kLast) {
+          x[1][t] = read_x(k + 1, 1, t);
         }
-        __builtin_amdgcn_sched_barrier(0);  // units stay in order
+        // copies: of this step's batch behind its barrier, of the last one's before
+        if (u >= kLast - 1)
+          batch(k, odd, (u - (kLast - 1)) * kT + t);
+        else
+          batch(k - 1, std::integral_constant<bool, !kOdd>(), (u + 2) * kT + t);
       }
     }
-    sw[0] = sw_next;
-    s = s1;
+  };
+  int k = 0;
+  for (; k + 1 < n; k += 2) {
+    step(k, std::false_type());
+    step(k + 1, std::true_type());
   }
+  if (k < n) step(k, std::false_type());
   wait_loads<0>();  // no copy may still be on its way into LDS
   __syncthreads();  // and every wave's reads are done: the caller may use LDS
-}
-
-template <int kRT, int kTT, int kWN, int kWM, int kStages>
-constexpr int mx_tile_lds() {
-  return kStages * (16 * kRT * kWN + 16 * kTT * kWM) * 68;
 }
 
 // Workgroup b of a grid of at least `tiles` -> its tile, or -1: consecutive workgroups
@@ -212,33 +315,83 @@ __device__ __forceinline__ void mx_tile_at(int t, int tiles_n, int tiles_m, int&
   tn = in / gm;
 }
 
-// bf16 outputs through LDS (each wave its own part, rows padded by 16 bytes), so that
-// they leave as whole lines, 16 bytes a lane: kCols values a token in v(t, m16-row of the
-// lane) order; put(t, o) writes the lane's values of token tile t at its row o.
-template <int kTT, int kCols, typename Put, typename Row>
+// bf16 outputs through LDS, so that they leave as whole lines, 16 bytes a lane: kCols values
+// a token. Each wave takes its token tiles in turn through its own kMxStage bytes (rows
+// padded by 16 bytes); put(t, o) writes the lane's values of token tile t at its token's
+// place o.
+template <int kCols>
+constexpr int kMxStage = 32 * (kCols * 2 + 16);
+
+template <int kT, int kCols, typename Put, typename Row>
 __device__ __forceinline__ void mx_store_bf16(uint8_t* lds, Put put, Row row_of, int n_left) {
   typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
   constexpr int kPitch = kCols * 2 + 16, kLanes = kCols / 8;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  uint8_t* o = lds + wave * (16 * kTT * kPitch);
-#pragma unroll
-  for (int t = 0; t < kTT; ++t) put(t, o + (t * 16 + (lane & 15)) * kPitch);
-  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  uint8_t* o = lds + (threadIdx.x >> 6) * kMxStage<kCols>;
   const int c16 = lane % kLanes, left = n_left - 8 * c16;
-#pragma unroll 4
-  for (int i = 0; i < 16 * kTT * kLanes / 64; ++i) {
-    const int row = i * (64 / kLanes) + lane / kLanes;
-    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(o + row * kPitch + 16 * c16);
-    uint16_t* to = row_of(row);
-    if (!to) continue;
-    to += 8 * c16;
-    if (left >= 8) {
-      *reinterpret_cast<u32x4_any_t*>(to) = v;
-    } else {
+  const auto in_order = [] {  // a wave's LDS accesses stay in order, in the code as well
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
 #pragma unroll
-      for (int c = 0; c < 7; ++c)
-        if (c < left) to[c] = static_cast<uint16_t>(v[c >> 1] >> (16 * (c & 1)));
+  for (int t = 0; t < kT; ++t) {
+    put(t, o + (lane & 31) * kPitch);
+    in_order();
+    u32x4_t v[32 * kLanes / 64];
+#pragma unroll
+    for (int i = 0; i < 32 * kLanes / 64; ++i)
+      v[i] = *reinterpret_cast<const u32x4_t*>(o + (i * (64 / kLanes) + lane / kLanes) * kPitch + 16 * c16);
+    in_order();
+#pragma unroll
+    for (int i = 0; i < 32 * kLanes / 64; ++i) {
+      uint16_t* to = row_of(t * 32 + i * (64 / kLanes) + lane / kLanes);
+      if (!to) continue;
+      to += 8 * c16;
+      if (left >= 8) {
+        *reinterpret_cast<u32x4_any_t*>(to) = v[i];
+      } else {
+#pragma unroll
+        for (int c = 0; c < 7; ++c)
+          if (c < left) to[c] = static_cast<uint16_t>(v[i][c >> 1] >> (16 * (c & 1)));
+      }
     }
+  }
+}
+
+// a tile's outputs: this wave's weight rows from n0 on; row_of(i) gives where the outputs
+// of the wave's token i start (n0 included), or NULL
+template <int kQ, int kT, typename Row>
+__device__ __forceinline__ void mx_store_tile_bf16(uint8_t* lds, const f32x16_t (&acc)[kQ][kT], Row row_of,
+                                                   int n_left) {
+  const int hi = (threadIdx.x & 63) >> 5;
+  mx_store_bf16<kT, 32 * kQ>(
+      lds,
+      [&](int t, uint8_t* o) {
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<u32x2_t*>(o + q * 64 + j * 16 + 8 * hi) =
+                u32x2_t{mx_bf16x2(acc[q][t][4 * j], acc[q][t][4 * j + 1]),
+                        mx_bf16x2(acc[q][t][4 * j + 2], acc[q][t][4 * j + 3])};
+      },
+      row_of, n_left);
+}
+template <int kQ, int kT, typename Row>
+__device__ __forceinline__ void mx_store_tile_f32(const f32x16_t (&acc)[kQ][kT], Row row_of, int n_left) {
+  const int lane = threadIdx.x & 63, hi = lane >> 5;
+#pragma unroll
+  for (int t = 0; t < kT; ++t) {
+    float* o = row_of(t * 32 + (lane & 31));
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = q * 32 + j * 8 + 4 * hi;
+        const f32x4_t v = {acc[q][t][4 * j], acc[q][t][4 * j + 1], acc[q][t][4 * j + 2], acc[q][t][4 * j + 3]};
+        if (o) store4<true>(o, n, n_left - n, v, false);
+        __builtin_amdgcn_sched_barrier(0);  // one piece's addresses at a time
+      }
   }
 }
 

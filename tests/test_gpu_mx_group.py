@@ -82,6 +82,13 @@ CASES = [
     (500, 8, 8, 3, 384, 640, [127, 0, 500]),
     (300, 4, 4, 4, 128, 128, [128, 129, 256, 1]),
     (1000, 32, 8, 32, 512, 256, None),
+    # both tile kernels: heights on either side of each instance's, rests that join the tile in front
+    (300, 8, 1, 8, 128, 384, [1, 32, 33, 64, 65, 0, 5, 100]),
+    (800, 9, 1, 8, 384, 128, [127, 128, 129, 192, 193, 1, 0, 30]),
+    (2000, 8, 1, 8, 256, 128, [1, 64, 65, 128, 129, 192, 193, 257]),
+    (3000, 8, 1, 8, 384, 256, [256, 319, 320, 321, 0, 577, 513, 400]),
+    (4000, 2, 1, 2, 128, 384, [1025, 2112]),
+    (900, 3, 2, 3, 1152, 128, [300, 290, 310]),
 ]
 
 
