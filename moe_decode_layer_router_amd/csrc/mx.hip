@@ -142,58 +142,61 @@ struct MxGemmArgs {
   SplitK split;
 };
 
-template <int kRT, int kTT, int kNW, int kRing, int kSrc>
-__global__ __launch_bounds__(64 * kNW) void mx_rows_kernel(MxGemmArgs a) {
-  constexpr int kEach = (kRT * kTT + kNW - 1) / kNW;
-  __shared__ f32x4_t red[mx_rows_red<kRT, kTT, kNW>()];
+constexpr int kRowsWaves = 8;
+
+template <int kTT, int kSrc>
+__global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(MxGemmArgs a) {
+  __shared__ f32x4_t red[mx_rows_red<kTT, kRowsWaves>()];
   __shared__ int last;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int tiles = a.tiles_n * a.tiles_m, part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
-  const int rt0 = tile % a.tiles_n * kRT, t0 = tile / a.tiles_n * 16 * kTT;
-  MxRowsTile p = {a.w, rt0, a.Kc, 0, 0, t0, a.M};
+  const int rb = tile % a.tiles_n, t0 = tile / a.tiles_n * 16 * kTT;
+  MxRowsTile p = {a.w + static_cast<size_t>(rb) * a.Kc * kMxTileBytes, a.Kc, 0, 0, t0, a.M};
   part_range(a.Kc, a.split.parts, part, p.c0, p.c1);
-  f32x4_t sum[kEach];
-  mx_rows_body<kRT, kTT, kNW, kRing, kSrc>(p, a.x, a.K, a.xq, a.xs, [](int t) { return t; }, red, sum);
+  f32x4_t sum[1];
+  static_assert(4 * kTT <= kRowsWaves, "a tile a wave");
+  mx_rows_body<kTT, kRowsWaves, (kTT == 2 && kSrc == kMxRowsFp32 ? 1 : 2), kSrc>(p, a.x, a.K, a.xq, a.xs, [](int t) { return t; }, red, sum);
   if (!join_parts(a.split, tile, part, true, sum, &last)) return;
-#pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    const int i = e * kNW + wave, token = t0 + (i % kTT) * 16 + (lane & 15);
-    const int n0 = (rt0 + i / kTT) * 16 + 4 * (lane >> 4);
-    if (token < a.M && i < kRT * kTT)
-      store4<true>(a.out, static_cast<size_t>(token) * a.N + n0, a.N - n0, sum[e], a.out_bf16);
-  }
+  const int token = t0 + (wave % kTT) * 16 + (lane & 15), n0 = (4 * rb + wave / kTT) * 16 + 4 * (lane >> 4);
+  if (token < a.M && wave < 4 * kTT)
+    store4<true>(a.out, static_cast<size_t>(token) * a.N + n0, a.N - n0, sum[0], a.out_bf16);
 }
 
-template <int kQ, int kT, int kWN, int kWM>
-__global__ __launch_bounds__(64 * kWN * kWM, kQ * kT * kWN * kWM > 16 ? 1 : 2) void mx_tile_kernel(MxGemmArgs a) {
+// a tile of up to 32 kT kWM rows from m0 on, on the narrowest instance that holds them
+template <int kQ, int kT, int kWN, int kWM, bool kSplit>
+__device__ __forceinline__ void gemm_tile(const MxGemmArgs& a, int tn, int m0, int rows, int part, int tile,
+                                          uint8_t* lds) {
   using S = MxTileShape<kQ, kT, kWN, kWM>;
-  __shared__ __attribute__((aligned(128))) uint8_t lds[S::kLds];
+  if constexpr (kT > 1) {
+    if (rows <= 32 * (kT - 1) * kWM) {
+      gemm_tile<kQ, kT - 1, kWN, kWM, kSplit>(a, tn, m0, rows, part, tile, lds);
+      return;
+    }
+  }
   const int wave = threadIdx.x >> 6, wn = wave % kWN, wm = wave / kWN;
-  const int tiles = a.tiles_n * a.tiles_m, part = blockIdx.x / tiles;
-  int tn, tm;
-  mx_tile_at(mx_xcd_tile(blockIdx.x - part * tiles, tiles), a.tiles_n, a.tiles_m, tn, tm);
-  const int rows = min(S::BM, a.M - tm * S::BM);
   MxTile p;
   p.w = a.w;
   p.rb0 = tn * (S::BN / 64);
   p.row_blocks = mx_row_blocks(a.N);
-  p.xq = a.xq + static_cast<size_t>(tm) * S::BM * a.Kc * 64;
-  p.xs = a.xs + static_cast<size_t>(tm) * S::BM * a.Kc * 4;
+  p.xq = a.xq + static_cast<size_t>(m0) * a.Kc * 64;
+  p.xs = a.xs + static_cast<size_t>(m0) * a.Kc * 4;
   p.xq_bytes = static_cast<uint32_t>(rows) * a.Kc * 64;
   p.xs_bytes = static_cast<uint32_t>(rows) * a.Kc * 4;
   p.Kc = a.Kc;
-  part_range(a.Kc, a.split.parts, part, p.c0, p.c1);
+  p.c0 = 0;
+  p.c1 = a.Kc;
+  if constexpr (kSplit) part_range(a.Kc, a.split.parts, part, p.c0, p.c1);
   f32x16_t acc[kQ][kT];
   mx_tile_body<kQ, kT, kWN, kWM>(p, [&](int i) { return min(i, rows - 1); }, lds, acc);
-  if constexpr (kQ * kT <= 4) {  // the larger tiles are never split
+  if constexpr (kSplit) {
     f32x4_t(&v)[4 * kQ * kT] = reinterpret_cast<f32x4_t(&)[4 * kQ * kT]>(acc);
-    if (!join_parts(a.split, tm * a.tiles_n + tn, part, true, v, reinterpret_cast<int*>(lds))) return;
+    if (!join_parts(a.split, tile, part, true, v, reinterpret_cast<int*>(lds))) return;
     __syncthreads();  // everyone has read the word of LDS
   }
-  const int n0 = tn * S::BN + wn * 32 * kQ, m0 = tm * S::BM + wm * 32 * kT;
+  const int n0 = tn * S::BN + wn * 32 * kQ, w0 = wm * 32 * kT;
   const auto row_of = [&](int row, auto type) -> decltype(type)* {
-    return m0 + row < a.M ? static_cast<decltype(type)*>(a.out) + static_cast<size_t>(m0 + row) * a.N + n0
-                          : nullptr;
+    return w0 + row < rows ? static_cast<decltype(type)*>(a.out) + static_cast<size_t>(m0 + w0 + row) * a.N + n0
+                           : nullptr;
   };
   if (a.out_bf16)
     mx_store_tile_bf16<kQ, kT>(lds, acc, [&](int row) { return row_of(row, uint16_t()); }, a.N - n0);
@@ -201,8 +204,23 @@ __global__ __launch_bounds__(64 * kWN * kWM, kQ * kT * kWN * kWM > 16 ? 1 : 2) v
     mx_store_tile_f32<kQ, kT>(acc, [&](int row) { return row_of(row, float()); }, a.N - n0);
 }
 
+// tiles of 32 kQ kWN weight rows x kBM rows, kBM + kOver = 32 kT kWM: the last one takes up
+// to kOver rows more (mx_tile.h)
+template <int kQ, int kT, int kWN, int kWM, int kOver, bool kSplit>
+__global__ __launch_bounds__(64 * kWN * kWM, 2) void mx_tile_kernel(MxGemmArgs a) {
+  using S = MxTileShape<kQ, kT, kWN, kWM>;
+  constexpr int kBM = S::BM - kOver;
+  __shared__ __attribute__((aligned(128))) uint8_t lds[S::kLds];
+  const int tiles = a.tiles_n * a.tiles_m, part = kSplit ? blockIdx.x / tiles : 0;
+  int tn, tm;
+  mx_tile_at(mx_xcd_tile(blockIdx.x - part * tiles, tiles), a.tiles_n, a.tiles_m, tn, tm);
+  const int m0 = tm * kBM, rows = tm == a.tiles_m - 1 ? a.M - m0 : kBM;
+  gemm_tile<kQ, kT, kWN, kWM, kSplit>(a, tn, m0, rows, part, tm * a.tiles_n + tn, lds);
+}
+
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// K parts that bring the workgroups to the number of CUs, each with at least `least` chunks
 int split_parts(int tiles, int Kc, int least) {
   if (tiles > kSplitTiles) return 1;
   int p = 256 / tiles;
@@ -210,12 +228,24 @@ int split_parts(int tiles, int Kc, int least) {
   return p < 1 ? 1 : p;
 }
 
-// How a product of these sizes runs: the kernel (rows: row tiles and token tiles a
-// workgroup), and its K parts.
-enum Form { kRows1, kRows2, kRows4, kTile128, kTile256 };
+// How a product of these sizes runs: the kernel, and its K parts. Measured, us, the product
+// alone; (p): K parts.
+//
+// Up to 32 rows registers (mx_rows.h, which quantise the rows as well), beyond tiles in
+// LDS: N = 4096, K = 7168, registers (4) / tiles of 64 x 64 (4): M = 16 6.9 / 10.0, M = 32
+// 8.4 / 10.2, M = 64 12.6 / 10.2. Parts cost about 2 us to add up: M = 1 9.8 (1), 8.6 (2), 8.2
+// (4); M = 1, N = 7168, K = 2048 5.3 (1), 6.7 (2); M = 8, N = 1024, K = 4096 7.8 (1), 6.3 (4).
+//
+// Tiles of 64 x 64 (four workgroups a CU) while they are at most 512, of 128 x 128 (two) or
+// 256 x 256 (one, its last row tile up to 320 rows) beyond, by rounds over the CUs. 64 / 128 /
+// 256: M = 128, N = 7168, K = 2048 6.2 / 7.7 / 9.9; M = 512, N = 4096, K = 7168 18.4 / 18.9 /
+// 37; M = 1024 - / 26 / 39, M = 2048 - / 41 / 45, M = 4096 - / 78 / 62, M = 8192 - / 147 / 117;
+// 3000 x 3000 x 3000 - / 26 / 24. K parts of 64 x 64 tiles: M = 64, N = 4096, K = 7168 13.2 (1),
+// 10.9 (2), 10.2 (4); M = 128, N = 512, K = 8192 14.4 (1), 9.1 (4), 9.7 (8); M = 40, N = 256, K =
+// 2048 5.8 (1), 6.6 (2).
+enum Form { kRows16, kRows32, kTile64, kTile128, kTile256 };
 struct Plan {
   Form form;
-  int rt;     // row tiles a workgroup (kRows*)
   int tiles_n, tiles_m, parts;
   size_t part_bytes;  // fp32 sums of one part of one tile
 };
@@ -223,30 +253,31 @@ struct Plan {
 Plan mx_plan(const moe_mx_dims& m) {
   const int Kc = mx_chunks(m.K);
   Plan p;
-  if (m.M <= 64 || ceil_div(m.N, 64) * ceil_div(m.M, 64) <= 256) {
-    const int tt = m.M <= 16 ? 1 : m.M <= 32 ? 2 : 4;
-    p.form = tt == 1 ? kRows1 : tt == 2 ? kRows2 : kRows4;
-    p.tiles_m = ceil_div(m.M, 16 * tt);
-    p.rt = tt == 1 ? (m.N <= 8192 ? 1 : 4) : ceil_div(m.N, 32) * p.tiles_m <= 256 ? 2 : 4;
-    p.tiles_n = ceil_div(m.N, 16 * p.rt);
-    p.parts = split_parts(p.tiles_n * p.tiles_m, Kc, tt == 1 ? 16 : 8);
-    p.part_bytes = 2 * 512 * 16;
+  p.parts = 1;
+  p.part_bytes = 0;
+  if (m.M <= 32) {
+    p.form = m.M <= 16 ? kRows16 : kRows32;
+    p.tiles_m = 1;
+    p.tiles_n = mx_row_blocks(m.N);
+    p.parts = split_parts(p.tiles_n, Kc, Kc >= 32 ? 8 : 16);
+    p.part_bytes = 64 * kRowsWaves * 16;
     return p;
   }
-  const size_t t256 = static_cast<size_t>(ceil_div(m.N, 256)) * ceil_div(m.M, 256);
-  if (t256 >= 256) {
-    p.form = kTile256;
-    p.tiles_n = ceil_div(m.N, 256);
-    p.tiles_m = ceil_div(m.M, 256);
-    p.parts = 1;
-  } else {
-    p.form = kTile128;
-    p.tiles_n = ceil_div(m.N, 128);
-    p.tiles_m = ceil_div(m.M, 128);
-    p.parts = split_parts(p.tiles_n * p.tiles_m, Kc, 8);
+  const auto tiles = [&](Form form, int tn, int tm) {
+    p.form = form;
+    p.tiles_n = tn;
+    p.tiles_m = tm;
+    return static_cast<size_t>(tn) * tm;
+  };
+  if (tiles(kTile64, mx_row_blocks(m.N), mx_row_tiles<64, 0>(m.M)) <= 512) {
+    p.parts = split_parts(p.tiles_n * p.tiles_m, Kc, 12);
+    p.part_bytes = 8 * 128 * 16;
+    return p;
   }
-  p.part_bytes = 16 * 256 * 16;
-  return p;
+  const size_t r128 = (tiles(kTile128, ceil_div(m.N, 128), mx_row_tiles<128, 0>(m.M)) + 511) / 512;
+  const Plan small = p;
+  const size_t r256 = (tiles(kTile256, ceil_div(m.N, 256), mx_row_tiles<256, 64>(m.M)) + 255) / 256;
+  return r128 * 66 <= r256 * 100 ? small : p;
 }
 
 size_t gemm_workspace(const moe_mx_dims& m) {
@@ -256,19 +287,16 @@ size_t gemm_workspace(const moe_mx_dims& m) {
 }
 
 template <int kSrc>
-void launch_few(const MxGemmArgs& a, const Plan& p, unsigned grid, hipStream_t stream) {
-  const auto launch = [&](auto kernel) { kernel<<<grid, 512, 0, stream>>>(a); };
-  if (p.form == kRows1) {
-    p.rt == 1 ? launch(mx_rows_kernel<1, 1, 8, 4, kSrc>) : launch(mx_rows_kernel<4, 1, 8, 2, kSrc>);
-  } else if constexpr (kSrc == kMxRowsQ) {
-    if (p.form == kRows2)
-      p.rt == 2 ? launch(mx_rows_kernel<2, 2, 8, 4, kSrc>) : launch(mx_rows_kernel<4, 2, 8, 2, kSrc>);
-    else
-      p.rt == 2 ? launch(mx_rows_kernel<2, 4, 8, 3, kSrc>) : launch(mx_rows_kernel<4, 4, 8, 2, kSrc>);
-  }
+void launch_rows(const MxGemmArgs& a, const Plan& p, unsigned grid, hipStream_t stream) {
+  if (p.form == kRows16)
+    mx_rows_kernel<1, kSrc><<<grid, 64 * kRowsWaves, 0, stream>>>(a);
+  else
+    mx_rows_kernel<2, kSrc><<<grid, 64 * kRowsWaves, 0, stream>>>(a);
 }
 
-// x: the rows themselves (at most 16), else NULL
+inline bool takes_rows(const Plan& p) { return p.form == kRows16 || p.form == kRows32; }
+
+// x: the rows themselves (where the kernel takes them), else NULL
 void launch_gemm(const moe_mx_dims& m, const void* x, const uint8_t* xq, const uint8_t* xs,
                  const void* packed, void* out, void* workspace, hipStream_t stream) {
   const Plan p = mx_plan(m);
@@ -289,15 +317,17 @@ void launch_gemm(const moe_mx_dims& m, const void* x, const uint8_t* xq, const u
                                reinterpret_cast<f32x4_t*>(ws + kSplitCounterBytes)}};
   const unsigned grid = static_cast<unsigned>(p.tiles_n) * p.tiles_m * p.parts;
   if (p.form == kTile256)
-    mx_tile_kernel<4, 4, 2, 2><<<grid, 256, 0, stream>>>(a);
+    mx_tile_kernel<2, 5, 4, 2, 64, false><<<grid, 512, 0, stream>>>(a);
   else if (p.form == kTile128)
-    mx_tile_kernel<2, 2, 2, 2><<<grid, 256, 0, stream>>>(a);
+    mx_tile_kernel<2, 2, 2, 2, 0, false><<<grid, 256, 0, stream>>>(a);
+  else if (p.form == kTile64)
+    mx_tile_kernel<2, 1, 1, 2, 0, true><<<grid, 128, 0, stream>>>(a);
   else if (!x)
-    launch_few<kMxRowsQ>(a, p, grid, stream);
+    launch_rows<kMxRowsQ>(a, p, grid, stream);
   else if (m.in_type == MOE_BF16)
-    launch_few<kMxRowsBf16>(a, p, grid, stream);
+    launch_rows<kMxRowsBf16>(a, p, grid, stream);
   else
-    launch_few<kMxRowsFp32>(a, p, grid, stream);
+    launch_rows<kMxRowsFp32>(a, p, grid, stream);
 }
 
 size_t codes_bytes(const moe_mx_dims& m) {
@@ -410,7 +440,7 @@ int moe_mx_proj(const moe_mx_dims* dims, const void* x, const void* w_packed, vo
   MOE_REQUIRE(aligned16(x) && aligned16(w_packed) && aligned16(out) && aligned16(workspace),
               MOE_ERR_ALIGN);
   MOE_REQUIRE(workspace_bytes >= moe_mx_proj_workspace_bytes(dims), MOE_ERR_WORKSPACE);
-  if (mx_plan(*dims).form == kRows1) {
+  if (takes_rows(mx_plan(*dims))) {
     launch_gemm(*dims, x, nullptr, nullptr, w_packed, out, workspace, stream);
   } else {
     uint8_t* q = static_cast<uint8_t*>(workspace) + gemm_workspace(*dims);

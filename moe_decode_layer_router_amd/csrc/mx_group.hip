@@ -36,14 +36,6 @@ struct Group {
   int e, first, count, tile;  // expert, its first row and rows; the tile within it (-1: none)
 };
 
-// How an expert's rows fall into tiles of kBM: the last one takes the rest, and up to
-// kOver rows more than kBM rather than leaving them a tile of their own.
-template <int kBM, int kOver>
-__device__ __forceinline__ int row_tiles(int count) {
-  const int full = count / kBM, rest = count - full * kBM;
-  return full + (rest > (full ? kOver : 0) ? 1 : 0);
-}
-
 // Tile `t` of all experts' (tiles_n a group of kBM rows). Lane i holds expert i; offsets
 // outside the rows are taken as the nearer end.
 template <int kBM, int kOver>
@@ -52,7 +44,7 @@ __device__ __forceinline__ Group find_group(const MxGroupArgs& a, int b, int til
   const int o = lane <= a.n ? min(max(a.offsets[lane], 0), a.R) : 0;
   const int next = __shfl_down(o, 1, kWave);
   const int count = lane < a.n ? max(next - o, 0) : 0;
-  const int tiles = row_tiles<kBM, kOver>(count) * tiles_n;
+  const int tiles = mx_row_tiles<kBM, kOver>(count) * tiles_n;
   int incl = tiles;
 #pragma unroll
   for (int s = 1; s < kMaxGroups; s <<= 1) {
@@ -210,7 +202,7 @@ __global__ __launch_bounds__(64 * kWN * kWM, 2) void mx_group_tile_kernel(MxGrou
   const int tiles_n = (a.N + S::BN - 1) / S::BN;
   const Group gr = find_group<kBM, kOver>(a, blockIdx.x, tiles_n);
   if (gr.tile < 0) return;
-  const int tiles_m = row_tiles<kBM, kOver>(gr.count);
+  const int tiles_m = mx_row_tiles<kBM, kOver>(gr.count);
   int tn, tm;
   mx_tile_at(gr.tile, tiles_n, tiles_m, tn, tm);
   const int rows = tm == tiles_m - 1 ? gr.count - tm * kBM : kBM;
@@ -219,18 +211,24 @@ __global__ __launch_bounds__(64 * kWN * kWM, 2) void mx_group_tile_kernel(MxGrou
 
 // ---------------------------------------------------------------- few rows of few experts
 //
-// A workgroup takes one row block and up to 64 rows of an expert, weights straight into
-// registers.
-constexpr int kFewRows = 64, kFewWaves = 8;
+// A workgroup takes one row block and 16 rows of an expert, weights straight into registers
+// (mx_rows.h).
+constexpr int kFewRows = 16, kFewWaves = 8;
 
-template <int kTT, bool kGateUp>
-__device__ __forceinline__ void few_rows(const MxGroupArgs& a, const Group& gr, int rb, int m0, f32x4_t* red) {
-  constexpr int kEach = (4 * kTT + kFewWaves - 1) / kFewWaves;
+template <bool kGateUp>
+__global__ __launch_bounds__(64 * kFewWaves) void mx_group_few_kernel(MxGroupArgs a) {
+  __shared__ f32x4_t red[mx_rows_red<1, kFewWaves>()];
+  const int blocks = a.N / kRowsPerBlock;
+  const Group gr = find_group<kFewRows, 0>(a, blockIdx.x, blocks);
+  if (gr.tile < 0) return;
+  const int tiles_m = mx_row_tiles<kFewRows, 0>(gr.count);
+  const int rb = gr.tile / tiles_m, m0 = gr.tile % tiles_m * kFewRows;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int m16 = lane & 15, g = lane >> 4;
-  const MxRowsTile p = {a.w + gr.e * a.w_bytes, 4 * rb, a.Kc, 0, a.Kc, m0, gr.count};
-  f32x4_t sum[kEach];
-  mx_rows_body<4, kTT, kFewWaves, 2, kMxRowsQ>(
+  const MxRowsTile p = {a.w + gr.e * a.w_bytes + static_cast<size_t>(rb) * a.Kc * kMxTileBytes, a.Kc, 0, a.Kc,
+                        m0, gr.count};
+  f32x4_t sum[1];  // waves 0 .. 3: of row tile `wave`
+  mx_rows_body<1, kFewWaves, 2, kMxRowsQ>(
       p, nullptr, 0, a.xq, a.xs,
       [&](int i) {
         if constexpr (kGateUp) return min(max(a.rows[gr.first + i], 0), a.T - 1);
@@ -238,31 +236,22 @@ __device__ __forceinline__ void few_rows(const MxGroupArgs& a, const Group& gr, 
       },
       red, sum);
   if constexpr (!kGateUp) {
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int i = e * kFewWaves + wave, row = m0 + (i % kTT) * 16 + m16;
-      const int n = (4 * rb + i / kTT) * 16 + 4 * g;
-      if (row < gr.count && i < 4 * kTT)
-        store4<true>(a.out, static_cast<size_t>(gr.first + row) * a.N + n, a.N - n, sum[e],
-                     a.type == MOE_BF16);
-    }
+    const int row = m0 + m16, n = (4 * rb + wave) * 16 + 4 * g;
+    if (wave < 4 && row < gr.count)
+      store4<true>(a.out, static_cast<size_t>(gr.first + row) * a.N + n, a.N - n, sum[0], a.type == MOE_BF16);
   } else {
     // the 32 intermediates of a row meet in LDS; then 4 threads a row, 8 values each
     constexpr int kPitch = 36;
     float* h = reinterpret_cast<float*>(red);
     __syncthreads();  // the sums have been read
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int i = e * kFewWaves + wave;
-      if (i < 4 * kTT) {
-        float* to = h + ((i % kTT) * 16 + m16) * kPitch + 8 * (i / kTT) + 2 * g;
-        to[0] = mx_swiglu(sum[e][0], sum[e][2]);
-        to[1] = mx_swiglu(sum[e][1], sum[e][3]);
-      }
+    if (wave < 4) {
+      float* to = h + m16 * kPitch + 8 * wave + 2 * g;
+      to[0] = mx_swiglu(sum[0][0], sum[0][2]);
+      to[1] = mx_swiglu(sum[0][1], sum[0][3]);
     }
     __syncthreads();
     const int row = threadIdx.x >> 2, j = threadIdx.x & 3, I = a.N / 2;
-    if (row >= 16 * kTT || m0 + row >= gr.count) return;  // all four threads of a row
+    if (row >= kFewRows || m0 + row >= gr.count) return;  // all four threads of a row
     const float* from = h + row * kPitch + 8 * j;
     float v[8];
 #pragma unroll
@@ -287,23 +276,6 @@ __device__ __forceinline__ void few_rows(const MxGroupArgs& a, const Group& gr, 
   }
 }
 
-template <bool kGateUp>
-__global__ __launch_bounds__(64 * kFewWaves) void mx_group_few_kernel(MxGroupArgs a) {
-  __shared__ f32x4_t red[kFewWaves * kFewWaves * 64];
-  const int blocks = a.N / kRowsPerBlock;
-  const Group gr = find_group<kFewRows, 0>(a, blockIdx.x, blocks);
-  if (gr.tile < 0) return;
-  const int tiles_m = (gr.count + kFewRows - 1) / kFewRows;
-  const int rb = gr.tile / tiles_m, m0 = gr.tile % tiles_m * kFewRows;
-  const int left = gr.count - m0;
-  if (left <= 16)
-    few_rows<1, kGateUp>(a, gr, rb, m0, red);
-  else if (left <= 32)
-    few_rows<2, kGateUp>(a, gr, rb, m0, red);
-  else
-    few_rows<4, kGateUp>(a, gr, rb, m0, red);
-}
-
 // ---------------------------------------------------------------- host
 
 // most tiles of kBM rows that R rows of n experts can make
@@ -315,26 +287,29 @@ inline int64_t max_tiles(int64_t R, int n, int bm) {
 // One kernel serves every expert of a call; which one follows from what the host knows, the
 // rows an expert has on average (evenly popular experts) and the experts that have any.
 // Measured, us, gate_up of 4096 x 2 x 2048, 32 of 256 experts held, top-8, tiles of 128 x 128 /
-// 256 x 256: 2 rows an expert 41.0 / 43.0, 32 rows 50.6 / 53.4, 94 rows 69.3 / 73.9, 128 rows
-// 90.5 / 78.5, 256 rows 138 / 112. Few rows of few experts leave most CUs without a tile of
-// 128 weight rows; the register kernel has twice the workgroups and all of their loads in
-// flight: one expert of 1 / 16 / 100 rows, tiles / registers, 10.5 / 4.9, 10.5 / 6.2, 13.0 / 12.8;
-// seven experts of one row 14.3 / 16.6.
+// 256 x 256: 2 rows an expert 41.5 / 42.6, 16 rows 50.5 / 48.1, 32 rows 55 / 50, 64 rows 73 / 56,
+// 256 rows - / 105.
+// Few experts leave most CUs without a tile: there tiles of 64 x 64, and for up to 16 rows
+// the register kernel, which splits K over its waves. One expert, 128 x 128 / 64 x 64 /
+// registers: 1 row 10.3 / 9.5 / 4.9, 16 rows 10.4 / 9.6 / 6.1, 64 rows 10.6 / 9.7 / 12.5, 100
+// rows 12.9 / 9.7 / 12.5; seven experts of one row 14.2 / 15.3 / 16.6.
 template <bool kGateUp>
 void launch_group(const moe_mx_group_dims& m, const MxGroupArgs& a, hipStream_t stream) {
   const int64_t picks = static_cast<int64_t>(m.T) * m.topk * m.n_local / m.E;  // that are local
   const int64_t per = static_cast<int64_t>(m.T) * m.topk / m.E;
   const int64_t active = picks < 1 ? 1 : picks < m.n_local ? picks : m.n_local;
-  if (per <= kFewRows && active * (a.N / 128) <= 128) {
-    const int64_t grid = max_tiles(a.R, a.n, kFewRows) * (a.N / kRowsPerBlock);
-    mx_group_few_kernel<kGateUp><<<static_cast<unsigned>(grid), 64 * kFewWaves, 0, stream>>>(a);
-  } else if (per <= 96) {
-    const int64_t grid = max_tiles(a.R, a.n, 128) * (a.N / 128);
-    mx_group_tile_kernel<2, 2, 2, 2, 0, kGateUp><<<static_cast<unsigned>(grid), 256, 0, stream>>>(a);
-  } else {
-    const int64_t grid = max_tiles(a.R, a.n, 256) * ((a.N + 255) / 256);
-    mx_group_tile_kernel<2, 5, 4, 2, 64, kGateUp><<<static_cast<unsigned>(grid), 512, 0, stream>>>(a);
-  }
+  const auto grid = [&](int bm, int bn) {
+    return static_cast<unsigned>(max_tiles(a.R, a.n, bm) * ((a.N + bn - 1) / bn));
+  };
+  const int64_t blocks = active * (a.N / kRowsPerBlock);
+  if (blocks <= 256 && per <= kFewRows)
+    mx_group_few_kernel<kGateUp><<<grid(kFewRows, 64), 64 * kFewWaves, 0, stream>>>(a);
+  else if (blocks * ((per + 63) / 64) <= 256)
+    mx_group_tile_kernel<2, 1, 1, 2, 0, kGateUp><<<grid(64, 64), 128, 0, stream>>>(a);
+  else if (per < 12)
+    mx_group_tile_kernel<2, 2, 2, 2, 0, kGateUp><<<grid(128, 128), 256, 0, stream>>>(a);
+  else
+    mx_group_tile_kernel<2, 5, 4, 2, 64, kGateUp><<<grid(256, 256), 512, 0, stream>>>(a);
 }
 
 }  // namespace

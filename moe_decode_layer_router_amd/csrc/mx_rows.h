@@ -1,14 +1,14 @@
 // mx_rows.h -- the MXFP4 product of few rows: weights straight into registers
 // (device code).
 //
-// A workgroup takes 16 kRT weight rows x 16 kTT rows (tokens); its kNW waves take
-// every kNW-th 128-K chunk of the workgroup's part, kRing chunks' loads in flight
-// each. The waves' sums are added through LDS in wave order. The weights are read once
-// per group of tokens, and their bytes bound the call.
+// A workgroup takes a block of 64 weight rows x 16 kTT rows (tokens); its kNW waves take
+// every kNW-th 128-K chunk of the workgroup's part, kRing chunks' loads in flight each. The
+// waves' sums are added through LDS in wave order. The weights are read once per group of
+// tokens, and their bytes bound the call.
 //
-// kSrc: quantised rows, or (up to 16 rows) the rows themselves: a lane holds one
-// MX block of its token, 32 adjacent columns, so it quantises them by itself, without
-// a launch in front and with the values moe_mx_quant gives.
+// kSrc: quantised rows, or the rows themselves: a lane holds one MX block of its token, 32
+// adjacent columns, so it quantises them by itself, without a launch in front and with the
+// values moe_mx_quant gives.
 #pragma once
 
 #include "mx_dev.h"
@@ -29,33 +29,35 @@ struct MxRaw {
 
 template <int kSrc>
 __device__ __forceinline__ void mx_load_raw(const void* row, int c0, int left, MxRaw<kSrc>& v) {
-  constexpr int kPer = kSrc == kMxRowsFp32 ? 4 : 8;  // columns 16 bytes hold
+  constexpr bool kF32 = kSrc == kMxRowsFp32;
+  constexpr int kPer = kF32 ? 4 : 8;  // columns 16 bytes hold
+  const uint8_t* p = static_cast<const uint8_t*>(row) + static_cast<size_t>(c0) * (kF32 ? 4 : 2);
 #pragma unroll
   for (int i = 0; i < MxRaw<kSrc>::kWords / 4; ++i) {
     u32x4_t q = {0, 0, 0, 0};
-    const int c = kPer * i;
-    if constexpr (kSrc == kMxRowsFp32) {
-      const float* p = static_cast<const float*>(row) + c0 + c;
-      if (c + kPer <= left) {
-        q = *reinterpret_cast<const mx_u32x4_any_t*>(p);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-          if (c + j < left) q[j] = __float_as_uint(p[j]);
-      }
-    } else {
-      const uint16_t* p = static_cast<const uint16_t*>(row) + c0 + c;
-      if (c + kPer <= left) {
-        q = *reinterpret_cast<const mx_u32x4_any_t*>(p);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 7; ++j)
-          if (c + j < left) q[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
-      }
-    }
+    if (kPer * (i + 1) <= left) q = *reinterpret_cast<const mx_u32x4_any_t*>(p + 16 * i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v.w[4 * i + j] = q[j];
   }
+  if (left <= 0 || left >= 32 || left % kPer == 0) return;
+  // the row ends inside 16 bytes: their columns one by one, the last one in the place of
+  // those behind it (all loads at once, none outside the row), which are then cleared
+  const int first = left / kPer * kPer;
+  uint32_t t[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int c = min(first + j, left - 1);
+    t[j] = kF32 ? reinterpret_cast<const uint32_t*>(p)[c] : reinterpret_cast<const uint16_t*>(p)[c];
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) t[j] = first + j < left ? t[j] : 0u;
+#pragma unroll
+  for (int i = 0; i < MxRaw<kSrc>::kWords / 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = kF32 ? t[j] : t[2 * j % kPer] | (t[(2 * j + 1) % kPer] << 16);
+      v.w[4 * i + j] = first == kPer * i ? w : v.w[4 * i + j];
+    }
 }
 
 // a block's 32 codes, and its scale byte
@@ -94,60 +96,58 @@ __device__ __forceinline__ u32x4_t mx_quant32(const MxRaw<kSrc>& v, uint32_t& by
   return q;
 }
 
-// What a workgroup multiplies: chunks [c0, c1) of 16 kRT weight rows (from row tile
-// rt0 of the matrix at w on) and of tokens t0 .. t0 + 16 kTT - 1 of M.
+// What a workgroup multiplies: chunks [c0, c1) of the row block whose first tile is at w, and
+// of tokens t0 .. t0 + 16 kTT - 1 of M.
 struct MxRowsTile {
   const uint8_t* w;
-  int rt0, Kc, c0, c1;
+  int Kc, c0, c1;
   int t0, M;
 };
 
-template <int kRT, int kTT, int kNW>
+template <int kTT, int kNW>
 constexpr int mx_rows_red() {
-  return kNW * (kRT * kTT < kNW ? kRT * kTT : kNW) * 64;
+  return kNW * (4 * kTT < kNW ? 4 * kTT : kNW) * 64;
 }
 
-// sum[e]: of tile i = kNW e + wave, i < kRT kTT: row tile i / kTT, token tile i % kTT.
-// red: mx_rows_red elements. row_of(token) gives a token's row of x.
-template <int kRT, int kTT, int kNW, int kRing, int kSrc, typename F>
+// sum[e]: of tile i = kNW e + wave, i < 4 kTT: row tile i / kTT, token tile i % kTT. red:
+// mx_rows_red elements. row_of(token) gives a token's row of x.
+template <int kTT, int kNW, int kRing, int kSrc, typename F>
 __device__ __forceinline__ void mx_rows_body(const MxRowsTile& p, const void* x, int K,
                                              const uint8_t* xq, const uint8_t* xs, F row_of,
-                                             f32x4_t* red, f32x4_t (&sum)[(kRT * kTT + kNW - 1) / kNW]) {
-  static_assert(kRT == 1 || kRT == 2 || kRT == 4, "row tiles of one row block");
-  static_assert(kSrc == kMxRowsQ || kTT == 1, "at most 16 rows are quantised here");
+                                             f32x4_t* red, f32x4_t (&sum)[(4 * kTT + kNW - 1) / kNW]) {
+  constexpr int kRT = 4;
+  constexpr bool kRaw = kSrc != kMxRowsQ;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int m16 = lane & 15, g = lane >> 4;
-  const int Kc = p.Kc, r0 = p.rt0 & 3;
-  const uint8_t* wt = p.w + static_cast<size_t>(p.rt0 >> 2) * Kc * kMxTileBytes;
+  const int Kc = p.Kc;
   const uint8_t *xp[kTT], *sp[kTT];
-  const void* raw = nullptr;
 #pragma unroll
   for (int t = 0; t < kTT; ++t) {
     const size_t row = row_of(min(p.t0 + 16 * t + m16, p.M - 1));
-    if constexpr (kSrc == kMxRowsQ) {
+    if constexpr (kRaw) {
+      xp[t] = static_cast<const uint8_t*>(x) + row * K * (kSrc == kMxRowsFp32 ? 4 : 2);
+    } else {
       xp[t] = xq + row * (static_cast<size_t>(Kc) * 64) + 16 * g;
       sp[t] = xs + row * (static_cast<size_t>(Kc) * 4) + g;
-    } else {
-      raw = static_cast<const uint8_t*>(x) + row * K * (kSrc == kMxRowsFp32 ? 4 : 2);
     }
   }
-  u32x4_t w[kRing][kRT], b[kRing][kTT];
-  uint32_t sw[kRing], sb[kRing][kTT];
-  MxRaw<kSrc> v[kSrc == kMxRowsQ ? 1 : kRing];
+  u32x4_t w[kRing][kRT], b[kRaw ? 1 : kRing][kTT];
+  uint32_t sw[kRing], sb[kRaw ? 1 : kRing][kTT];
+  MxRaw<kSrc> v[kRaw ? kRing : 1][kRaw ? kTT : 1];
   const auto load = [&](int i, int c) {
-    const uint8_t* t = wt + static_cast<size_t>(c) * kMxTileBytes;
+    const uint8_t* t = p.w + static_cast<size_t>(c) * kMxTileBytes;
 #pragma unroll
-    for (int r = 0; r < kRT; ++r) w[i][r] = ld_nt<u32x4_t>(t + (r0 + r) * 1024 + lane * 16);
+    for (int r = 0; r < kRT; ++r) w[i][r] = ld_nt<u32x4_t>(t + r * 1024 + lane * 16);
     sw[i] = *reinterpret_cast<const uint32_t*>(t + 4096 + lane * 4);
-    if constexpr (kSrc == kMxRowsQ) {
 #pragma unroll
-      for (int t = 0; t < kTT; ++t) {
-        b[i][t] = *reinterpret_cast<const u32x4_t*>(xp[t] + c * 64);
-        sb[i][t] = sp[t][c * 4];
+    for (int q = 0; q < kTT; ++q) {
+      if constexpr (kRaw) {
+        const int col = kChunkK * c + kMxBlock * g;
+        mx_load_raw<kSrc>(xp[q], col, K - col, v[i][q]);
+      } else {
+        b[i][q] = *reinterpret_cast<const u32x4_t*>(xp[q] + c * 64);
+        sb[i][q] = sp[q][c * 4];
       }
-    } else {
-      const int col = kChunkK * c + kMxBlock * g;
-      mx_load_raw<kSrc>(raw, col, K - col, v[i]);
     }
   };
   f32x4_t acc[kRT][kTT];
@@ -156,12 +156,14 @@ __device__ __forceinline__ void mx_rows_body(const MxRowsTile& p, const void* x,
 #pragma unroll
     for (int t = 0; t < kTT; ++t) acc[r][t] = f32x4_t{0, 0, 0, 0};
   const auto multiply = [&](int i) {
-    if constexpr (kSrc != kMxRowsQ) b[i][0] = mx_quant32<kSrc>(v[i], sb[i][0]);
-    const uint32_t s = kRT == 4 ? sw[i] : sw[i] >> (8 * r0);
+    const int j = kRaw ? 0 : i;
 #pragma unroll
-    for (int r = 0; r < kRT; ++r)
+    for (int t = 0; t < kTT; ++t) {
+      if constexpr (kRaw) b[0][t] = mx_quant32<kSrc>(v[i][t], sb[0][t]);
 #pragma unroll
-      for (int t = 0; t < kTT; ++t) acc[r][t] = mfma_mx_row(r, w[i][r], b[i][t], acc[r][t], s, sb[i][t]);
+      for (int r = 0; r < kRT; ++r)
+        acc[r][t] = mfma_mx_row(r, w[i][r], b[j][t], acc[r][t], sw[i], sb[j][t]);
+    }
   };
 #pragma unroll
   for (int i = 0; i < kRing; ++i)

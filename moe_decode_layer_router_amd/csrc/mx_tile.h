@@ -306,6 +306,13 @@ __device__ __forceinline__ int mx_xcd_tile(int b, int tiles) {
   if (i >= per + (xcd < rem ? 1 : 0)) return -1;
   return xcd * per + min(xcd, rem) + i;
 }
+// How `count` rows fall into tiles of kBM: the last one takes the rest, and up to kOver
+// rows more than kBM rather than leaving them a tile of their own.
+template <int kBM, int kOver>
+__host__ __device__ inline int mx_row_tiles(int count) {
+  const int full = count / kBM, rest = count - full * kBM;
+  return full + (rest > (full ? kOver : 0) ? 1 : 0);
+}
 // tile t of tiles_n x tiles_m, in groups of 8 token tiles (kept in one L2)
 __device__ __forceinline__ void mx_tile_at(int t, int tiles_n, int tiles_m, int& tn, int& tm) {
   const int group = t / (8 * tiles_n);
