@@ -762,9 +762,9 @@ size_t moe_mx_gemm_workspace_bytes(const moe_mx_dims* dims);
 int moe_mx_gemm(const moe_mx_dims* dims, const void* xq, const void* xs, const void* w_packed,
                 void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
-/* moe_mx_quant of x and moe_mx_gemm in one call, with identical outputs (one launch up
- * to 16 rows, whose workgroups quantise them; else the quantised rows live in the
- * workspace).
+/* moe_mx_quant of x and moe_mx_gemm in one call, with identical outputs (one launch for
+ * few rows or small products, whose workgroups quantise the rows; else the quantised
+ * rows live in the workspace).
  *   x [M, K] in_type; out [M, N] out_type; workspace: moe_mx_gemm's rules. */
 size_t moe_mx_proj_workspace_bytes(const moe_mx_dims* dims);
 int moe_mx_proj(const moe_mx_dims* dims, const void* x, const void* w_packed, void* out,

@@ -9,11 +9,14 @@
 // Scores are taken relative to the largest where that keeps them from vanishing:
 // s(l) e^-m with m = min(max l, 0) is exp(min(l, 0) - m) / (1 + exp(-|l|)).
 //
-// Sixteen lanes hold a row (lanes16.h), four rows a wave. The forward orders the
-// keys as integers, takes the largest in each of topk rounds (a maximum over the
-// row, the lowest column that has it, that column struck out), and lane s keeps
-// pick s. The backward fills the row in LDS (zeros, or softmax's dense part), adds
-// the picks' terms there and stores it whole.
+// Sixteen lanes hold a row (lanes16.h), four rows a wave. The forward takes the largest
+// key in each of topk rounds, and lane s keeps pick s. Its rounds run on words of a key's
+// upper 24 bits and the column (the lower one above): all words differ, so the largest
+// below m is the largest word - m as an unsigned number, one subtraction a word in place of
+// finding and striking out a column. Where the lower 8 bits could matter (a pick out of
+// order with the next, or keys at the border that agree in 24 bits only) the wave takes
+// the rounds on whole keys. The backward fills the row in LDS (zeros, or softmax's dense
+// part), adds the picks' terms there and stores it whole.
 #include <type_traits>
 
 #include "common.h"
@@ -38,13 +41,12 @@ __device__ __forceinline__ float exp_near(float x) {
 }
 
 // An order of fp32 keys as integers: NaN above all (whatever its sign), then as
-// floats (-0 = +0); kNever for -inf, which is never picked.
-constexpr uint32_t kNever = 0;
+// floats (-0 = +0). -inf, which is never picked, comes last: kNever.
+constexpr uint32_t kNever = 0x007fffffu;
 __device__ __forceinline__ uint32_t order_key(float f) {
-  if (f != f) return 0xffffffffu;
-  if (f == -INFINITY) return kNever;
   const uint32_t u = __float_as_uint(f + 0.0f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return f != f ? 0xffffffffu : k;
 }
 
 template <int kCtrl>
@@ -117,6 +119,28 @@ __device__ __forceinline__ float pick_weight(float v, bool on, int score, int re
   return total == 0.0f ? 0.0f : a / total;
 }
 
+// the topk rounds on whole keys: the row's pick s in lane s, -1 where there is none
+template <int kNI>
+__device__ __forceinline__ int pick_exact(uint32_t (&key)[4 * kNI], int topk, int j) {
+  int id = -1;
+  for (int s = 0; s < topk; ++s) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < 4 * kNI; ++i) m = max(m, key[i]);
+    m = row_max_u(m);
+    uint32_t col = 0xffffu;  // lowest column with the maximum: 64 i + c ascends with the index
+#pragma unroll
+    for (int i = 4 * kNI - 1; i >= 0; --i)
+      col = key[i] == m ? static_cast<uint32_t>((i >> 2) * 64 + (i & 3)) : col;
+    const uint32_t e = row_min_u(col == 0xffffu ? col : col + 4 * j);
+#pragma unroll
+    for (int i = 0; i < 4 * kNI; ++i)
+      key[i] = e == static_cast<uint32_t>((i >> 2) * 64 + 4 * j + (i & 3)) ? 0u : key[i];
+    if (j == s) id = m <= kNever ? -1 : static_cast<int>(e);
+  }
+  return id;
+}
+
 template <int kNI>
 __global__ __launch_bounds__(256) void gate_kernel(GateArgs a) {
   const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
@@ -134,31 +158,54 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs a) {
   for (int base = blockIdx.x * kGateRows; base < a.T; base += step, row += step) {
     const Row<kNI> l = next;
     load_row<kNI>(a.logits, min(row + step, a.T - 1), E, j, next);
+    const float* lrow = a.logits + static_cast<size_t>(min(row, a.T - 1)) * E;
     uint32_t key[4 * kNI];
 #pragma unroll
     for (int i = 0; i < 4 * kNI; ++i) key[i] = order_key(a.bias ? l.v[i] + bias.v[i] : l.v[i]);
-    int id = -1;
-    for (int s = 0; s < a.topk; ++s) {
-      uint32_t m = key[0];
+    uint32_t word[4 * kNI], m = 0;
 #pragma unroll
-      for (int i = 1; i < 4 * kNI; ++i) m = max(m, key[i]);
-      m = row_max_u(m);
-      uint32_t col = 0xffffu;  // lowest column with the maximum: 64 i + c ascends with the index
-#pragma unroll
-      for (int i = 4 * kNI - 1; i >= 0; --i)
-        col = key[i] == m ? static_cast<uint32_t>((i >> 2) * 64 + (i & 3)) : col;
-      const uint32_t e = row_min_u(col == 0xffffu ? col : col + 4 * j);
-#pragma unroll
-      for (int i = 0; i < 4 * kNI; ++i)
-        key[i] = e == static_cast<uint32_t>((i >> 2) * 64 + 4 * j + (i & 3)) ? kNever : key[i];
-      if (j == s) id = m == kNever ? -1 : static_cast<int>(e);
+    for (int i = 0; i < 4 * kNI; ++i) {
+      const uint32_t e = (i >> 2) * 64 + 4 * j + (i & 3);
+      word[i] = (key[i] & 0xffffff00u) | (255u - e);
+      m = max(m, word[i]);
     }
-    float m = 0.0f, total = 1.0f;
-    if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) softmax_row<kNI>(l, m, total, nullptr);
-    const bool on = id >= 0 && row < a.T;
-    const float v = on ? a.logits[static_cast<size_t>(row) * E + id] : -INFINITY;
+    m = row_max_u(m);
+    // lane s: the word of rank s, up to rank topk (there are at least 64)
+    uint32_t mine = m;
+    for (int s = 1; s <= a.topk; ++s) {
+      uint32_t d = 0;
+#pragma unroll
+      for (int i = 0; i < 4 * kNI; ++i) d = max(d, word[i] - m);
+      m += row_max_u(d);
+      if (j == s) mine = m;
+    }
+    int id = mine <= kNever ? -1 : 255 - static_cast<int>(mine & 255u);
+    float v = id >= 0 ? lrow[id] : -INFINITY;
+    {
+      // the picks' whole keys have to descend, and behind the last pick all keys that share
+      // its 24 bits have to be equal to it
+      const uint32_t exact = id >= 0 ? order_key(a.bias ? v + a.bias[id] : v) : 0u;
+      const uint32_t after = static_cast<uint32_t>(
+          __builtin_amdgcn_update_dpp(0, static_cast<int>(exact), 0x101, 0xf, 0xf, true));  // lane + 1
+      bool bad = j < a.topk && exact < after;
+      const int first = threadIdx.x & 48;  // the row's lane 0
+      const uint32_t last = __shfl(mine, first + a.topk - 1, kWave), edge = __shfl(mine, first + a.topk, kWave);
+      const bool tie = last >> 8 == edge >> 8 && edge > kNever;
+      if (__any(tie)) {
+        const uint32_t whole = __shfl(exact, first + a.topk - 1, kWave);
+#pragma unroll
+        for (int i = 0; i < 4 * kNI; ++i) bad = bad || (tie && key[i] >> 8 == last >> 8 && key[i] != whole);
+      }
+      if (__any(bad)) {
+        id = pick_exact<kNI>(key, a.topk, j);
+        v = id >= 0 ? lrow[id] : -INFINITY;
+      }
+    }
+    float top = 0.0f, total = 1.0f;
+    if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) softmax_row<kNI>(l, top, total, nullptr);
+    const bool on = id >= 0 && j < a.topk;
     float slope;
-    const float w = pick_weight(v, on, a.score, a.renorm, m, total, slope);
+    const float w = pick_weight(v, on, a.score, a.renorm, top, total, slope);
     if (j < a.topk && row < a.T) {
       const size_t at = static_cast<size_t>(row) * a.topk + j;
       a.ids[at] = id;

@@ -147,6 +147,7 @@ constexpr int kRowsWaves = 8;
 template <int kTT, int kSrc>
 __global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(MxGemmArgs a) {
   __shared__ f32x4_t red[mx_rows_red<kTT, kRowsWaves>()];
+  __shared__ __attribute__((aligned(16))) uint8_t pass[kSrc == kMxRowsQ ? 16 : kRowsWaves * kTT * kMxPass];
   __shared__ int last;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int tiles = a.tiles_n * a.tiles_m, part = blockIdx.x / tiles, tile = blockIdx.x - part * tiles;
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(MxGemmArgs a) 
   part_range(a.Kc, a.split.parts, part, p.c0, p.c1);
   f32x4_t sum[1];
   static_assert(4 * kTT <= kRowsWaves, "a tile a wave");
-  mx_rows_body<kTT, kRowsWaves, (kTT == 2 && kSrc == kMxRowsFp32 ? 1 : 2), kSrc>(p, a.x, a.K, a.xq, a.xs, [](int t) { return t; }, red, sum);
+  mx_rows_body<kTT, kRowsWaves, (kTT == 2 && kSrc == kMxRowsFp32 ? 1 : 2), kSrc>(p, a.x, a.K, a.xq, a.xs, [](int t) { return t; }, pass, red, sum);
   if (!join_parts(a.split, tile, part, true, sum, &last)) return;
   const int token = t0 + (wave % kTT) * 16 + (lane & 15), n0 = (4 * rb + wave / kTT) * 16 + 4 * (lane >> 4);
   if (token < a.M && wave < 4 * kTT)
@@ -199,9 +200,9 @@ __device__ __forceinline__ void gemm_tile(const MxGemmArgs& a, int tn, int m0, i
                            : nullptr;
   };
   if (a.out_bf16)
-    mx_store_tile_bf16<kQ, kT>(lds, acc, [&](int row) { return row_of(row, uint16_t()); }, a.N - n0);
+    mx_store_tile<uint16_t>(lds, acc, [&](int row) { return row_of(row, uint16_t()); }, a.N - n0);
   else
-    mx_store_tile_f32<kQ, kT>(acc, [&](int row) { return row_of(row, float()); }, a.N - n0);
+    mx_store_tile<float>(lds, acc, [&](int row) { return row_of(row, float()); }, a.N - n0);
 }
 
 // tiles of 32 kQ kWN weight rows x kBM rows, kBM + kOver = 32 kT kWM: the last one takes up
@@ -231,10 +232,16 @@ int split_parts(int tiles, int Kc, int least) {
 // How a product of these sizes runs: the kernel, and its K parts. Measured, us, the product
 // alone; (p): K parts.
 //
-// Up to 32 rows registers (mx_rows.h, which quantise the rows as well), beyond tiles in
-// LDS: N = 4096, K = 7168, registers (4) / tiles of 64 x 64 (4): M = 16 6.9 / 10.0, M = 32
-// 8.4 / 10.2, M = 64 12.6 / 10.2. Parts cost about 2 us to add up: M = 1 9.8 (1), 8.6 (2), 8.2
-// (4); M = 1, N = 7168, K = 2048 5.3 (1), 6.7 (2); M = 8, N = 1024, K = 4096 7.8 (1), 6.3 (4).
+// Registers (mx_rows.h) up to 32 rows: N = 4096, K = 7168, registers (4) / tiles of 64 x 64 (4):
+// M = 16 6.9 / 10.0, M = 32 8.4 / 10.2. They quantise the rows as well (moe_mx_proj in one
+// launch), so they also take more rows while that gives at most one workgroup a CU, of at
+// most 18 chunks (two or three a wave). moe_mx_proj, us, registers / quantise and tiles: M =
+// 256, N = 512, K = 1024 4.5 / 8.6; M = 64, N = 4096, K = 2048 8.7 / 11.1; M = 1000, N = 64, K =
+// 4096 8.0 (4) / 12.4; on two workgroups a CU M = 512, N = 2048, K = 1024 9.6 / 7.6; of 32
+// chunks M = 64, N = 4096, K = 4096 14.4 / 13.3. 16 rows a workgroup while that keeps to one a
+// CU, else 32: M = 64, N = 2048, K = 2048 16 rows 5.8, 32 rows 8.6. Parts cost about 2 us to add
+// up: M = 1 9.8 (1), 8.6 (2), 7.8 (4); M = 1, N = 7168, K = 2048 5.3 (1), 6.7 (2); M = 8, N =
+// 1024, K = 4096 7.8 (1), 6.3 (4).
 //
 // Tiles of 64 x 64 (four workgroups a CU) while they are at most 512, of 128 x 128 (two) or
 // 256 x 256 (one, its last row tile up to 320 rows) beyond, by rounds over the CUs. 64 / 128 /
@@ -253,16 +260,16 @@ struct Plan {
 Plan mx_plan(const moe_mx_dims& m) {
   const int Kc = mx_chunks(m.K);
   Plan p;
-  p.parts = 1;
-  p.part_bytes = 0;
-  if (m.M <= 32) {
-    p.form = m.M <= 16 ? kRows16 : kRows32;
-    p.tiles_m = 1;
-    p.tiles_n = mx_row_blocks(m.N);
-    p.parts = split_parts(p.tiles_n, Kc, Kc >= 32 ? 8 : 16);
+  p.tiles_n = mx_row_blocks(m.N);
+  p.form = p.tiles_n * ceil_div(m.M, 16) <= 256 || m.M <= 16 ? kRows16 : kRows32;
+  p.tiles_m = ceil_div(m.M, p.form == kRows16 ? 16 : 32);
+  p.parts = split_parts(p.tiles_n * p.tiles_m, Kc, Kc >= 32 ? 8 : 16);
+  if (m.M <= 32 || (p.tiles_n * p.tiles_m <= 256 && ceil_div(Kc, p.parts) <= 18)) {
     p.part_bytes = 64 * kRowsWaves * 16;
     return p;
   }
+  p.parts = 1;
+  p.part_bytes = 0;
   const auto tiles = [&](Form form, int tn, int tm) {
     p.form = form;
     p.tiles_n = tn;

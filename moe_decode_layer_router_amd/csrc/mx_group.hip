@@ -118,7 +118,7 @@ __device__ __forceinline__ void group_tile(const MxGroupArgs& a, const Group& gr
           acc[q][t][4 * j + 1] = mx_swiglu(acc[q][t][4 * j + 1], acc[q][t][4 * j + 3]);
         }
     if (a.type == MOE_BF16) {
-      mx_store_bf16<kT, 16 * kQ>(
+      mx_store<uint16_t, kT, 16 * kQ>(
           lds,
           [&](int t, uint8_t* o) {
 #pragma unroll
@@ -173,9 +173,9 @@ __device__ __forceinline__ void group_tile(const MxGroupArgs& a, const Group& gr
   } else {
     const int n0 = tn * S::BN + wn * 32 * kQ;
     if (a.type == MOE_BF16)
-      mx_store_tile_bf16<kQ, kT>(lds, acc, [&](int row) { return row_of(row, uint16_t(), a.N, n0); }, a.N - n0);
+      mx_store_tile<uint16_t>(lds, acc, [&](int row) { return row_of(row, uint16_t(), a.N, n0); }, a.N - n0);
     else
-      mx_store_tile_f32<kQ, kT>(acc, [&](int row) { return row_of(row, float(), a.N, n0); }, a.N - n0);
+      mx_store_tile<float>(lds, acc, [&](int row) { return row_of(row, float(), a.N, n0); }, a.N - n0);
   }
 }
 
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_group_few_kernel(MxGroupArg
         if constexpr (kGateUp) return min(max(a.rows[gr.first + i], 0), a.T - 1);
         return gr.first + i;
       },
-      red, sum);
+      nullptr, red, sum);
   if constexpr (!kGateUp) {
     const int row = m0 + m16, n = (4 * rb + wave) * 16 + 4 * g;
     if (wave < 4 && row < gr.count)
@@ -288,11 +288,11 @@ inline int64_t max_tiles(int64_t R, int n, int bm) {
 // rows an expert has on average (evenly popular experts) and the experts that have any.
 // Measured, us, gate_up of 4096 x 2 x 2048, 32 of 256 experts held, top-8, tiles of 128 x 128 /
 // 256 x 256: 2 rows an expert 41.5 / 42.6, 16 rows 50.5 / 48.1, 32 rows 55 / 50, 64 rows 73 / 56,
-// 256 rows - / 105.
-// Few experts leave most CUs without a tile: there tiles of 64 x 64, and for up to 16 rows
-// the register kernel, which splits K over its waves. One expert, 128 x 128 / 64 x 64 /
-// registers: 1 row 10.3 / 9.5 / 4.9, 16 rows 10.4 / 9.6 / 6.1, 64 rows 10.6 / 9.7 / 12.5, 100
-// rows 12.9 / 9.7 / 12.5; seven experts of one row 14.2 / 15.3 / 16.6.
+// 256 rows 138 / 105; seven experts of one row 14.2 / 16.4.
+// Few experts, or narrow ones, leave most CUs without a large tile: there tiles of 64 x 64,
+// and for up to 16 rows the register kernel, which splits K over its waves. One expert,
+// 128 x 128 / 64 x 64 / registers: 1 row 10.3 / 9.5 / 4.9, 16 rows 10.4 / 9.6 / 6.1, 64 rows 10.6 /
+// 9.7 / -, 100 rows 12.9 / 9.7 / -.
 template <bool kGateUp>
 void launch_group(const moe_mx_group_dims& m, const MxGroupArgs& a, hipStream_t stream) {
   const int64_t picks = static_cast<int64_t>(m.T) * m.topk * m.n_local / m.E;  // that are local
@@ -301,15 +301,16 @@ void launch_group(const moe_mx_group_dims& m, const MxGroupArgs& a, hipStream_t 
   const auto grid = [&](int bm, int bn) {
     return static_cast<unsigned>(max_tiles(a.R, a.n, bm) * ((a.N + bn - 1) / bn));
   };
-  const int64_t blocks = active * (a.N / kRowsPerBlock);
+  const int64_t blocks = active * (a.N / kRowsPerBlock), tiles64 = blocks * ((per + 63) / 64);
+  const int64_t tiles256 = active * ((a.N + 255) / 256) * (per < 384 ? 1 : (per + 128) / 256);
   if (blocks <= 256 && per <= kFewRows)
     mx_group_few_kernel<kGateUp><<<grid(kFewRows, 64), 64 * kFewWaves, 0, stream>>>(a);
-  else if (blocks * ((per + 63) / 64) <= 256)
-    mx_group_tile_kernel<2, 1, 1, 2, 0, kGateUp><<<grid(64, 64), 128, 0, stream>>>(a);
-  else if (per < 12)
-    mx_group_tile_kernel<2, 2, 2, 2, 0, kGateUp><<<grid(128, 128), 256, 0, stream>>>(a);
-  else
+  else if (per >= 12 && tiles256 >= 200)
     mx_group_tile_kernel<2, 5, 4, 2, 64, kGateUp><<<grid(256, 256), 512, 0, stream>>>(a);
+  else if (tiles64 <= 512)
+    mx_group_tile_kernel<2, 1, 1, 2, 0, kGateUp><<<grid(64, 64), 128, 0, stream>>>(a);
+  else
+    mx_group_tile_kernel<2, 2, 2, 2, 0, kGateUp><<<grid(128, 128), 256, 0, stream>>>(a);
 }
 
 }  // namespace

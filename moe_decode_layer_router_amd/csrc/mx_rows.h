@@ -6,11 +6,13 @@
 // waves' sums are added through LDS in wave order. The weights are read once per group of
 // tokens, and their bytes bound the call.
 //
-// kSrc: quantised rows, or the rows themselves: a lane holds one MX block of its token, 32
-// adjacent columns, so it quantises them by itself, without a launch in front and with the
-// values moe_mx_quant gives.
+// kSrc: quantised rows, or the rows themselves, quantised here without a launch in front and
+// to the values moe_mx_quant gives: 16 lanes read a row's chunk (whole lines; a block a lane,
+// 64 bytes apart, touches each line four times: 99 x 286 x 1899 14.1 us, so 10.4), four of
+// them share a block, and the codes pass through the wave's own LDS into operand order.
 #pragma once
 
+#include "fp8_quant.h"
 #include "mx_dev.h"
 
 namespace moeblk {
@@ -19,82 +21,100 @@ enum MxSource { kMxRowsBf16, kMxRowsFp32, kMxRowsQ };
 
 typedef u32x4_t mx_u32x4_any_t __attribute__((aligned(2)));
 
-// 32 columns of a row from column c0 on (`left` of them inside the row), as fp32 words
-// or pairs of bf16
+// 8 columns of a row, as 8 fp32 words or 4 pairs of bf16
 template <int kSrc>
 struct MxRaw {
-  static constexpr int kWords = kSrc == kMxRowsFp32 ? 32 : 16;
-  uint32_t w[kWords];
+  uint32_t w[kSrc == kMxRowsFp32 ? 8 : 4];
 };
 
+// Columns c .. c + 7 of a row of K; where the row ends before that, its last 8 columns, for
+// mx_shift_raw to put in place. Rows of fewer than 8 columns come with their zeros.
 template <int kSrc>
-__device__ __forceinline__ void mx_load_raw(const void* row, int c0, int left, MxRaw<kSrc>& v) {
+__device__ __forceinline__ void mx_load_raw(const void* row, int c, int K, MxRaw<kSrc>& v) {
   constexpr bool kF32 = kSrc == kMxRowsFp32;
-  constexpr int kPer = kF32 ? 4 : 8;  // columns 16 bytes hold
-  const uint8_t* p = static_cast<const uint8_t*>(row) + static_cast<size_t>(c0) * (kF32 ? 4 : 2);
+  const uint8_t* p = static_cast<const uint8_t*>(row);
+  if (K >= 8) {
+    p += static_cast<size_t>(min(c, K - 8)) * (kF32 ? 4 : 2);
 #pragma unroll
-  for (int i = 0; i < MxRaw<kSrc>::kWords / 4; ++i) {
-    u32x4_t q = {0, 0, 0, 0};
-    if (kPer * (i + 1) <= left) q = *reinterpret_cast<const mx_u32x4_any_t*>(p + 16 * i);
+    for (int i = 0; i < (kF32 ? 2 : 1); ++i) {
+      const u32x4_t q = *reinterpret_cast<const mx_u32x4_any_t*>(p + 16 * i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v.w[4 * i + j] = q[j];
-  }
-  if (left <= 0 || left >= 32 || left % kPer == 0) return;
-  // the row ends inside 16 bytes: their columns one by one, the last one in the place of
-  // those behind it (all loads at once, none outside the row), which are then cleared
-  const int first = left / kPer * kPer;
-  uint32_t t[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int c = min(first + j, left - 1);
-    t[j] = kF32 ? reinterpret_cast<const uint32_t*>(p)[c] : reinterpret_cast<const uint16_t*>(p)[c];
-  }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) t[j] = first + j < left ? t[j] : 0u;
-#pragma unroll
-  for (int i = 0; i < MxRaw<kSrc>::kWords / 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = kF32 ? t[j] : t[2 * j % kPer] | (t[(2 * j + 1) % kPer] << 16);
-      v.w[4 * i + j] = first == kPer * i ? w : v.w[4 * i + j];
+      for (int j = 0; j < 4; ++j) v.w[4 * i + j] = q[j];
     }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < (kF32 ? 8 : 4); ++j) v.w[j] = 0;
+#pragma unroll
+  for (int j = 0; j < 7; ++j) {
+    if (c + j >= K) continue;
+    if constexpr (kF32)
+      v.w[j] = reinterpret_cast<const uint32_t*>(p)[c + j];
+    else
+      v.w[j >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[c + j]) << (16 * (j & 1));
+  }
 }
 
-// a block's 32 codes, and its scale byte
+// the columns `by` places further on in front, zeros behind them
 template <int kSrc>
-__device__ __forceinline__ u32x4_t mx_quant32(const MxRaw<kSrc>& v, uint32_t& byte) {
+__device__ __forceinline__ void mx_shift_raw(MxRaw<kSrc>& v, int by) {
+  by = min(by, 8);
+  if constexpr (kSrc == kMxRowsFp32) {
+#pragma unroll
+    for (int s = 4; s >= 1; s >>= 1) {
+      const bool on = (by & s) != 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v.w[i] = on ? (i + s < 8 ? v.w[i + s] : 0u) : v.w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.w[i] = by == 8 ? 0u : v.w[i];
+  } else {
+    uint64_t lo = v.w[0] | static_cast<uint64_t>(v.w[1]) << 32, hi = v.w[2] | static_cast<uint64_t>(v.w[3]) << 32;
+    if (by & 4) lo = hi, hi = 0;
+    const int s = 16 * (by & 3);
+    lo = s ? (lo >> s) | (hi << (64 - s)) : lo;
+    hi >>= s;
+    if (by == 8) lo = hi = 0;
+    v.w[0] = static_cast<uint32_t>(lo);
+    v.w[1] = static_cast<uint32_t>(lo >> 32);
+    v.w[2] = static_cast<uint32_t>(hi);
+    v.w[3] = static_cast<uint32_t>(hi >> 32);
+  }
+}
+
+// The codes of 8 columns by one of four adjacent lanes that share a block (all of which
+// take part), and the block's scale byte.
+template <int kSrc>
+__device__ __forceinline__ uint32_t mx_quant8(const MxRaw<kSrc>& v, uint32_t& byte) {
   typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
   uint32_t m = 0;
   if constexpr (kSrc == kMxRowsFp32) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t a = v.w[i] & 0x7fffffffu;
-      m = m > a ? m : a;
-    }
+    for (int i = 0; i < 8; ++i) m = max(m, v.w[i] & 0x7fffffffu);
   } else {
     u16x2_t p = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 4; ++i)
       p = __builtin_elementwise_max(p, __builtin_bit_cast(u16x2_t, v.w[i] & 0x7fff7fffu));
     m = static_cast<uint32_t>(p[0] > p[1] ? p[0] : p[1]) << 16;
   }
+  m = max_dpp<0xb1>(m);  // lane ^ 1
+  m = max_dpp<0x4e>(m);  // lane ^ 2
   byte = mx_scale_byte(m);
   const float s = e8m0_scale(byte);
-  u32x4_t q;
+  uint32_t q;
+  if constexpr (kSrc == kMxRowsFp32) {
+    float f[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (kSrc == kMxRowsFp32) {
-      float f[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(v.w[8 * i + j]);
-      q[i] = mx_codes(f, s);
-    } else {
-      q[i] = mx_codes_bf16(&v.w[4 * i], s);
-    }
-    q[i] = mx_codes_or_zero(q[i], byte);
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v.w[i]);
+    q = mx_codes(f, s);
+  } else {
+    q = mx_codes_bf16(v.w, s);
   }
-  return q;
+  return mx_codes_or_zero(q, byte);
 }
+
+constexpr int kMxPass = 1024 + 64;  // LDS bytes of a wave's token tile: codes, scale bytes
 
 // What a workgroup multiplies: chunks [c0, c1) of the row block whose first tile is at w, and
 // of tokens t0 .. t0 + 16 kTT - 1 of M.
@@ -110,30 +130,36 @@ constexpr int mx_rows_red() {
 }
 
 // sum[e]: of tile i = kNW e + wave, i < 4 kTT: row tile i / kTT, token tile i % kTT. red:
-// mx_rows_red elements. row_of(token) gives a token's row of x.
+// mx_rows_red elements; pass: kNW kTT kMxPass bytes (rows as they are only). row_of(token)
+// gives a token's row of x.
 template <int kTT, int kNW, int kRing, int kSrc, typename F>
 __device__ __forceinline__ void mx_rows_body(const MxRowsTile& p, const void* x, int K,
                                              const uint8_t* xq, const uint8_t* xs, F row_of,
-                                             f32x4_t* red, f32x4_t (&sum)[(4 * kTT + kNW - 1) / kNW]) {
+                                             uint8_t* pass, f32x4_t* red, f32x4_t (&sum)[(4 * kTT + kNW - 1) / kNW]) {
   constexpr int kRT = 4;
   constexpr bool kRaw = kSrc != kMxRowsQ;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int m16 = lane & 15, g = lane >> 4;
   const int Kc = p.Kc;
-  const uint8_t *xp[kTT], *sp[kTT];
+  constexpr int kRows = kRaw ? 4 : 1;  // rows a lane reads of a token tile
+  const int tokens = p.M - p.t0;
+  const uint8_t *xp[kTT][kRows], *sp[kTT];
 #pragma unroll
   for (int t = 0; t < kTT; ++t) {
-    const size_t row = row_of(min(p.t0 + 16 * t + m16, p.M - 1));
-    if constexpr (kRaw) {
-      xp[t] = static_cast<const uint8_t*>(x) + row * K * (kSrc == kMxRowsFp32 ? 4 : 2);
-    } else {
-      xp[t] = xq + row * (static_cast<size_t>(Kc) * 64) + 16 * g;
-      sp[t] = xs + row * (static_cast<size_t>(Kc) * 4) + g;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const size_t row = row_of(min(p.t0 + 16 * t + (kRaw ? 4 * i + g : m16), p.M - 1));
+      if constexpr (kRaw) {
+        xp[t][i] = static_cast<const uint8_t*>(x) + row * K * (kSrc == kMxRowsFp32 ? 4 : 2);
+      } else {
+        xp[t][i] = xq + row * (static_cast<size_t>(Kc) * 64) + 16 * g;
+        sp[t] = xs + row * (static_cast<size_t>(Kc) * 4) + g;
+      }
     }
   }
   u32x4_t w[kRing][kRT], b[kRaw ? 1 : kRing][kTT];
   uint32_t sw[kRing], sb[kRaw ? 1 : kRing][kTT];
-  MxRaw<kSrc> v[kRaw ? kRing : 1][kRaw ? kTT : 1];
+  MxRaw<kSrc> v[kRaw ? kRing : 1][kTT][kRows];
   const auto load = [&](int i, int c) {
     const uint8_t* t = p.w + static_cast<size_t>(c) * kMxTileBytes;
 #pragma unroll
@@ -142,10 +168,11 @@ __device__ __forceinline__ void mx_rows_body(const MxRowsTile& p, const void* x,
 #pragma unroll
     for (int q = 0; q < kTT; ++q) {
       if constexpr (kRaw) {
-        const int col = kChunkK * c + kMxBlock * g;
-        mx_load_raw<kSrc>(xp[q], col, K - col, v[i][q]);
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+          if (16 * q + 4 * j < tokens) mx_load_raw<kSrc>(xp[q][j], kChunkK * c + 8 * m16, K, v[i][q][j]);
       } else {
-        b[i][q] = *reinterpret_cast<const u32x4_t*>(xp[q] + c * 64);
+        b[i][q] = *reinterpret_cast<const u32x4_t*>(xp[q][0] + c * 64);
         sb[i][q] = sp[q][c * 4];
       }
     }
@@ -155,11 +182,31 @@ __device__ __forceinline__ void mx_rows_body(const MxRowsTile& p, const void* x,
   for (int r = 0; r < kRT; ++r)
 #pragma unroll
     for (int t = 0; t < kTT; ++t) acc[r][t] = f32x4_t{0, 0, 0, 0};
-  const auto multiply = [&](int i) {
+  const auto multiply = [&](int i, int c) {
     const int j = kRaw ? 0 : i;
+    const bool tail = kRaw && K >= 8 && kChunkK * (c + 1) > K;
 #pragma unroll
     for (int t = 0; t < kTT; ++t) {
-      if constexpr (kRaw) b[0][t] = mx_quant32<kSrc>(v[i][t], sb[0][t]);
+      if constexpr (kRaw) {
+        // row 4 j + g, columns 8 m16 .. + 7 -> token m16, block g; a wave's LDS accesses stay
+        // in order, in the code as well
+        uint8_t* o = pass + (wave * kTT + t) * kMxPass;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (16 * t + 4 * j >= tokens) break;  // nothing there; those tokens' sums are not looked at
+          if (tail) mx_shift_raw<kSrc>(v[i][t][j], kChunkK * c + 8 * m16 - min(kChunkK * c + 8 * m16, K - 8));
+          uint32_t byte;
+          const uint32_t q = mx_quant8<kSrc>(v[i][t][j], byte);
+          *reinterpret_cast<uint32_t*>(o + (4 * j + g) * 64 + 4 * m16) = q;
+          if ((m16 & 3) == 0) o[1024 + (4 * j + g) * 4 + (m16 >> 2)] = static_cast<uint8_t>(byte);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        b[0][t] = *reinterpret_cast<const u32x4_t*>(o + m16 * 64 + g * 16);
+        sb[0][t] = o[1024 + m16 * 4 + g];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
 #pragma unroll
       for (int r = 0; r < kRT; ++r)
         acc[r][t] = mfma_mx_row(r, w[i][r], b[j][t], acc[r][t], sw[i], sb[j][t]);
@@ -173,7 +220,7 @@ __device__ __forceinline__ void mx_rows_body(const MxRowsTile& p, const void* x,
     for (int i = 0; i < kRing; ++i) {
       const int c = base + kNW * i;
       if (c < p.c1) {
-        multiply(i);
+        multiply(i, c);
         if (c + kNW * kRing < p.c1) load(i, c + kNW * kRing);
       }
     }

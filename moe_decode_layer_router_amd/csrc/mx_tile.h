@@ -81,7 +81,7 @@ struct MxTileShape {
   static_assert(BN / 16 % kWaves == 0 && BM / 8 % kWaves == 0, "whole pieces a wave");
   static_assert(kLds <= 160 * 1024, "LDS");
   // what the outputs pass through behind the last step
-  static_assert(kWaves * 32 * (32 * kQ * 2 + 16) <= kLds && kWaves * 32 * kT * (kQ / 2) * 16 <= kLds, "LDS");
+  static_assert(kWaves * 32 * (32 * kQ * 4 + 16) <= kLds && kWaves * 32 * kT * (kQ / 2) * 16 <= kLds, "LDS");
 };
 
 // row_of(i) gives the row (from p.xq) of the tile's token i
@@ -322,20 +322,23 @@ __device__ __forceinline__ void mx_tile_at(int t, int tiles_n, int tiles_m, int&
   tn = in / gm;
 }
 
-// bf16 outputs through LDS, so that they leave as whole lines, 16 bytes a lane: kCols values
-// a token. Each wave takes its token tiles in turn through its own kMxStage bytes (rows
-// padded by 16 bytes); put(t, o) writes the lane's values of token tile t at its token's
-// place o.
-template <int kCols>
-constexpr int kMxStage = 32 * (kCols * 2 + 16);
+// Outputs through LDS, so that they leave as whole lines, 16 bytes a lane: kCols values of
+// type T a token (fp32, 7414 x 2049 x 941 with its quantisation 29 us, straight from the
+// registers 33). Each wave takes its token tiles in turn through its own kMxStage bytes (rows padded by 16 bytes); put(t, o)
+// writes the lane's values of token tile t at its token's place o; row_of(i) gives where the
+// outputs of the wave's token i start, or NULL.
+template <typename T, int kCols>
+constexpr int kMxStage = 32 * (kCols * sizeof(T) + 16);
 
-template <int kT, int kCols, typename Put, typename Row>
-__device__ __forceinline__ void mx_store_bf16(uint8_t* lds, Put put, Row row_of, int n_left) {
+template <typename T, int kT, int kCols, typename Put, typename Row>
+__device__ __forceinline__ void mx_store(uint8_t* lds, Put put, Row row_of, int n_left) {
   typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
-  constexpr int kPitch = kCols * 2 + 16, kLanes = kCols / 8;
+  constexpr int kPer = 16 / sizeof(T);  // values a lane
+  constexpr int kPitch = kCols * sizeof(T) + 16, kLanes = kCols / kPer, kRows = 64 / kLanes;
+  static_assert(kLanes <= 64 && kRows <= 32, "whole rows a wave");
   const int lane = threadIdx.x & 63;
-  uint8_t* o = lds + (threadIdx.x >> 6) * kMxStage<kCols>;
-  const int c16 = lane % kLanes, left = n_left - 8 * c16;
+  uint8_t* o = lds + (threadIdx.x >> 6) * kMxStage<T, kCols>;
+  const int c16 = lane % kLanes, left = n_left - kPer * c16;
   const auto in_order = [] {  // a wave's LDS accesses stay in order, in the code as well
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -344,62 +347,54 @@ __device__ __forceinline__ void mx_store_bf16(uint8_t* lds, Put put, Row row_of,
   for (int t = 0; t < kT; ++t) {
     put(t, o + (lane & 31) * kPitch);
     in_order();
-    u32x4_t v[32 * kLanes / 64];
+    u32x4_t v[32 / kRows];
 #pragma unroll
-    for (int i = 0; i < 32 * kLanes / 64; ++i)
-      v[i] = *reinterpret_cast<const u32x4_t*>(o + (i * (64 / kLanes) + lane / kLanes) * kPitch + 16 * c16);
+    for (int i = 0; i < 32 / kRows; ++i)
+      v[i] = *reinterpret_cast<const u32x4_t*>(o + (i * kRows + lane / kLanes) * kPitch + 16 * c16);
     in_order();
 #pragma unroll
-    for (int i = 0; i < 32 * kLanes / 64; ++i) {
-      uint16_t* to = row_of(t * 32 + i * (64 / kLanes) + lane / kLanes);
+    for (int i = 0; i < 32 / kRows; ++i) {
+      T* to = row_of(t * 32 + i * kRows + lane / kLanes);
       if (!to) continue;
-      to += 8 * c16;
-      if (left >= 8) {
+      to += kPer * c16;
+      if (left >= kPer) {
         *reinterpret_cast<u32x4_any_t*>(to) = v[i];
       } else {
 #pragma unroll
-        for (int c = 0; c < 7; ++c)
-          if (c < left) to[c] = static_cast<uint16_t>(v[i][c >> 1] >> (16 * (c & 1)));
+        for (int c = 0; c < kPer - 1; ++c) {
+          if (c >= left) continue;
+          if constexpr (sizeof(T) == 2)
+            to[c] = static_cast<T>(v[i][c >> 1] >> (16 * (c & 1)));
+          else
+            to[c] = __uint_as_float(v[i][c]);
+        }
       }
     }
   }
 }
 
-// a tile's outputs: this wave's weight rows from n0 on; row_of(i) gives where the outputs
-// of the wave's token i start (n0 included), or NULL
-template <int kQ, int kT, typename Row>
-__device__ __forceinline__ void mx_store_tile_bf16(uint8_t* lds, const f32x16_t (&acc)[kQ][kT], Row row_of,
-                                                   int n_left) {
+// a tile's outputs: this wave's weight rows in order
+template <typename T, int kQ, int kT, typename Row>
+__device__ __forceinline__ void mx_store_tile(uint8_t* lds, const f32x16_t (&acc)[kQ][kT], Row row_of,
+                                              int n_left) {
   const int hi = (threadIdx.x & 63) >> 5;
-  mx_store_bf16<kT, 32 * kQ>(
+  mx_store<T, kT, 32 * kQ>(
       lds,
       [&](int t, uint8_t* o) {
 #pragma unroll
         for (int q = 0; q < kQ; ++q)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<u32x2_t*>(o + q * 64 + j * 16 + 8 * hi) =
-                u32x2_t{mx_bf16x2(acc[q][t][4 * j], acc[q][t][4 * j + 1]),
-                        mx_bf16x2(acc[q][t][4 * j + 2], acc[q][t][4 * j + 3])};
+          for (int j = 0; j < 4; ++j) {
+            const f32x16_t& d = acc[q][t];
+            uint8_t* to = o + (q * 32 + j * 8 + 4 * hi) * sizeof(T);
+            if constexpr (sizeof(T) == 2)
+              *reinterpret_cast<u32x2_t*>(to) =
+                  u32x2_t{mx_bf16x2(d[4 * j], d[4 * j + 1]), mx_bf16x2(d[4 * j + 2], d[4 * j + 3])};
+            else
+              *reinterpret_cast<f32x4_t*>(to) = f32x4_t{d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]};
+          }
       },
       row_of, n_left);
-}
-template <int kQ, int kT, typename Row>
-__device__ __forceinline__ void mx_store_tile_f32(const f32x16_t (&acc)[kQ][kT], Row row_of, int n_left) {
-  const int lane = threadIdx.x & 63, hi = lane >> 5;
-#pragma unroll
-  for (int t = 0; t < kT; ++t) {
-    float* o = row_of(t * 32 + (lane & 31));
-#pragma unroll
-    for (int q = 0; q < kQ; ++q)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = q * 32 + j * 8 + 4 * hi;
-        const f32x4_t v = {acc[q][t][4 * j], acc[q][t][4 * j + 1], acc[q][t][4 * j + 2], acc[q][t][4 * j + 3]};
-        if (o) store4<true>(o, n, n_left - n, v, false);
-        __builtin_amdgcn_sched_barrier(0);  // one piece's addresses at a time
-      }
-  }
 }
 
 }  // namespace moeblk

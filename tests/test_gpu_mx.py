@@ -173,7 +173,8 @@ SMALL = [(1, 1, 1), (1, 16, 128), (1, 64, 4096), (2, 17, 129), (16, 100, 300), (
          (17, 64, 128), (32, 33, 500), (31, 4100, 130), (33, 64, 1000), (64, 129, 384), (63, 4099, 256), (64, 16, 4096),
          (65, 100, 200), (77, 4099, 2120), (100, 1, 77), (129, 500, 640), (200, 4100, 1500), (300, 4096, 1024), (1000, 1000, 1000),
          (5, 300, 4100), (16, 4096, 1030), (24, 700, 8191), (32, 128, 3999), (33, 100, 5000), (64, 1024, 3080), (100, 64, 20000),
-         (512, 4096, 128), (520, 4096, 300), (2100, 2048, 257)]
+         (512, 4096, 128), (520, 4096, 300), (2100, 2048, 257), (1000, 64, 4096), (2048, 60, 700), (333, 500, 2304), (8000, 17, 33),
+         (129, 2000, 3000), (900, 900, 2500)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "fp32"])
