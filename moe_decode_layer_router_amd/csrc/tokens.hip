@@ -154,68 +154,96 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
 
 // ---------------------------------------------------------------- rows
 //
-// Rows move in pieces of 8 values: kLanes threads take a token's row, every kLanes-th
-// piece each, so that a token's row is read once for all of its picks. Rows of any
-// length start anywhere: 16-byte accesses take any alignment. All of it is bound by
-// memory.
+// Rows move in pieces of 16 bytes of the wider type, 8 bf16 values or 4: kLanes threads
+// take a token's row, every kLanes-th piece each, so that a wave's accesses are contiguous and
+// a token's row is read once for all of its picks. Rows of any length start anywhere:
+// accesses take any alignment. All of it is bound by memory.
 typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+typedef u32x2_t u32x2_any_t __attribute__((aligned(2)));
 typedef f32x4_t f32x4_any4_t __attribute__((aligned(4)));
 
+template <int kN>
 struct Piece {
-  float v[8];
+  float v[kN];
+};
+template <typename Tok, typename Row>
+constexpr int kPiece = sizeof(Tok) + sizeof(Row) == 4 ? 8 : 4;
+
+// a piece as loaded; behind the row's end: zeros
+template <typename T, int kN>
+struct Raw {
+  uint32_t w[kN * sizeof(T) / 4];
 };
 
-__device__ __forceinline__ Piece load_piece(const uint16_t* row, int c, int d) {
-  Piece p;
-  if (c + 8 <= d) {
-    const u32x4_t q = *reinterpret_cast<const u32x4_any_t*>(row + c);
+template <typename T, int kN>
+__device__ __forceinline__ Raw<T, kN> load_raw(const T* row, int c, int d) {
+  Raw<T, kN> r;
+  if (c + kN <= d) {
+    if constexpr (kN * sizeof(T) >= 16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p.v[2 * i] = bf16_lo(q[i]);
-      p.v[2 * i + 1] = bf16_hi(q[i]);
+      for (int h = 0; h < static_cast<int>(kN * sizeof(T) / 16); ++h) {
+        const u32x4_t u = *reinterpret_cast<const u32x4_any_t*>(row + c + 16 / sizeof(T) * h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[4 * h + i] = u[i];
+      }
+    } else {
+      static_assert(kN * sizeof(T) == 8, "8, 16 or 32 bytes");
+      const u32x2_t u = *reinterpret_cast<const u32x2_any_t*>(row + c);
+      r.w[0] = u[0];
+      r.w[1] = u[1];
     }
-  } else {
+    return r;
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p.v[i] = c + i < d ? bf16_to_f32(row[c + i]) : 0.0f;
+  for (int i = 0; i < static_cast<int>(kN * sizeof(T) / 4); ++i) r.w[i] = 0;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    if (c + i >= d) continue;
+    if constexpr (sizeof(T) == 2)
+      r.w[i >> 1] |= static_cast<uint32_t>(row[c + i]) << (16 * (i & 1));
+    else
+      r.w[i] = __float_as_uint(row[c + i]);
+  }
+  return r;
+}
+template <typename T, int kN>
+__device__ __forceinline__ Piece<kN> values(const Raw<T, kN>& r) {
+  Piece<kN> p;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    if constexpr (sizeof(T) == 2)
+      p.v[i] = i & 1 ? bf16_hi(r.w[i >> 1]) : bf16_lo(r.w[i >> 1]);
+    else
+      p.v[i] = __uint_as_float(r.w[i]);
   }
   return p;
 }
-__device__ __forceinline__ Piece load_piece(const float* row, int c, int d) {
-  Piece p;
-  if (c + 8 <= d) {
+
+// Stores go past the caches: 8192 x 7168, bf16 rows, fp32 tokens, 32 of 256 experts held, us with
+// / without: moe_return 54 / 82, moe_dispatch 51 / 58.
+template <int kN>
+__device__ __forceinline__ void store_piece(uint16_t* row, int c, int d, const Piece<kN>& p) {
+  uint32_t q[kN / 2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4_t q = *reinterpret_cast<const f32x4_any4_t*>(row + c + 4 * h);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p.v[4 * h + i] = q[i];
-    }
+  for (int i = 0; i < kN / 2; ++i) q[i] = pack_bf16x2(p.v[2 * i], p.v[2 * i + 1]);
+  if (c + kN <= d) {
+    if constexpr (kN == 8)
+      __builtin_nontemporal_store(u32x4_t{q[0], q[1], q[2], q[3]}, reinterpret_cast<u32x4_any_t*>(row + c));
+    else
+      __builtin_nontemporal_store(u32x2_t{q[0], q[1]}, reinterpret_cast<u32x2_any_t*>(row + c));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p.v[i] = c + i < d ? row[c + i] : 0.0f;
-  }
-  return p;
-}
-__device__ __forceinline__ void store_piece(uint16_t* row, int c, int d, const Piece& p) {
-  u32x4_t q;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = pack_bf16x2(p.v[2 * i], p.v[2 * i + 1]);
-  if (c + 8 <= d) {
-    *reinterpret_cast<u32x4_any_t*>(row + c) = q;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < kN - 1; ++i)
       if (c + i < d) row[c + i] = static_cast<uint16_t>(q[i >> 1] >> (16 * (i & 1)));
   }
 }
-__device__ __forceinline__ void store_piece(float* row, int c, int d, const Piece& p) {
-  if (c + 8 <= d) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<f32x4_any4_t*>(row + c + 4 * h) =
-          f32x4_t{p.v[4 * h], p.v[4 * h + 1], p.v[4 * h + 2], p.v[4 * h + 3]};
+template <int kN>
+__device__ __forceinline__ void store_piece(float* row, int c, int d, const Piece<kN>& p) {
+  if (c + kN <= d) {
+    __builtin_nontemporal_store(f32x4_t{p.v[0], p.v[1], p.v[2], p.v[3]}, reinterpret_cast<f32x4_any4_t*>(row + c));
   } else {
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
+    for (int i = 0; i < kN - 1; ++i)
       if (c + i < d) row[c + i] = p.v[i];
   }
 }
@@ -229,25 +257,32 @@ struct RowsArgs {
   int T, topk, d, R;
 };
 
-// The positions of a token's picks; a position outside the sorted rows is none.
-template <int kTopk>
-__device__ __forceinline__ void load_pos(const RowsArgs& a, int t, int (&pos)[kTopk]) {
+// The positions of a token's picks; a position outside the sorted rows is none. With a wave
+// or more a row they are the same in the whole wave, and known to be.
+template <int kLanes>
+__device__ __forceinline__ void load_pos(const RowsArgs& a, int t, int (&pos)[8]) {
 #pragma unroll
-  for (int s = 0; s < kTopk; ++s) {
+  for (int s = 0; s < 8; ++s) {
     pos[s] = s < a.topk ? a.pick_pos[static_cast<size_t>(t) * a.topk + s] : -1;
     if (pos[s] >= a.R) pos[s] = -1;
+    if constexpr (kLanes >= kWave) pos[s] = __builtin_amdgcn_readfirstlane(pos[s]);
   }
 }
 
 template <typename Tok, typename Row, int kLanes>
 __global__ __launch_bounds__(256) void dispatch_kernel(RowsArgs a) {
+  constexpr int kN = kPiece<Tok, Row>;
   const int t = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
   if (t >= a.T) return;
   int pos[8];
-  load_pos(a, t, pos);
+  load_pos<kLanes>(a, t, pos);
+  bool any = false;  // rows of tokens without a pick are not read
+#pragma unroll
+  for (int s = 0; s < 8; ++s) any = any || pos[s] >= 0;
+  if (!any) return;
   const Tok* x = static_cast<const Tok*>(a.tok) + static_cast<size_t>(t) * a.d;
-  for (int c = threadIdx.x % kLanes * 8; c < a.d; c += kLanes * 8) {
-    const Piece p = load_piece(x, c, a.d);
+  for (int c = threadIdx.x % kLanes * kN; c < a.d; c += kLanes * kN) {
+    const Piece<kN> p = values<Tok, kN>(load_raw<Tok, kN>(x, c, a.d));
 #pragma unroll
     for (int s = 0; s < 8; ++s)
       if (pos[s] >= 0)
@@ -255,28 +290,38 @@ __global__ __launch_bounds__(256) void dispatch_kernel(RowsArgs a) {
   }
 }
 
+// the pieces of all picks' rows, their loads in flight together
+template <typename Row, int kN>
+__device__ __forceinline__ void load_rows(const RowsArgs& a, const int (&pos)[8], int c, Raw<Row, kN> (&y)[8]) {
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    if (pos[s] >= 0)
+      y[s] = load_raw<Row, kN>(static_cast<const Row*>(a.row) + static_cast<size_t>(pos[s]) * a.d, c, a.d);
+}
+
 // sums in fp32, in slot order, one rounding
 template <typename Tok, typename Row, int kLanes>
 __global__ __launch_bounds__(256) void return_kernel(RowsArgs a) {
+  constexpr int kN = kPiece<Tok, Row>;
   const int t = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
   if (t >= a.T) return;
   int pos[8];
   float w[8];
-  load_pos(a, t, pos);
+  load_pos<kLanes>(a, t, pos);
 #pragma unroll
   for (int s = 0; s < 8; ++s)
     w[s] = a.w && pos[s] >= 0 ? a.w[static_cast<size_t>(t) * a.topk + s] : 1.0f;
   Tok* out = static_cast<Tok*>(a.tok_out) + static_cast<size_t>(t) * a.d;
-  for (int c = threadIdx.x % kLanes * 8; c < a.d; c += kLanes * 8) {
-    Piece sum = {};
+  for (int c = threadIdx.x % kLanes * kN; c < a.d; c += kLanes * kN) {
+    Raw<Row, kN> y[8];
+    load_rows(a, pos, c, y);
+    Piece<kN> sum = {};
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
-      if (pos[s] >= 0) {
-        const Piece p =
-            load_piece(static_cast<const Row*>(a.row) + static_cast<size_t>(pos[s]) * a.d, c, a.d);
+      if (pos[s] < 0) continue;
+      const Piece<kN> p = values<Row, kN>(y[s]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum.v[i] = __builtin_fmaf(p.v[i], w[s], sum.v[i]);
-      }
+      for (int i = 0; i < kN; ++i) sum.v[i] = __builtin_fmaf(p.v[i], w[s], sum.v[i]);
     }
     store_piece(out, c, a.d, sum);
   }
@@ -286,35 +331,38 @@ __global__ __launch_bounds__(256) void return_kernel(RowsArgs a) {
 // threads' fp32 sums are added in a fixed tree
 template <typename Tok, typename Row, int kLanes>
 __global__ __launch_bounds__(256) void return_backward_kernel(RowsArgs a) {
+  constexpr int kN = 16 / sizeof(Row);  // the rows' bytes, read and written, are most of all
   __shared__ float red[256 / kWave][8];
   const int t = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
   const bool in = t < a.T;
   int pos[8];
   float w[8], dw[8];
-#pragma unroll
-  for (int s = 0; s < 8; ++s) pos[s] = -1;
-  if (in) load_pos(a, t, pos);
+  load_pos<kLanes>(a, in ? t : 0, pos);
+  bool any = false;  // rows of tokens without a pick are not read
 #pragma unroll
   for (int s = 0; s < 8; ++s) {
-    w[s] = a.w && pos[s] >= 0 ? a.w[static_cast<size_t>(t) * a.topk + s] : 1.0f;
+    if (!in) pos[s] = -1;
+    any = any || pos[s] >= 0;
+    w[s] = pos[s] >= 0 ? a.w[static_cast<size_t>(t) * a.topk + s] : 1.0f;
     dw[s] = 0.0f;
   }
   const Tok* g = static_cast<const Tok*>(a.tok) + static_cast<size_t>(in ? t : 0) * a.d;
-  for (int c = threadIdx.x % kLanes * 8; in && c < a.d; c += kLanes * 8) {
-    const Piece p = load_piece(g, c, a.d);
+  for (int c = threadIdx.x % kLanes * kN; any && c < a.d; c += kLanes * kN) {
+    const Raw<Tok, kN> graw = load_raw<Tok, kN>(g, c, a.d);
+    Raw<Row, kN> y[8];
+    load_rows(a, pos, c, y);
+    const Piece<kN> p = values<Tok, kN>(graw);
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
-      if (pos[s] >= 0) {
-        const size_t at = static_cast<size_t>(pos[s]) * a.d;
-        const Piece y = load_piece(static_cast<const Row*>(a.row) + at, c, a.d);
-        Piece q;
+      if (pos[s] < 0) continue;
+      const Piece<kN> v = values<Row, kN>(y[s]);
+      Piece<kN> q;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dw[s] = __builtin_fmaf(p.v[i], y.v[i], dw[s]);
-          q.v[i] = p.v[i] * w[s];
-        }
-        store_piece(static_cast<Row*>(a.row_out) + at, c, a.d, q);
+      for (int i = 0; i < kN; ++i) {
+        dw[s] = __builtin_fmaf(p.v[i], v.v[i], dw[s]);
+        q.v[i] = p.v[i] * w[s];
       }
+      store_piece(static_cast<Row*>(a.row_out) + static_cast<size_t>(pos[s]) * a.d, c, a.d, q);
     }
   }
 #pragma unroll
@@ -342,12 +390,12 @@ __global__ __launch_bounds__(256) void return_backward_kernel(RowsArgs a) {
   if (in && s < a.topk) a.dw[static_cast<size_t>(t) * a.topk + s] = mine;
 }
 
-// threads a row: a piece each while that leaves none idle, at most a workgroup
+// threads a row: 16, 64 or a workgroup's 256, about a piece each
 template <typename F>
 void for_lanes(int d, F f) {
-  if (d <= 16 * 8)
+  if (d <= 128)
     f(std::integral_constant<int, 16>());
-  else if (d <= 128 * 8)
+  else if (d <= 1024)
     f(std::integral_constant<int, 64>());
   else
     f(std::integral_constant<int, 256>());

@@ -216,3 +216,17 @@ def test_gate_large_and_deterministic():
     again = torch.empty_like(w)
     mb.moe_gate(d, l, None, ids, again)
     assert torch.equal(w, again)
+
+
+@pytest.mark.parametrize("E,k", [(256, 8), (100, 3), (9, 8), (64, 1)])
+@pytest.mark.parametrize("base", [1.0, -1.0, 1e-30])
+def test_gate_close_keys(E, k, base):
+    """Logits that differ in the last few bits only: picks out of order in their upper 24 bits,
+    and borders that many keys share."""
+    r = np.random.default_rng([E, k])
+    one = np.float32(base).view(np.int32)
+    l = (one + r.integers(0, 600, (300, E))).astype(np.int32).view(np.float32)
+    l[::3] = (one + r.integers(0, 4, (100, E)) * 100).astype(np.int32).view(np.float32)
+    l[1::3, : E // 2] = r.standard_normal((100, E // 2)).astype(np.float32)
+    _check(l, k, "softmax", 1)
+    _check(l, k, "sigmoid", 0, (1e-7 * r.standard_normal(E)).astype(np.float32))
