@@ -11,9 +11,10 @@
 //
 // Sixteen lanes hold a row (lanes16.h), four rows a wave. The forward takes the largest
 // key in each of topk rounds, and lane s keeps pick s. Its rounds run on words of a key's
-// upper 24 bits and the column (the lower one above): all words differ, so the largest
-// below m is the largest word - m as an unsigned number, one subtraction a word in place of
-// finding and striking out a column. Where the lower 8 bits could matter (a pick out of
+// upper 24 bits and the column (the lower one above), which all differ: a lane sorts its
+// four largest, a round takes the largest of the 16 lanes' first ones and the lane that had it
+// moves up (65536 x 256, topk 8: 750 vector instructions for four rows when each round went
+// through all words, 510 so). Where the lower 8 bits could matter (a pick out of
 // order with the next, or keys at the border that agree in 24 bits only) the wave takes
 // the rounds on whole keys. The backward fills the row in LDS (zeros, or softmax's dense
 // part), adds the picks' terms there and stores it whole.
@@ -74,7 +75,9 @@ struct GateArgs {
   int T, E, topk, score, renorm;
 };
 
-// a row's largest logit (0 if there is none) and its sum of exp(l - m)
+// A row's largest logit (0 if there is none) and its sum of exp(l - m). For the sum alone the
+// hardware's exp2 of the rounded product will do: a term is off by |l - m| 2.3 2^-24 then, which
+// weighted by the terms is 8 2^-24 at most (256 terms: the mean of |l - m| stays below 3.4).
 template <int kNI>
 __device__ __forceinline__ void softmax_row(const Row<kNI>& l, float& m, float& total, Row<kNI>* p) {
   m = l.v[0];
@@ -85,7 +88,7 @@ __device__ __forceinline__ void softmax_row(const Row<kNI>& l, float& m, float& 
   total = 0.0f;
 #pragma unroll
   for (int i = 0; i < 4 * kNI; ++i) {
-    const float e = exp_near(l.v[i] - m);
+    const float e = p ? exp_near(l.v[i] - m) : __builtin_amdgcn_exp2f((l.v[i] - m) * 1.44269504088896341f);
     if (p) p->v[i] = e;
     total += e;
   }
@@ -141,76 +144,112 @@ __device__ __forceinline__ int pick_exact(uint32_t (&key)[4 * kNI], int topk, in
   return id;
 }
 
+__device__ __forceinline__ void descend(uint32_t& a, uint32_t& b) {
+  const uint32_t t = max(a, b);
+  b = min(a, b);
+  a = t;
+}
+__device__ __forceinline__ void sort4(uint32_t (&v)[4]) {
+  descend(v[0], v[1]);
+  descend(v[2], v[3]);
+  descend(v[0], v[2]);
+  descend(v[1], v[3]);
+  descend(v[1], v[2]);
+}
+// the four largest of a and b, all descending
+__device__ __forceinline__ void merge4(uint32_t (&a)[4], const uint32_t (&b)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = max(a[i], b[3 - i]);
+  descend(a[0], a[2]);
+  descend(a[1], a[3]);
+  descend(a[0], a[1]);
+  descend(a[2], a[3]);
+}
+// A lane's four largest words, or those below `below`, descending (0: no more)
+template <int kNI, bool kBelow>
+__device__ __forceinline__ void largest_words(const uint32_t (&key)[4 * kNI], int j, uint32_t below,
+                                              uint32_t (&best)[4]) {
+#pragma unroll
+  for (int i = 0; i < kNI; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      w[c] = (key[4 * i + c] & 0xffffff00u) | (255u - (i * 64 + 4 * j + c));
+      if (kBelow) w[c] = w[c] < below ? w[c] : 0u;
+    }
+    sort4(w);
+    if (i > 0) {
+      merge4(best, w);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) best[c] = w[c];
+    }
+  }
+}
+
 template <int kNI>
-__global__ __launch_bounds__(256) void gate_kernel(GateArgs a) {
+__global__ __launch_bounds__(256, 7) void gate_kernel(GateArgs a) {
   const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
   const int E = a.E;
-  Row<kNI> bias;
+  // the lanes of a row stay together, and so do the four rows of a wave (those behind the
+  // last row take the last one)
+  const int row = blockIdx.x * kGateRows + group;
+  const float* lrow = a.logits + static_cast<size_t>(min(row, a.T - 1)) * E;
+  Row<kNI> l;
+  load_row<kNI>(a.logits, min(row, a.T - 1), E, j, l);
+  float top = 0.0f, total = 1.0f;
+  if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) softmax_row<kNI>(l, top, total, nullptr);
+  if (a.bias) {
+    Row<kNI> bias;
+    load_row<kNI>(a.bias, 0, E, j, bias);
 #pragma unroll
-  for (int i = 0; i < 4 * kNI; ++i) bias.v[i] = 0.0f;
-  if (a.bias) load_row<kNI>(a.bias, 0, E, j, bias);
-  const int step = kGateRows * gridDim.x;
-  int row = blockIdx.x * kGateRows + group;
-  Row<kNI> next;
-  load_row<kNI>(a.logits, min(row, a.T - 1), E, j, next);
-  // the lanes of a row stay together, and so do the four rows of a wave (the loads
-  // past the last row are of the last row)
-  for (int base = blockIdx.x * kGateRows; base < a.T; base += step, row += step) {
-    const Row<kNI> l = next;
-    load_row<kNI>(a.logits, min(row + step, a.T - 1), E, j, next);
-    const float* lrow = a.logits + static_cast<size_t>(min(row, a.T - 1)) * E;
-    uint32_t key[4 * kNI];
+    for (int i = 0; i < 4 * kNI; ++i) l.v[i] += bias.v[i];
+  }
+  uint32_t key[4 * kNI];
 #pragma unroll
-    for (int i = 0; i < 4 * kNI; ++i) key[i] = order_key(a.bias ? l.v[i] + bias.v[i] : l.v[i]);
-    uint32_t word[4 * kNI], m = 0;
+  for (int i = 0; i < 4 * kNI; ++i) key[i] = order_key(l.v[i]);
+  uint32_t best[4];  // the lane's largest words, descending
+  largest_words<kNI, false>(key, j, 0, best);
+  // lane s: the word of rank s, up to rank topk (there are at least 64)
+  uint32_t m = row_max_u(best[0]), mine = m;
+  for (int s = 1; s <= a.topk; ++s) {
+    const bool taken = best[0] == m;
 #pragma unroll
-    for (int i = 0; i < 4 * kNI; ++i) {
-      const uint32_t e = (i >> 2) * 64 + 4 * j + (i & 3);
-      word[i] = (key[i] & 0xffffff00u) | (255u - e);
-      m = max(m, word[i]);
+    for (int c = 0; c < 4; ++c) best[c] = taken ? (c < 3 ? best[c + 1] : 0u) : best[c];
+    // a lane that gave four may have more: all that are left are below m
+    if (kNI > 1 && __any(best[0] == 0)) largest_words<kNI, true>(key, j, m, best);
+    m = row_max_u(best[0]);
+    if (j == s) mine = m;
+  }
+  int id = mine <= kNever ? -1 : 255 - static_cast<int>(mine & 255u);
+  float v = id >= 0 ? lrow[id] : -INFINITY;
+  {
+    // the picks' whole keys have to descend, and behind the last pick all keys that share
+    // its 24 bits have to be equal to it
+    const uint32_t exact = id >= 0 ? order_key(a.bias ? v + a.bias[id] : v) : 0u;
+    const uint32_t after = static_cast<uint32_t>(
+        __builtin_amdgcn_update_dpp(0, static_cast<int>(exact), 0x101, 0xf, 0xf, true));  // lane + 1
+    bool bad = j < a.topk && exact < after;
+    const int first = threadIdx.x & 48;  // the row's lane 0
+    const uint32_t last = __shfl(mine, first + a.topk - 1, kWave), edge = __shfl(mine, first + a.topk, kWave);
+    const bool tie = last >> 8 == edge >> 8 && edge > kNever;
+    if (__any(tie)) {
+      const uint32_t whole = __shfl(exact, first + a.topk - 1, kWave);
+#pragma unroll
+      for (int i = 0; i < 4 * kNI; ++i) bad = bad || (tie && key[i] >> 8 == last >> 8 && key[i] != whole);
     }
-    m = row_max_u(m);
-    // lane s: the word of rank s, up to rank topk (there are at least 64)
-    uint32_t mine = m;
-    for (int s = 1; s <= a.topk; ++s) {
-      uint32_t d = 0;
-#pragma unroll
-      for (int i = 0; i < 4 * kNI; ++i) d = max(d, word[i] - m);
-      m += row_max_u(d);
-      if (j == s) mine = m;
+    if (__any(bad)) {
+      id = pick_exact<kNI>(key, a.topk, j);
+      v = id >= 0 ? lrow[id] : -INFINITY;
     }
-    int id = mine <= kNever ? -1 : 255 - static_cast<int>(mine & 255u);
-    float v = id >= 0 ? lrow[id] : -INFINITY;
-    {
-      // the picks' whole keys have to descend, and behind the last pick all keys that share
-      // its 24 bits have to be equal to it
-      const uint32_t exact = id >= 0 ? order_key(a.bias ? v + a.bias[id] : v) : 0u;
-      const uint32_t after = static_cast<uint32_t>(
-          __builtin_amdgcn_update_dpp(0, static_cast<int>(exact), 0x101, 0xf, 0xf, true));  // lane + 1
-      bool bad = j < a.topk && exact < after;
-      const int first = threadIdx.x & 48;  // the row's lane 0
-      const uint32_t last = __shfl(mine, first + a.topk - 1, kWave), edge = __shfl(mine, first + a.topk, kWave);
-      const bool tie = last >> 8 == edge >> 8 && edge > kNever;
-      if (__any(tie)) {
-        const uint32_t whole = __shfl(exact, first + a.topk - 1, kWave);
-#pragma unroll
-        for (int i = 0; i < 4 * kNI; ++i) bad = bad || (tie && key[i] >> 8 == last >> 8 && key[i] != whole);
-      }
-      if (__any(bad)) {
-        id = pick_exact<kNI>(key, a.topk, j);
-        v = id >= 0 ? lrow[id] : -INFINITY;
-      }
-    }
-    float top = 0.0f, total = 1.0f;
-    if (a.score == MOE_SCORE_SOFTMAX && !a.renorm) softmax_row<kNI>(l, top, total, nullptr);
-    const bool on = id >= 0 && j < a.topk;
-    float slope;
-    const float w = pick_weight(v, on, a.score, a.renorm, top, total, slope);
-    if (j < a.topk && row < a.T) {
-      const size_t at = static_cast<size_t>(row) * a.topk + j;
-      a.ids[at] = id;
-      a.w[at] = w;
-    }
+  }
+  const bool on = id >= 0 && j < a.topk;
+  float slope;
+  const float w = pick_weight(v, on, a.score, a.renorm, top, total, slope);
+  if (j < a.topk && row < a.T) {
+    const size_t at = static_cast<size_t>(row) * a.topk + j;
+    a.ids[at] = id;
+    a.w[at] = w;
   }
 }
 
@@ -233,76 +272,62 @@ template <int kNI, bool kDense>
 __global__ __launch_bounds__(256) void gate_backward_kernel(GateBackwardArgs a) {
   __shared__ __attribute__((aligned(16))) float rows[kGateRows][64 * kNI];
   const int j = threadIdx.x & 15, group = threadIdx.x >> 4;
-  const int E = a.E, step = kGateRows * gridDim.x;
+  const int E = a.E, row = blockIdx.x * kGateRows + group;
   float* mine = rows[group];
-  Row<kNI> next;
-  int next_id = -1;
-  float next_dw = 0.0f;
-  const auto load = [&](int row) {
-    next_id = -1;
-    if (row < a.T) {
-      if (j < a.topk) {
-        next_id = a.ids[static_cast<size_t>(row) * a.topk + j];
-        next_dw = a.dw[static_cast<size_t>(row) * a.topk + j];
-      }
-      if constexpr (kDense) load_row<kNI>(a.logits, row, E, j, next);
+  int id = -1;
+  float dw = 0.0f;
+  if (row < a.T && j < a.topk) {
+    id = a.ids[static_cast<size_t>(row) * a.topk + j];
+    dw = a.dw[static_cast<size_t>(row) * a.topk + j];
+  }
+  Row<kNI> l;
+  if constexpr (kDense) load_row<kNI>(a.logits, min(row, a.T - 1), E, j, l);
+  const bool in = row < a.T, on = id >= 0 && id < E;
+  const float v = on ? a.logits[static_cast<size_t>(row) * E + id] : -INFINITY;
+  float m = 0.0f, total = 1.0f;
+  Row<kNI> p;
+  if constexpr (kDense) softmax_row<kNI>(l, m, total, &p);
+  float slope;
+  const float w = pick_weight(v, on, a.score, a.renorm, m, total, slope);
+  const float g = on ? dw : 0.0f;
+  const float mean = kDense || a.renorm ? row_sum(on ? g * w : 0.0f) : 0.0f;
+  // the row in LDS: its 16 lanes are of one wave
+#pragma unroll
+  for (int i = 0; i < kNI; ++i) {
+    f32x4_t q = {0, 0, 0, 0};
+    if constexpr (kDense) {
+      const float scale = total == 0.0f ? 0.0f : -mean / total;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) q[c] = p.v[4 * i + c] * scale;
     }
-  };
-  int row = blockIdx.x * kGateRows + group;
-  load(row);
-  for (int base = blockIdx.x * kGateRows; base < a.T; base += step, row += step) {
-    const int id = next_id;
-    const float dw = next_dw;
-    const Row<kNI> l = next;
-    load(row + step);
-    const bool in = row < a.T, on = id >= 0 && id < E;
-    const float v = on ? a.logits[static_cast<size_t>(row) * E + id] : -INFINITY;
-    float m = 0.0f, total = 1.0f;
-    Row<kNI> p;
-    if constexpr (kDense) softmax_row<kNI>(l, m, total, &p);
-    float slope;
-    const float w = pick_weight(v, on, a.score, a.renorm, m, total, slope);
-    const float g = on ? dw : 0.0f;
-    const float mean = kDense || a.renorm ? row_sum(on ? g * w : 0.0f) : 0.0f;
-    // the row in LDS: its 16 lanes are of one wave
+    *reinterpret_cast<f32x4_t*>(mine + 64 * i + 4 * j) = q;
+  }
+  wave_sync();
+  if (on) atomicAdd(&mine[id], kDense ? w * g : w * slope * (g - mean));  // the same id twice adds up
+  wave_sync();
+  if (in) {
+    const size_t at = static_cast<size_t>(row) * E;
 #pragma unroll
     for (int i = 0; i < kNI; ++i) {
-      f32x4_t q = {0, 0, 0, 0};
-      if constexpr (kDense) {
-        const float scale = total == 0.0f ? 0.0f : -mean / total;
+      const int e = 64 * i + 4 * j;
+      f32x4_t q = *reinterpret_cast<const f32x4_t*>(mine + e);
+      if (e + 4 <= E) {
+        if (a.dadd) q += *reinterpret_cast<const f32x4_any_t*>(a.dadd + at + e);
+        __builtin_nontemporal_store(q, reinterpret_cast<f32x4_any_t*>(a.dlogits + at + e));
+      } else {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) q[c] = p.v[4 * i + c] * scale;
-      }
-      *reinterpret_cast<f32x4_t*>(mine + 64 * i + 4 * j) = q;
-    }
-    wave_sync();
-    if (on) atomicAdd(&mine[id], kDense ? w * g : w * slope * (g - mean));  // the same id twice adds up
-    wave_sync();
-    if (in) {
-      const size_t at = static_cast<size_t>(row) * E;
-#pragma unroll
-      for (int i = 0; i < kNI; ++i) {
-        const int e = 64 * i + 4 * j;
-        f32x4_t q = *reinterpret_cast<const f32x4_t*>(mine + e);
-        if (e + 4 <= E) {
-          if (a.dadd) q += *reinterpret_cast<const f32x4_any_t*>(a.dadd + at + e);
-          *reinterpret_cast<f32x4_any_t*>(a.dlogits + at + e) = q;
-        } else {
-#pragma unroll
-          for (int c = 0; c < 3; ++c)
-            if (e + c < E) a.dlogits[at + e + c] = a.dadd ? q[c] + a.dadd[at + e + c] : q[c];
-        }
+        for (int c = 0; c < 3; ++c)
+          if (e + c < E) a.dlogits[at + e + c] = a.dadd ? q[c] + a.dadd[at + e + c] : q[c];
       }
     }
-    wave_sync();
   }
 }
 
-// enough workgroups to fill the CUs several times over
-unsigned gate_grid(int T) {
-  const int n = (T + kGateRows - 1) / kGateRows;
-  return static_cast<unsigned>(n < 2048 ? n : 2048);
-}
+// A workgroup a kGateRows rows, no loop: the scheduler keeps some waves loading while others
+// compute. 2048 workgroups in a loop, the next rows' loads ahead: 65536 x 256 27 and 25 us in place of
+// 19 and 21 (floors 14 and 26 at a copy's 5.1 TB/s: the gradient's stores pass the caches, with
+// which they took 2 us longer). The forward is bound by its vector instructions, 14 us of them.
+inline unsigned gate_grid(int T) { return static_cast<unsigned>((T + kGateRows - 1) / kGateRows); }
 
 template <typename F>
 void for_width(int E, F f) {

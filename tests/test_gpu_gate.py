@@ -230,3 +230,24 @@ def test_gate_close_keys(E, k, base):
     l[1::3, : E // 2] = r.standard_normal((100, E // 2)).astype(np.float32)
     _check(l, k, "softmax", 1)
     _check(l, k, "sigmoid", 0, (1e-7 * r.standard_normal(E)).astype(np.float32))
+
+
+@pytest.mark.parametrize("E,k", [(256, 8), (255, 5), (128, 8), (97, 7), (64, 8)])
+@pytest.mark.parametrize("group", [4, 16])
+def test_gate_picks_close_together(E, k, group):
+    """The largest logits in columns 64 i + 4 j + c of few j: all picks fall to one lane or two,
+    up to whole rows of one value, of -inf and of NaN in those columns."""
+    r = np.random.default_rng([E, k, group])
+    l = r.standard_normal((200, E)).astype(np.float32)
+    col = np.arange(E)
+    for t in range(200):
+        mine = col % 64 // group == r.integers(0, 64 // group)
+        l[t, mine] += 20
+        if t % 5 == 1:
+            l[t, mine] = 20
+        if t % 5 == 2:
+            l[t, ~mine] = -np.inf
+        if t % 5 == 3:
+            l[t, np.nonzero(mine)[0][:3]] = -np.inf
+    _check(l, k, "softmax", 0)
+    _check(l, k, "sigmoid", 1, r.standard_normal(E).astype(np.float32))
