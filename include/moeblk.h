@@ -676,7 +676,7 @@ int moe_sort(const moe_rows_dims* dims, const int32_t* topk_ids, int32_t* counts
 
 /* The tokens' rows in sorted order: xs[pick_pos[t][s]] = x[t] for every place with
  * pick_pos in [0, R).
- *   x [T, d] tok_type; pick_pos moe_sort's;
+ *   x [T, d] tok_type; pick_pos moe_sort's (no position twice);
  *   xs [R, d] row_type, written for the rows some pick has; other rows are left as they
  *      were. One rounding where row_type is the smaller.
  * Its gradient is moe_return without weights. */
@@ -695,7 +695,8 @@ int moe_return(const moe_rows_dims* dims, const void* y, const float* topk_w,
 /* The gradient of moe_return:
  *   dy[pick_pos[t][s]] = topk_w[t][s] * dout[t],  dtopk_w[t][s] = <dout[t], y[pick_pos[t][s]]>
  * (fp32 sums in a fixed order), 0 for a slot without a sorted row.
- *   dout [T, d] tok_type; y, topk_w, pick_pos as given to moe_return (topk_w not NULL);
+ *   dout [T, d] tok_type; y, topk_w, pick_pos as given to moe_return (topk_w not NULL, no
+ *   position twice);
  *   dy [R, d] row_type, written for the rows some pick has; dtopk_w [T, topk] fp32,
  *   written. */
 int moe_return_backward(const moe_rows_dims* dims, const void* dout, const void* y,

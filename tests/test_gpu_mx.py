@@ -268,6 +268,66 @@ def test_gemm_workspace_is_left_ready():
             assert torch.equal(a, b)
 
 
+def test_products_in_graphs_that_share_a_workspace():
+    """Two captured products of one workspace, replayed in turn on new rows, eager calls on the
+    same workspace between; split over K and not, quantised in the kernel and in front of it."""
+    sizes = [(1, 512, 8192), (64, 256, 8192), (300, 500, 4096), (300, 4096, 1024), (40, 130, 300)]
+    dims = [mb.mx_dims_from(dict(M=M, N=N, K=K, out_type=mb.MOE_FP32)) for M, N, K in sizes]
+    ws = torch.zeros(max(mb.moe_mx_proj_workspace_bytes(d) for d in dims), dtype=torch.uint8, device="cuda")
+    calls = []
+    for d in dims:
+        q, s, _ = _weight(d.N, d.K, 4)
+        packed = torch.empty(mb.moe_packed_mx_bytes(d), dtype=torch.uint8, device="cuda")
+        mb.moe_pack_mx(d, torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), packed)
+        x = _rows(d.M, d.K, "bf16", 4).cuda()
+        calls.append((d, x, packed, torch.empty((d.M, d.N), device="cuda"), ws))
+    stream = torch.cuda.Stream()
+    graphs = []
+    torch.cuda.synchronize()
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            mb.moe_mx_proj(*c)
+        graphs.append(g)
+    for i in range(3):
+        for c in calls:
+            c[1].copy_(_rows(c[0].M, c[0].K, "bf16", 10 + i))
+        want = []
+        for c in calls:
+            mb.moe_mx_proj(*c)
+            want.append(c[3].clone())
+            c[3].zero_()
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(c[3], w) for c, w in zip(calls, want)), i
+
+
+def test_products_on_two_streams():
+    """Calls at once, each with its own workspace."""
+    M, N, K = 16, 1024, 8192
+    d = mb.mx_dims_from(dict(M=M, N=N, K=K, out_type=mb.MOE_FP32))
+    q, s, _ = _weight(N, K, 6)
+    packed = torch.empty(mb.moe_packed_mx_bytes(d), dtype=torch.uint8, device="cuda")
+    mb.moe_pack_mx(d, torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), packed)
+    xs = [_rows(M, K, "bf16", i).cuda() for i in range(2)]
+    ws = [torch.zeros(mb.moe_mx_proj_workspace_bytes(d), dtype=torch.uint8, device="cuda") for _ in xs]
+    want = []
+    for x, w in zip(xs, ws):
+        out = torch.empty((M, N), device="cuda")
+        mb.moe_mx_proj(d, x, packed, out, w)
+        want.append(out)
+    streams = [torch.cuda.Stream() for _ in xs]
+    outs = [[torch.zeros((M, N), device="cuda") for _ in range(20)] for _ in xs]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for x, w, o, st in zip(xs, ws, outs, streams):
+            mb.moe_mx_proj(d, x, packed, o[i], w, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for w, many in zip(want, outs) for o in many)
+
+
 def test_quant_behind_2_to_32_bytes():
     M, K = 262144, 16384
     x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")

@@ -152,6 +152,29 @@ def test_down(T, E, k, n, d, I, counts, out_type):  # noqa: E741
         assert (np.abs(got - ref) <= rm.product_tol(mag, I) + rm.half_step("bf16" if bf else "fp32") * np.abs(ref) * 1.01).all()
 
 
+# wide weights of many experts: the tiles of 256 x 256, whose last one takes up to 320 rows
+MANY = [0, 1, 64, 65, 128, 129, 192, 193, 255, 256, 257, 319, 320, 321, 384, 385, 511, 512, 513, 576, 577, 40, 0, 0, 7, 100,
+        31, 32, 33, 2, 0, 3]
+LARGE = [
+    (1000, 32, 8, 32, 128, 896, MANY),
+    (1000, 32, 8, 32, 1792, 128, MANY),
+    (64, 32, 8, 32, 1920, 896, None),
+    (8000, 8, 1, 8, 1792, 896, [1000, 1025, 1088, 1089, 0, 1300, 1000, 1498]),
+]
+
+
+@pytest.mark.parametrize("h_type", [mb.MOE_BF16, mb.MOE_MXFP4])
+@pytest.mark.parametrize("T,E,k,n,d,I,counts", LARGE)
+def test_gate_up_of_wide_experts(T, E, k, n, d, I, counts, h_type):  # noqa: E741
+    test_gate_up(T, E, k, n, d, I, counts, h_type)
+
+
+@pytest.mark.parametrize("out_type", [mb.MOE_BF16, mb.MOE_FP32])
+@pytest.mark.parametrize("T,E,k,n,d,I,counts", LARGE)
+def test_down_of_wide_experts(T, E, k, n, d, I, counts, out_type):  # noqa: E741
+    test_down(T, E, k, n, d, I, counts, out_type)
+
+
 def test_gate_up_of_rows_that_are_not_finite():
     """A NaN row stays alone; its MXFP4 blocks are NaN with zero codes."""
     for T in (20, 300):
@@ -350,3 +373,50 @@ def test_path_repeats_bit_for_bit():
         p.step()
         got = p.result()
         assert all(torch.equal(got[key], want[key]) for key in p.OUT)
+
+
+def test_experts_of_a_graph_replayed():
+    """The kernels of wide experts and of one expert's few rows, captured and replayed on other
+    offsets and rows than they were captured with."""
+    for T, E, k, n, d, I, all_counts in (  # noqa: E741
+        (1000, 32, 8, 32, 1792, 896, [MANY, MANY[::-1], [0] * 32, [8000] + [0] * 31]),
+        (20, 8, 2, 2, 256, 128, [[20, 20], [0, 1], [0, 0], [17, 0]]),
+    ):
+        md = _group(T, E, k, n, d, I)
+        w13, _ = _expert_weights(n, 2 * I, d, mb.MOE_W13, d, I, 5)
+        w2, _ = _expert_weights(n, d, I, mb.MOE_W2, d, I, 6)
+        code, sc = _x(T, d, 7)
+        xq, xs = _cuda(rm.mx_pack(code)), _cuda(sc)
+        R = T * k
+        off, rows = torch.zeros(n + 1, dtype=torch.int32, device="cuda"), torch.zeros(R, dtype=torch.int32, device="cuda")
+        hq = torch.zeros((R, I // 2), dtype=torch.uint8, device="cuda")
+        hs = torch.zeros((R, I // 32), dtype=torch.uint8, device="cuda")
+        y = torch.zeros((R, d), dtype=torch.bfloat16, device="cuda")
+
+        def step(stream=None):
+            mb.moe_mx_gate_up(md, xq, xs, off, rows, w13, hq, hs, stream=stream)
+            mb.moe_mx_down(md, hq, hs, off, w2, y, stream=stream)
+
+        def put(i):
+            o, r = _counts_to_rows(all_counts[i], T, k, i)
+            off.copy_(torch.from_numpy(o))
+            rows.copy_(torch.from_numpy(r))
+            for t in (hq, hs, y):
+                t.zero_()
+
+        stream = torch.cuda.Stream()
+        put(0)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+        for i in (1, 0, 2, 3, 0):
+            put(i)
+            step()
+            want = [t.clone() for t in (hq, hs, y)]
+            put(i)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip((hq, hs, y), want):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (T, i)
