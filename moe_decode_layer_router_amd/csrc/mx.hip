@@ -14,7 +14,8 @@ namespace {
 // ---------------------------------------------------------------- quantise, read back
 //
 // One pass over the rows, bound by memory. Two lanes share a block: 16 columns each,
-// one DPP step for the maximum, 8 bytes of codes a lane.
+// one DPP step for the maximum, 8 bytes of codes a lane. 16384 rows of 7168: 45 us from bf16
+// and 95 from fp32 (6.6 and 5.6 TB/s); 8 x 4096 2.4 us.
 
 template <typename T>
 __global__ __launch_bounds__(256) void mx_quant_kernel(const T* __restrict__ x,
