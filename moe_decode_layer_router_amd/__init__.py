@@ -558,9 +558,13 @@ _torch = None
 
 
 def _t() -> _Torch:
-    global _torch
+    global _torch, _buf
     if _torch is None:
         _torch = _Torch()
+        try:  # the same check in C (csrc/marshal.cpp); it links against the torch it was built with
+            from ._marshal import buf as _buf
+        except ImportError:
+            pass
     return _torch
 
 

@@ -1,16 +1,19 @@
-"""Build ``libmoeblk.so`` (all HIP sources, gfx950 only) in-tree with hipcc."""
+"""Build ``libmoeblk.so`` (all HIP sources, gfx950 only) in-tree with hipcc, and the
+binding's argument check (``_marshal.so``, host code) with g++."""
 
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoeblk.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep hipcc from emitting v_pk_{add,mul,fma}_f32 (hipcc's
@@ -51,5 +54,27 @@ def build_library(verbose: bool = False, extra_flags: list[str] | None = None) -
     return LIB
 
 
+def build_marshal(verbose: bool = False) -> str:
+    import torch
+    from torch.utils import cpp_extension
+
+    tmp = MARSHAL + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall"]
+    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f"-isystem{i}" for i in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"])]
+    cmd += [os.path.join(CSRC, "marshal.cpp"), "-o", tmp]
+    cmd += [f"-L{p}" for p in cpp_extension.library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stderr}")
+    if verbose and res.stderr.strip():
+        print(res.stderr)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 if __name__ == "__main__":
     print(build_library(verbose=True))
+    print(build_marshal(verbose=True))
