@@ -30,6 +30,7 @@
 
 #include <type_traits>
 
+#include "mx_copy.h"
 #include "mx_dev.h"
 
 namespace moeblk {
@@ -120,38 +121,31 @@ __device__ __forceinline__ void mx_tile_body(const MxTile& p, F row_of, uint8_t*
     soff[i] = static_cast<uint32_t>(row_of(64 * min(wave + i * kWaves, BM / 64 - 1) + lane)) * (Kc * 4u);
   // Copies of weight chunk k, of token unit u (chunks 2 u, 2 u + 1), of scale unit v (chunks
   // 4 v .. 4 v + 3), all counted from p.c0; behind the last chunk they read nothing (an offset
-  // behind every buffer) or what is not used.
-  constexpr uint32_t kPast = 1u << 31;
+  // behind every buffer) or what is not used (mx_copy.h).
   const int n = p.c1 - p.c0;
   const auto copy_w = [&](int i, int k) {
     uint8_t* to = lds + (k & (kWRing - 1)) * S::kWBuf;
-    const uint32_t past = k < n ? 0u : kPast;
-    const int c = min(p.c0 + k, Kc - 1);
     if (i < kW) {
       const int q = wave + i * kWaves;  // piece: row tile of 16
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          wr, (mx_lptr_t)(to + q * 1024), 16, (lane * 16) | past,
-          (min(q >> 2, blocks - 1) * Kc + c) * kMxTileBytes + (q & 3) * 1024, 0, 0);
+      const MxCopy at = mx_w_copy(lane * 16, p.c0, n, k, Kc, q >> 2, blocks, kMxTileBytes, (q & 3) * 1024);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (mx_lptr_t)(to + q * 1024), 16, at.lane, at.scalar, 0, 0);
     } else {
       const int q = (wave + (i - kW) * kWaves) % (BN / 64);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (mx_lptr_t)(to + BN * 64 + q * 256), 4,
-                                               (lane * 4) | past,
-                                               (min(q, blocks - 1) * Kc + c) * kMxTileBytes + 4096, 0, 0);
+      const MxCopy at = mx_w_copy(lane * 4, p.c0, n, k, Kc, q, blocks, kMxTileBytes, 4096);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (mx_lptr_t)(to + BN * 64 + q * 256), 4, at.lane, at.scalar, 0, 0);
     }
   };
   const auto copy_x = [&](int i, int u) {
-    const uint32_t past = 2 * u < n ? 0u : kPast;
+    const MxCopy at = mx_x_copy(xoff[i], p.c0, n, u);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        xr, (mx_lptr_t)(lds + S::kXAt + (u & 1) * S::kXBuf + (wave + i * kWaves) * 1024), 16,
-        xoff[i] | past, (p.c0 + 2 * u) * 64, 0, 0);
+        xr, (mx_lptr_t)(lds + S::kXAt + (u & 1) * S::kXBuf + (wave + i * kWaves) * 1024), 16, at.lane, at.scalar, 0, 0);
   };
   const auto copy_s = [&](int i, int v, bool real = true) {  // !real: reads nothing
     const int q = wave + i * kWaves;
     real = real && q < BM / 64;  // with fewer pieces than waves some have none
-    const uint32_t past = 4 * v < n && real ? 0u : kPast;
-    const int at = real ? (v & 1) * S::kSBuf + q * 1024 : kXRing * S::kSBuf;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (mx_lptr_t)(lds + S::kSAt + at), 16, soff[i] | past,
-                                             (p.c0 + 4 * v) * 4, 0, 0);
+    const MxCopy at = mx_s_copy(soff[i], p.c0, real ? n : 0, v);
+    const int to = real ? (v & 1) * S::kSBuf + q * 1024 : kXRing * S::kSBuf;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(sr, (mx_lptr_t)(lds + S::kSAt + to), 16, at.lane, at.scalar, 0, 0);
   };
 
   // operand reads of step k
