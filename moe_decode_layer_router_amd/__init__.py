@@ -562,9 +562,12 @@ def _t() -> _Torch:
     if _torch is None:
         _torch = _Torch()
         try:  # the same check in C (csrc/marshal.cpp); it links against the torch it was built with
-            from ._marshal import buf as _buf
+            from . import _marshal
         except ImportError:
             pass
+        else:
+            _marshal.set_python(_buf)  # for what it leaves to the check below
+            _buf = _marshal.buf
     return _torch
 
 

@@ -9,6 +9,10 @@
 
 namespace {
 
+// the check in Python, which takes what is left to it here: objects that are no torch tensors
+// but answer like one, and sizes beyond 64 bits
+PyObject* python_buf = nullptr;
+
 // buf(t, name, n, kinds, device): _buf in __init__.py
 PyObject* buf(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   if (nargs != 5 || !PyUnicode_Check(args[1]) || !(args[3] == Py_None || PyTuple_Check(args[3]))) {
@@ -20,10 +24,18 @@ PyObject* buf(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     Py_INCREF(o);
     return o;
   }
-  if (!THPVariable_Check(o))
+  if (!THPVariable_Check(o)) {
+    if (python_buf && PyObject_HasAttrString(o, "data_ptr")) return PyObject_Vectorcall(python_buf, args, nargs, nullptr);
     return PyErr_Format(PyExc_TypeError, "%U: %S is not a tensor, None or a pointer", name, Py_TYPE(o));
-  const long long n = PyLong_AsLongLong(args[2]), device = PyLong_AsLongLong(args[4]);
-  if (PyErr_Occurred()) return nullptr;
+  }
+  const long long n = PyLong_AsLongLong(args[2]);
+  if (n == -1 && PyErr_Occurred()) {
+    if (!python_buf || !PyErr_ExceptionMatches(PyExc_OverflowError)) return nullptr;
+    PyErr_Clear();
+    return PyObject_Vectorcall(python_buf, args, nargs, nullptr);
+  }
+  const long long device = PyLong_AsLongLong(args[4]);
+  if (device == -1 && PyErr_Occurred()) return nullptr;
   try {
     const at::Tensor& t = THPVariable_Unpack(o);
     if (t.get_device() != device)
@@ -44,8 +56,16 @@ PyObject* buf(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   }
 }
 
+PyObject* set_python(PyObject*, PyObject* f) {
+  Py_INCREF(f);
+  Py_XSETREF(python_buf, f);
+  Py_RETURN_NONE;
+}
+
 PyMethodDef methods[] = {
-    {"buf", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(buf)), METH_FASTCALL, nullptr}, {nullptr}};
+    {"buf", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(buf)), METH_FASTCALL, nullptr},
+    {"set_python", set_python, METH_O, nullptr},
+    {nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods};
 
 }  // namespace
