@@ -561,14 +561,23 @@ def _t() -> _Torch:
     global _torch, _buf
     if _torch is None:
         _torch = _Torch()
-        try:  # the same check in C (csrc/marshal.cpp); it links against the torch it was built with
-            from . import _marshal
-        except ImportError:
-            pass
-        else:
-            _marshal.set_python(_buf)  # for what it leaves to the check below
-            _buf = _marshal.buf
+        _buf = _check_in_c(_buf)
     return _torch
+
+
+def _check_in_c(python_buf):
+    """The same check in C (csrc/marshal.cpp), where it is built for this torch: it reads
+    tensors by the layout it was compiled with."""
+    import torch
+
+    try:
+        from . import _marshal
+    except ImportError:
+        return python_buf
+    if getattr(_marshal, "torch_build", None) != f"{torch.__version__} {torch.version.git_version}":
+        return python_buf
+    _marshal.set_python(python_buf)  # for what it leaves to it
+    return _marshal.buf
 
 
 def _buf(t, name: str, n: int, kinds, device: int):

@@ -1,11 +1,12 @@
 """Build ``libmoeblk.so`` (all HIP sources, gfx950 only) in-tree with hipcc, and the
-binding's argument check (``_marshal.so``, host code) with g++."""
+binding's argument check (``_marshal``, host code) with g++."""
 
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -13,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoeblk.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))  # of this Python alone
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep hipcc from emitting v_pk_{add,mul,fma}_f32 (hipcc's
@@ -54,21 +55,32 @@ def build_library(verbose: bool = False, extra_flags: list[str] | None = None) -
     return LIB
 
 
-def build_marshal(verbose: bool = False) -> str:
-    import torch
-    from torch.utils import cpp_extension
-
+def build_marshal(verbose: bool = False) -> str | None:
+    """The check in C, for the Python and torch that build it. None, with a message, where that
+    fails (no g++, or no headers): the binding then checks in Python, and finds no older file."""
+    for old in (MARSHAL, os.path.join(PKG, "_marshal.so")):  # the latter: of any Python
+        if os.path.exists(old):
+            os.remove(old)
     tmp = MARSHAL + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall"]
-    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
-    cmd += [f"-isystem{i}" for i in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"])]
-    cmd += [os.path.join(CSRC, "marshal.cpp"), "-o", tmp]
-    cmd += [f"-L{p}" for p in cpp_extension.library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"g++ failed ({res.returncode}):\n{res.stderr}")
+    try:
+        import torch
+        from torch.utils import cpp_extension
+
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall"]
+        cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+        cmd += [f'-DMARSHAL_TORCH="{torch.__version__} {torch.version.git_version}"']
+        cmd += [f"-isystem{i}" for i in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"])]
+        cmd += [os.path.join(CSRC, "marshal.cpp"), "-o", tmp]
+        cmd += [f"-L{p}" for p in cpp_extension.library_paths()] + ["-ltorch_python", "-ltorch_cpu", "-lc10"]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        error = f"{cmd[0]} failed ({res.returncode})\n{res.stderr}" if res.returncode != 0 else ""
+    except (ImportError, OSError) as e:
+        error = str(e)
+    if error:
+        print(f"the binding's check in C is not built, the one in Python serves:\n{error}", file=sys.stderr)
+        return None
     if verbose and res.stderr.strip():
         print(res.stderr)
     os.replace(tmp, MARSHAL)

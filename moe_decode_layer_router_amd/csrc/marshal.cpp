@@ -70,4 +70,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+// torch_build: the torch whose layouts are compiled in; the binding asks before it uses buf
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_build", MARSHAL_TORCH) < 0) Py_CLEAR(m);
+  return m;
+}
