@@ -616,12 +616,13 @@ int moe_check_gate_dims(const moe_gate_dims* dims);
  *   topk_w   [T, topk] fp32, written, 0 beside an id of -1; with l the logits and P the
  *            token's picks:
  *              sigmoid: 1 / (1 + exp(-l)), with renorm divided by its sum over P;
- *              softmax: exp(l) / sum over all E of exp, with renorm over P. */
+ *              softmax: exp(l) / sum over all E of exp, with renorm over P.
+ *            A logit of NaN (softmax: or +inf) makes NaN of the weights whose formula it is in. */
 int moe_gate(const moe_gate_dims* dims, const float* logits, const float* bias, int32_t* topk_ids,
              float* topk_w, hipStream_t stream);
 
 /* Its gradient with respect to the logits, the picks held constant: with g = dtopk_w
- * and w the weights that moe_gate gives,
+ * and w the weights that moe_gate gives (the same bits),
  *   sigmoid            dlogits[p] = g_p w_p (1 - sigmoid(l_p))
  *   sigmoid, renorm    dlogits[p] = w_p (1 - sigmoid(l_p)) (g_p - sum_P g w)
  *   softmax            dlogits[e] = softmax(l)_e (sum of g over picks of e - sum_P g w)
