@@ -293,24 +293,38 @@ inline int64_t max_tiles(int64_t R, int n, int bm) {
 // and for up to 16 rows the register kernel, which splits K over its waves. One expert,
 // 128 x 128 / 64 x 64 / registers: 1 row 10.3 / 9.5 / 4.9, 16 rows 10.4 / 9.6 / 6.1, 64 rows 10.6 /
 // 9.7 / -, 100 rows 12.9 / 9.7 / -.
-template <bool kGateUp>
-void launch_group(const moe_mx_group_dims& m, const MxGroupArgs& a, hipStream_t stream) {
+enum GroupForm { kGroupFew, kGroup64, kGroup128, kGroup256 };
+
+GroupForm group_form(const moe_mx_group_dims& m, int N) {
   const int64_t picks = static_cast<int64_t>(m.T) * m.topk * m.n_local / m.E;  // that are local
   const int64_t per = static_cast<int64_t>(m.T) * m.topk / m.E;
   const int64_t active = picks < 1 ? 1 : picks < m.n_local ? picks : m.n_local;
+  const int64_t blocks = active * (N / kRowsPerBlock), tiles64 = blocks * ((per + 63) / 64);
+  const int64_t tiles256 = active * ((N + 255) / 256) * (per < 384 ? 1 : (per + 128) / 256);
+  if (blocks <= 256 && per <= kFewRows) return kGroupFew;
+  if (per >= 12 && tiles256 >= 200) return kGroup256;
+  return tiles64 <= 512 ? kGroup64 : kGroup128;
+}
+
+template <bool kGateUp>
+void launch_group(const moe_mx_group_dims& m, const MxGroupArgs& a, hipStream_t stream) {
   const auto grid = [&](int bm, int bn) {
     return static_cast<unsigned>(max_tiles(a.R, a.n, bm) * ((a.N + bn - 1) / bn));
   };
-  const int64_t blocks = active * (a.N / kRowsPerBlock), tiles64 = blocks * ((per + 63) / 64);
-  const int64_t tiles256 = active * ((a.N + 255) / 256) * (per < 384 ? 1 : (per + 128) / 256);
-  if (blocks <= 256 && per <= kFewRows)
-    mx_group_few_kernel<kGateUp><<<grid(kFewRows, 64), 64 * kFewWaves, 0, stream>>>(a);
-  else if (per >= 12 && tiles256 >= 200)
-    mx_group_tile_kernel<2, 5, 4, 2, 64, kGateUp><<<grid(256, 256), 512, 0, stream>>>(a);
-  else if (tiles64 <= 512)
-    mx_group_tile_kernel<2, 1, 1, 2, 0, kGateUp><<<grid(64, 64), 128, 0, stream>>>(a);
-  else
-    mx_group_tile_kernel<2, 2, 2, 2, 0, kGateUp><<<grid(128, 128), 256, 0, stream>>>(a);
+  switch (group_form(m, a.N)) {
+    case kGroupFew:
+      mx_group_few_kernel<kGateUp><<<grid(kFewRows, 64), 64 * kFewWaves, 0, stream>>>(a);
+      break;
+    case kGroup64:
+      mx_group_tile_kernel<2, 1, 1, 2, 0, kGateUp><<<grid(64, 64), 128, 0, stream>>>(a);
+      break;
+    case kGroup128:
+      mx_group_tile_kernel<2, 2, 2, 2, 0, kGateUp><<<grid(128, 128), 256, 0, stream>>>(a);
+      break;
+    case kGroup256:
+      mx_group_tile_kernel<2, 5, 4, 2, 64, kGateUp><<<grid(256, 256), 512, 0, stream>>>(a);
+      break;
+  }
 }
 
 }  // namespace
@@ -335,6 +349,12 @@ using namespace moeblk;
 extern "C" {
 
 int moe_check_mx_group_dims(const moe_mx_group_dims* dims) { return check_mx_group_dims(dims); }
+
+// The kernel that a product with N weight rows an expert takes (GroupForm), for tests: no part
+// of the interface.
+int moeblk_mx_group_form(const moe_mx_group_dims* dims, int N) {
+  return check_mx_group_dims(dims) ? -1 : group_form(*dims, N);
+}
 
 int moe_mx_gate_up(const moe_mx_group_dims* dims, const void* xq, const void* xs,
                    const int32_t* offsets, const int32_t* rows, const void* w13_packed, void* h,
