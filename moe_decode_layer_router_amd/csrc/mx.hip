@@ -145,7 +145,7 @@ constexpr int kRowsWaves = 8;
 
 template <int kTT, int kSrc>
 __global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(MxGemmArgs a) {
-  __shared__ f32x4_t red[mx_rows_red<kTT, kRowsWaves>()];
+  __shared__ f32x4_t red[mx_rows_red<kTT, kRowsWaves>];
   __shared__ __attribute__((aligned(16))) uint8_t pass[kSrc == kMxRowsQ ? 16 : kRowsWaves * kTT * kMxPass];
   __shared__ int last;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -154,8 +154,8 @@ __global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(MxGemmArgs a) 
   MxRowsTile p = {a.w + static_cast<size_t>(rb) * a.Kc * kMxTileBytes, a.Kc, 0, 0, t0, a.M};
   part_range(a.Kc, a.split.parts, part, p.c0, p.c1);
   f32x4_t sum[1];
-  static_assert(4 * kTT <= kRowsWaves, "a tile a wave");
-  mx_rows_body<kTT, kRowsWaves, (kTT == 2 && kSrc == kMxRowsFp32 ? 1 : 2), kSrc>(p, a.x, a.K, a.xq, a.xs, [](int t) { return t; }, pass, red, sum);
+  mx_rows_body<kTT, kRowsWaves, (kTT == 2 && kSrc == kMxRowsFp32 ? 1 : 2), kSrc>(
+      p, a.x, a.K, a.xq, a.xs, [](int t) { return t; }, pass, red, sum[0]);
   if (!join_parts(a.split, tile, part, true, sum, &last)) return;
   const int token = t0 + (wave % kTT) * 16 + (lane & 15), n0 = (4 * rb + wave / kTT) * 16 + 4 * (lane >> 4);
   if (token < a.M && wave < 4 * kTT)
@@ -163,13 +163,13 @@ __global__ __launch_bounds__(64 * kRowsWaves) void mx_rows_kernel(MxGemmArgs a) 
 }
 
 // a tile of up to 32 kT kWM rows from m0 on, on the narrowest instance that holds them
-template <int kQ, int kT, int kWN, int kWM, bool kSplit>
+template <int kT, int kWN, int kWM, bool kSplit>
 __device__ __forceinline__ void gemm_tile(const MxGemmArgs& a, int tn, int m0, int rows, int part, int tile,
                                           uint8_t* lds) {
-  using S = MxTileShape<kQ, kT, kWN, kWM>;
+  using S = MxTileShape<kT, kWN, kWM>;
   if constexpr (kT > 1) {
     if (rows <= 32 * (kT - 1) * kWM) {
-      gemm_tile<kQ, kT - 1, kWN, kWM, kSplit>(a, tn, m0, rows, part, tile, lds);
+      gemm_tile<kT - 1, kWN, kWM, kSplit>(a, tn, m0, rows, part, tile, lds);
       return;
     }
   }
@@ -187,7 +187,7 @@ __device__ __forceinline__ void gemm_tile(const MxGemmArgs& a, int tn, int m0, i
   p.c1 = a.Kc;
   if constexpr (kSplit) part_range(a.Kc, a.split.parts, part, p.c0, p.c1);
   f32x16_t acc[kQ][kT];
-  mx_tile_body<kQ, kT, kWN, kWM>(p, [&](int i) { return min(i, rows - 1); }, lds, acc);
+  mx_tile_body<kT, kWN, kWM>(p, [&](int i) { return min(i, rows - 1); }, lds, acc);
   if constexpr (kSplit) {
     f32x4_t(&v)[4 * kQ * kT] = reinterpret_cast<f32x4_t(&)[4 * kQ * kT]>(acc);
     if (!join_parts(a.split, tile, part, true, v, reinterpret_cast<int*>(lds))) return;
@@ -204,18 +204,18 @@ __device__ __forceinline__ void gemm_tile(const MxGemmArgs& a, int tn, int m0, i
     mx_store_tile<float>(lds, acc, [&](int row) { return row_of(row, float()); }, a.N - n0);
 }
 
-// tiles of 32 kQ kWN weight rows x kBM rows, kBM + kOver = 32 kT kWM: the last one takes up
+// tiles of 64 kWN weight rows x kBM rows, kBM + kOver = 32 kT kWM: the last one takes up
 // to kOver rows more (mx_tile.h)
-template <int kQ, int kT, int kWN, int kWM, int kOver, bool kSplit>
+template <int kT, int kWN, int kWM, int kOver, bool kSplit>
 __global__ __launch_bounds__(64 * kWN * kWM, 2) void mx_tile_kernel(MxGemmArgs a) {
-  using S = MxTileShape<kQ, kT, kWN, kWM>;
+  using S = MxTileShape<kT, kWN, kWM>;
   constexpr int kBM = S::BM - kOver;
   __shared__ __attribute__((aligned(128))) uint8_t lds[S::kLds];
   const int tiles = a.tiles_n * a.tiles_m, part = kSplit ? blockIdx.x / tiles : 0;
   int tn, tm;
   mx_tile_at(mx_xcd_tile(blockIdx.x - part * tiles, tiles), a.tiles_n, a.tiles_m, tn, tm);
   const int m0 = tm * kBM, rows = tm == a.tiles_m - 1 ? a.M - m0 : kBM;
-  gemm_tile<kQ, kT, kWN, kWM, kSplit>(a, tn, m0, rows, part, tm * a.tiles_n + tn, lds);
+  gemm_tile<kT, kWN, kWM, kSplit>(a, tn, m0, rows, part, tm * a.tiles_n + tn, lds);
 }
 
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -323,11 +323,11 @@ void launch_gemm(const moe_mx_dims& m, const void* x, const uint8_t* xq, const u
                                reinterpret_cast<f32x4_t*>(ws + kSplitCounterBytes)}};
   const unsigned grid = static_cast<unsigned>(p.tiles_n) * p.tiles_m * p.parts;
   if (p.form == kTile256)
-    mx_tile_kernel<2, 5, 4, 2, 64, false><<<grid, 512, 0, stream>>>(a);
+    mx_tile_kernel<5, 4, 2, 64, false><<<grid, 512, 0, stream>>>(a);
   else if (p.form == kTile128)
-    mx_tile_kernel<2, 2, 2, 2, 0, false><<<grid, 256, 0, stream>>>(a);
+    mx_tile_kernel<2, 2, 2, 0, false><<<grid, 256, 0, stream>>>(a);
   else if (p.form == kTile64)
-    mx_tile_kernel<2, 1, 1, 2, 0, true><<<grid, 128, 0, stream>>>(a);
+    mx_tile_kernel<1, 1, 2, 0, true><<<grid, 128, 0, stream>>>(a);
   else if (!x)
     launch_rows<kMxRowsQ>(a, p, grid, stream);
   else if (m.in_type == MOE_BF16)

@@ -70,10 +70,10 @@ __device__ __forceinline__ Group find_group(const MxGroupArgs& a, int b, int til
 // ---------------------------------------------------------------- many rows an expert
 
 // a tile of an expert's rows: `rows` of them from `first` on, up to 32 kT kWM
-template <int kQ, int kT, int kWN, int kWM, bool kGateUp>
+template <int kT, int kWN, int kWM, bool kGateUp>
 __device__ __forceinline__ void group_tile(const MxGroupArgs& a, const Group& gr, int tn, int first,
                                            int rows, uint8_t* lds) {
-  using S = MxTileShape<kQ, kT, kWN, kWM>;
+  using S = MxTileShape<kT, kWN, kWM>;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int m32 = lane & 31, hi = lane >> 5;
   const int wn = wave % kWN, wm = wave / kWN;
@@ -91,7 +91,7 @@ __device__ __forceinline__ void group_tile(const MxGroupArgs& a, const Group& gr
   p.c0 = 0;
   p.c1 = a.Kc;
   f32x16_t acc[kQ][kT];
-  mx_tile_body<kQ, kT, kWN, kWM>(
+  mx_tile_body<kT, kWN, kWM>(
       p,
       [&](int i) {
         i = min(i, rows - 1);
@@ -107,7 +107,7 @@ __device__ __forceinline__ void group_tile(const MxGroupArgs& a, const Group& gr
   };
   if constexpr (kGateUp) {
     // elements 4 j .. 4 j + 3 are (gate i, gate i + 1, up i, up i + 1) of i = 16 q + 4 j + 2 hi
-    const int I = a.N / 2, i0 = (p.rb0 + wn * (kQ / 2)) * 32;  // first intermediate of this wave
+    const int I = a.N / 2, i0 = (p.rb0 + wn) * 32;  // first intermediate of this wave
 #pragma unroll
     for (int q = 0; q < kQ; ++q)
 #pragma unroll
@@ -131,43 +131,39 @@ __device__ __forceinline__ void group_tile(const MxGroupArgs& a, const Group& gr
           [&](int row) { return row_of(row, uint16_t(), I, i0); }, I - i0);
       return;
     }
-    // MXFP4: a block is two 32-row units, 16 values of a lane and 16 of lane ^ 32; its codes
+    // MXFP4: a block is the two 32-row units, 16 values of a lane and 16 of lane ^ 32; its codes
     // meet in LDS, 16 bytes a row
-    constexpr int kB = kQ / 2;
-    uint8_t* o = lds + wave * (32 * kT * kB * 16);
+    uint8_t* o = lds + wave * (32 * kT * 16);
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
       const int row = m0 + t * 32 + m32;
+      float v[2][8];
+      uint32_t m = 0;
 #pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        float v[2][8];
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          v[i >> 3][i & 7] = acc[2 * b + (i >> 3)][t][4 * ((i & 7) >> 1) + (i & 1)];
-          m = max(m, __float_as_uint(v[i >> 3][i & 7]) & 0x7fffffffu);
-        }
-        m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32, kWave)));
-        const uint32_t byte = mx_scale_byte(m);
-        const float s = e8m0_scale(byte);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t c = mx_codes_or_zero(mx_codes(v[h], s), byte);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o[((t * 32 + m32) * kB + b) * 16 + 8 * h + 2 * j + hi] = static_cast<uint8_t>(c >> (8 * j));
-        }
-        if (hi == 0 && row < rows && i0 + 32 * b < I)
-          a.hs[static_cast<size_t>(first + row) * (I / 32) + i0 / 32 + b] = static_cast<uint8_t>(byte);
+      for (int i = 0; i < 16; ++i) {
+        v[i >> 3][i & 7] = acc[i >> 3][t][4 * ((i & 7) >> 1) + (i & 1)];
+        m = max(m, __float_as_uint(v[i >> 3][i & 7]) & 0x7fffffffu);
       }
+      m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32, kWave)));
+      const uint32_t byte = mx_scale_byte(m);
+      const float s = e8m0_scale(byte);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t c = mx_codes_or_zero(mx_codes(v[h], s), byte);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[(t * 32 + m32) * 16 + 8 * h + 2 * j + hi] = static_cast<uint8_t>(c >> (8 * j));
+      }
+      if (hi == 0 && row < rows && i0 < I)
+        a.hs[static_cast<size_t>(first + row) * (I / 32) + i0 / 32] = static_cast<uint8_t>(byte);
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < (32 * kT * kB + 63) / 64; ++i) {
-      const int at = i * 64 + lane, row = m0 + at / kB, b = at % kB;
-      if (at < 32 * kT * kB && row < rows && i0 + 32 * b < I)
+    for (int i = 0; i < (32 * kT + 63) / 64; ++i) {
+      const int at = i * 64 + lane, row = m0 + at;
+      if (at < 32 * kT && row < rows && i0 < I)
         *reinterpret_cast<u32x4_t*>(static_cast<uint8_t*>(a.out) +
-                                    static_cast<size_t>(first + row) * (I / 2) + i0 / 2 + 16 * b) =
+                                    static_cast<size_t>(first + row) * (I / 2) + i0 / 2) =
             *reinterpret_cast<const u32x4_t*>(o + at * 16);
     }
   } else {
@@ -181,22 +177,22 @@ __device__ __forceinline__ void group_tile(const MxGroupArgs& a, const Group& gr
 
 // A tile of `rows` rows runs on the narrowest instance that holds them, in steps of 32 kWM:
 // fewer MFMAs, down to where the weights' copies are its time.
-template <int kQ, int kT, int kWN, int kWM, bool kGateUp>
+template <int kT, int kWN, int kWM, bool kGateUp>
 __device__ __forceinline__ void group_tile_rows(const MxGroupArgs& a, const Group& gr, int tn, int first,
                                                 int rows, uint8_t* lds) {
   if constexpr (kT > 1) {
     if (rows <= 32 * (kT - 1) * kWM) {
-      group_tile_rows<kQ, kT - 1, kWN, kWM, kGateUp>(a, gr, tn, first, rows, lds);
+      group_tile_rows<kT - 1, kWN, kWM, kGateUp>(a, gr, tn, first, rows, lds);
       return;
     }
   }
-  group_tile<kQ, kT, kWN, kWM, kGateUp>(a, gr, tn, first, rows, lds);
+  group_tile<kT, kWN, kWM, kGateUp>(a, gr, tn, first, rows, lds);
 }
 
-// tiles of 32 kQ kWN weight rows x kBM rows, kBM + kOver = 32 kT kWM
-template <int kQ, int kT, int kWN, int kWM, int kOver, bool kGateUp>
+// tiles of 64 kWN weight rows x kBM rows, kBM + kOver = 32 kT kWM
+template <int kT, int kWN, int kWM, int kOver, bool kGateUp>
 __global__ __launch_bounds__(64 * kWN * kWM, 2) void mx_group_tile_kernel(MxGroupArgs a) {
-  using S = MxTileShape<kQ, kT, kWN, kWM>;
+  using S = MxTileShape<kT, kWN, kWM>;
   constexpr int kBM = S::BM - kOver;
   __shared__ __attribute__((aligned(128))) uint8_t lds[S::kLds];
   const int tiles_n = (a.N + S::BN - 1) / S::BN;
@@ -206,7 +202,7 @@ __global__ __launch_bounds__(64 * kWN * kWM, 2) void mx_group_tile_kernel(MxGrou
   int tn, tm;
   mx_tile_at(gr.tile, tiles_n, tiles_m, tn, tm);
   const int rows = tm == tiles_m - 1 ? gr.count - tm * kBM : kBM;
-  group_tile_rows<kQ, kT, kWN, kWM, kGateUp>(a, gr, tn, gr.first + tm * kBM, rows, lds);
+  group_tile_rows<kT, kWN, kWM, kGateUp>(a, gr, tn, gr.first + tm * kBM, rows, lds);
 }
 
 // ---------------------------------------------------------------- few rows of few experts
@@ -217,7 +213,7 @@ constexpr int kFewRows = 16, kFewWaves = 8;
 
 template <bool kGateUp>
 __global__ __launch_bounds__(64 * kFewWaves) void mx_group_few_kernel(MxGroupArgs a) {
-  __shared__ f32x4_t red[mx_rows_red<1, kFewWaves>()];
+  __shared__ f32x4_t red[mx_rows_red<1, kFewWaves>];
   const int blocks = a.N / kRowsPerBlock;
   const Group gr = find_group<kFewRows, 0>(a, blockIdx.x, blocks);
   if (gr.tile < 0) return;
@@ -227,7 +223,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_group_few_kernel(MxGroupArg
   const int m16 = lane & 15, g = lane >> 4;
   const MxRowsTile p = {a.w + gr.e * a.w_bytes + static_cast<size_t>(rb) * a.Kc * kMxTileBytes, a.Kc, 0, a.Kc,
                         m0, gr.count};
-  f32x4_t sum[1];  // waves 0 .. 3: of row tile `wave`
+  f32x4_t sum;  // waves 0 .. 3: of row tile `wave`
   mx_rows_body<1, kFewWaves, 2, kMxRowsQ>(
       p, nullptr, 0, a.xq, a.xs,
       [&](int i) {
@@ -238,7 +234,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_group_few_kernel(MxGroupArg
   if constexpr (!kGateUp) {
     const int row = m0 + m16, n = (4 * rb + wave) * 16 + 4 * g;
     if (wave < 4 && row < gr.count)
-      store4<true>(a.out, static_cast<size_t>(gr.first + row) * a.N + n, a.N - n, sum[0], a.type == MOE_BF16);
+      store4<true>(a.out, static_cast<size_t>(gr.first + row) * a.N + n, a.N - n, sum, a.type == MOE_BF16);
   } else {
     // the 32 intermediates of a row meet in LDS; then 4 threads a row, 8 values each
     constexpr int kPitch = 36;
@@ -246,8 +242,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_group_few_kernel(MxGroupArg
     __syncthreads();  // the sums have been read
     if (wave < 4) {
       float* to = h + m16 * kPitch + 8 * wave + 2 * g;
-      to[0] = mx_swiglu(sum[0][0], sum[0][2]);
-      to[1] = mx_swiglu(sum[0][1], sum[0][3]);
+      to[0] = mx_swiglu(sum[0], sum[2]);
+      to[1] = mx_swiglu(sum[1], sum[3]);
     }
     __syncthreads();
     const int row = threadIdx.x >> 2, j = threadIdx.x & 3, I = a.N / 2;
@@ -316,13 +312,13 @@ void launch_group(const moe_mx_group_dims& m, const MxGroupArgs& a, hipStream_t 
       mx_group_few_kernel<kGateUp><<<grid(kFewRows, 64), 64 * kFewWaves, 0, stream>>>(a);
       break;
     case kGroup64:
-      mx_group_tile_kernel<2, 1, 1, 2, 0, kGateUp><<<grid(64, 64), 128, 0, stream>>>(a);
+      mx_group_tile_kernel<1, 1, 2, 0, kGateUp><<<grid(64, 64), 128, 0, stream>>>(a);
       break;
     case kGroup128:
-      mx_group_tile_kernel<2, 2, 2, 2, 0, kGateUp><<<grid(128, 128), 256, 0, stream>>>(a);
+      mx_group_tile_kernel<2, 2, 2, 0, kGateUp><<<grid(128, 128), 256, 0, stream>>>(a);
       break;
     case kGroup256:
-      mx_group_tile_kernel<2, 5, 4, 2, 64, kGateUp><<<grid(256, 256), 512, 0, stream>>>(a);
+      mx_group_tile_kernel<5, 4, 2, 64, kGateUp><<<grid(256, 256), 512, 0, stream>>>(a);
       break;
   }
 }

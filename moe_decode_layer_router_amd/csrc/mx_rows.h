@@ -125,18 +125,17 @@ struct MxRowsTile {
 };
 
 template <int kTT, int kNW>
-constexpr int mx_rows_red() {
-  return kNW * (4 * kTT < kNW ? 4 * kTT : kNW) * 64;
-}
+constexpr int mx_rows_red = kNW * 4 * kTT * 64;
 
-// sum[e]: of tile i = kNW e + wave, i < 4 kTT: row tile i / kTT, token tile i % kTT. red:
+// sum: of tile i = wave < 4 kTT: row tile i / kTT, token tile i % kTT. red:
 // mx_rows_red elements; pass: kNW kTT kMxPass bytes (rows as they are only). row_of(token)
 // gives a token's row of x.
 template <int kTT, int kNW, int kRing, int kSrc, typename F>
 __device__ __forceinline__ void mx_rows_body(const MxRowsTile& p, const void* x, int K,
                                              const uint8_t* xq, const uint8_t* xs, F row_of,
-                                             uint8_t* pass, f32x4_t* red, f32x4_t (&sum)[(4 * kTT + kNW - 1) / kNW]) {
-  constexpr int kRT = 4;
+                                             uint8_t* pass, f32x4_t* red, f32x4_t& sum) {
+  constexpr int kRT = 4, kTiles = kRT * kTT;
+  static_assert(kTiles <= kNW, "a tile a wave");
   constexpr bool kRaw = kSrc != kMxRowsQ;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int m16 = lane & 15, g = lane >> 4;
@@ -225,21 +224,14 @@ __device__ __forceinline__ void mx_rows_body(const MxRowsTile& p, const void* x,
       }
     }
   }
-  constexpr int kEach = (kRT * kTT + kNW - 1) / kNW;
-  constexpr int kRound = kRT * kTT < kNW ? kRT * kTT : kNW;  // tiles a round
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) {
-    if (e) __syncthreads();
+  for (int i = 0; i < kTiles; ++i) red[(wave * kTiles + i) * 64 + lane] = acc[i / kTT][i % kTT];
+  __syncthreads();
+  sum = f32x4_t{0, 0, 0, 0};
+  if (wave < kTiles) {
+    sum = red[wave * 64 + lane];
 #pragma unroll
-    for (int i = 0; i < kNW && e * kNW + i < kRT * kTT; ++i)
-      red[(wave * kRound + i) * 64 + lane] = acc[(e * kNW + i) / kTT][(e * kNW + i) % kTT];
-    __syncthreads();
-    sum[e] = f32x4_t{0, 0, 0, 0};
-    if (e * kNW + wave < kRT * kTT) {
-      sum[e] = red[wave * 64 + lane];
-#pragma unroll
-      for (int q = 1; q < kNW; ++q) sum[e] += red[(q * kRound + wave) * 64 + lane];
-    }
+    for (int q = 1; q < kNW; ++q) sum += red[(q * kTiles + wave) * 64 + lane];
   }
 }
 

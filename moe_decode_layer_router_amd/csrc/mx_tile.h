@@ -1,7 +1,7 @@
 // mx_tile.h -- the MXFP4 product of many rows, tiled through LDS (device code).
 //
-// A workgroup of kWN x kWM waves takes 32 kQ kWN weight rows x 32 kT kWM rows
-// (tokens) and steps through the 128-K chunks; a wave holds kQ x kT accumulators of
+// A workgroup of kWN x kWM waves takes 64 kWN weight rows x 32 kT kWM rows
+// (tokens) and steps through the 128-K chunks; a wave holds 2 x kT accumulators of
 // 32 x 32, to which the 32x32x64 scaled MFMA adds half a chunk's products directly (alone,
 // with one wave a SIMD, it reached 6.4 PFLOP/s on random codes, the 16x16x128 one 4.5).
 //
@@ -13,7 +13,7 @@
 // token rows by whole lines, two chunks at once, and their scales four chunks at once, in
 // rings of two.
 //
-// A step is one chunk: 2 kQ units of kT MFMAs, unit (h, q) being half h of the chunk and
+// A step is one chunk: 4 units of kT MFMAs, unit (h, q) being half h of the chunk and
 // 32 weight rows. Its weight operand is read from LDS two units ahead; the tokens'
 // operands of a step stay in registers, replaced by the next step's in the last two units.
 // One barrier a step, in front of those: each wave has waited for its own copies of step
@@ -38,6 +38,7 @@ namespace moeblk {
 typedef __attribute__((address_space(3))) void* mx_lptr_t;
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
+constexpr int kQ = 2;  // units of 32 weight rows a wave: a row block
 constexpr int kWRing = 4, kXRing = 2;
 
 struct MxTile {
@@ -71,25 +72,24 @@ __device__ __forceinline__ f32x16_t mfma_mx32_at(int q, int h, u32x4_t a, u32x4_
   return h ? mfma_mx32<0, 2>(a, b, c, sa, sb) : mfma_mx32<0, 0>(a, b, c, sa, sb);
 }
 
-template <int kQ, int kT, int kWN, int kWM>
+template <int kT, int kWN, int kWM>
 struct MxTileShape {
   static constexpr int kWaves = kWN * kWM;
   static constexpr int BN = 32 * kQ * kWN, BM = 32 * kT * kWM;
   static constexpr int kWBuf = BN * 68, kXBuf = BM * 128, kSBuf = BM * 16;  // bytes
   static constexpr int kXAt = kWRing * kWBuf, kSAt = kXAt + kXRing * kXBuf;
   static constexpr int kLds = kSAt + kXRing * kSBuf + 1024;
-  static_assert(kQ % 2 == 0, "whole row blocks a wave");
   static_assert(BN / 16 % kWaves == 0 && BM / 8 % kWaves == 0, "whole pieces a wave");
   static_assert(kLds <= 160 * 1024, "LDS");
   // what the outputs pass through behind the last step
-  static_assert(kWaves * 32 * (32 * kQ * 4 + 16) <= kLds && kWaves * 32 * kT * (kQ / 2) * 16 <= kLds, "LDS");
+  static_assert(kWaves * 32 * (32 * kQ * 4 + 16) <= kLds && kWaves * 32 * kT * 16 <= kLds, "LDS");
 };
 
 // row_of(i) gives the row (from p.xq) of the tile's token i
-template <int kQ, int kT, int kWN, int kWM, typename F>
+template <int kT, int kWN, int kWM, typename F>
 __device__ __forceinline__ void mx_tile_body(const MxTile& p, F row_of, uint8_t* lds,
                                              f32x16_t (&acc)[kQ][kT]) {
-  using S = MxTileShape<kQ, kT, kWN, kWM>;
+  using S = MxTileShape<kT, kWN, kWM>;
   constexpr int kWaves = S::kWaves, BN = S::BN, BM = S::BM;
   constexpr int kW = BN / 16 / kWaves, kX = BM / 8 / kWaves;  // 1 KiB pieces a wave copies
   constexpr int kSW = (BN / 64 + kWaves - 1) / kWaves, kSX = (BM / 64 + kWaves - 1) / kWaves;
@@ -246,9 +246,9 @@ __device__ __forceinline__ void mx_tile_body(const MxTile& p, F row_of, uint8_t*
         // all but the batch of step k - 1 have landed: that is weights, tokens and scales of
         // step k + 1
         asm volatile("" ::: "memory");
-        // with two units a half the step's second tokens are not in use yet: wait for them,
-        // since others may replace them behind the barrier
-        if constexpr (kQ == 2) __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+        // the step's second tokens are not in use yet: wait for them, since others may replace
+        // them behind the barrier
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
         wait_loads<kOdd ? kEven : kOddLoads>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
@@ -368,7 +368,7 @@ __device__ __forceinline__ void mx_store(uint8_t* lds, Put put, Row row_of, int 
 }
 
 // a tile's outputs: this wave's weight rows in order
-template <typename T, int kQ, int kT, typename Row>
+template <typename T, int kT, typename Row>
 __device__ __forceinline__ void mx_store_tile(uint8_t* lds, const f32x16_t (&acc)[kQ][kT], Row row_of,
                                               int n_left) {
   const int hi = (threadIdx.x & 63) >> 5;
