@@ -9,8 +9,8 @@
 
 namespace {
 
-// the check in Python, which takes what is left to it here: objects that are no torch tensors
-// but answer like one, and sizes beyond 64 bits
+// the check in Python, which takes what is left to it here: objects that answer like a tensor but
+// are none, or of a subclass whose answers may be its own, and sizes beyond 64 bits
 PyObject* python_buf = nullptr;
 
 // buf(t, name, n, kinds, device): _buf in __init__.py
@@ -24,7 +24,7 @@ PyObject* buf(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     Py_INCREF(o);
     return o;
   }
-  if (!THPVariable_Check(o)) {
+  if (!THPVariable_CheckExact(o)) {  // a Parameter is taken as exact
     if (python_buf && PyObject_HasAttrString(o, "data_ptr")) return PyObject_Vectorcall(python_buf, args, nargs, nullptr);
     return PyErr_Format(PyExc_TypeError, "%U: %S is not a tensor, None or a pointer", name, Py_TYPE(o));
   }

@@ -54,6 +54,20 @@ def test_such_a_buffer_is_checked(bad):
         _buf()(Buffer(**bad), "x", 16, F32, 0)
 
 
+class Shard(torch.Tensor):
+    """A subclass with answers of its own."""
+
+    def numel(self):
+        return 4
+
+
+def test_a_subclass_answers_for_itself():
+    t = torch.zeros(16).as_subclass(Shard)
+    assert _buf()(t, "x", 4, F32, -1) == t.data_ptr()
+    with pytest.raises(ValueError, match="4 elements"):
+        _buf()(t, "x", 16, F32, -1)
+
+
 def test_other_objects_are_refused():
     for bad in ("s", 1.5, [torch.zeros(4)]):
         with pytest.raises((TypeError, AttributeError)):
