@@ -108,10 +108,10 @@ __device__ __forceinline__ float pick_weight(float v, bool on, int score, int re
   if (score == MOE_SCORE_SIGMOID) {
     const float top = renorm ? row_max(on ? v : -INFINITY) : 0.0f;
     m = top == -INFINITY ? 0.0f : fminf(top, 0.0f);
-    const float r = 1.0f / (1.0f + exp_near(-fabsf(v)));
-    a = exp_near(fminf(v, 0.0f) - m) * r;
+    const float e = exp_near(-fabsf(v));
+    a = exp_near(fminf(v, 0.0f) - m) / (1.0f + e);
     if (v != v) a = v;  // fminf drops a NaN
-    slope = (v >= 0.0f ? exp_near(-v) : 1.0f) * r;
+    slope = (v >= 0.0f ? e : 1.0f) / (1.0f + e);
     total = 1.0f;
   } else {
     if (renorm) {
