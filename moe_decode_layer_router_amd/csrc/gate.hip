@@ -14,7 +14,7 @@
 // upper 24 bits and the column (the lower one above), which all differ: a lane sorts its
 // four largest, a round takes the largest of the 16 lanes' first ones and the lane that had it
 // moves up (65536 x 256, topk 8: 750 vector instructions for four rows when each round went
-// through all words, 510 so). Where the lower 8 bits could matter (a pick out of
+// through all words, 529 so). Where the lower 8 bits could matter (a pick out of
 // order with the next, or keys at the border that agree in 24 bits only) the wave takes
 // the rounds on whole keys. The backward fills the row in LDS (zeros, or softmax's dense
 // part), adds the picks' terms there and stores it whole.

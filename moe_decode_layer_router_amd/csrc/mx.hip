@@ -14,8 +14,8 @@ namespace {
 // ---------------------------------------------------------------- quantise, read back
 //
 // One pass over the rows, bound by memory. Two lanes share a block: 16 columns each,
-// one DPP step for the maximum, 8 bytes of codes a lane. 16384 rows of 7168: 45 us from bf16
-// and 95 from fp32 (6.6 and 5.6 TB/s); 8 x 4096 2.4 us.
+// one DPP step for the maximum, 8 bytes of codes a lane. 16384 rows of 7168: 49 to 51 us from
+// bf16 and 95 from fp32 (6.0 and 5.6 TB/s); 8 x 4096 2.4 us.
 
 template <typename T>
 __global__ __launch_bounds__(256) void mx_quant_kernel(const T* __restrict__ x,
@@ -63,8 +63,9 @@ __global__ __launch_bounds__(256) void mx_quant_kernel(const T* __restrict__ x,
   if ((i & 1) == 0) s[row * (static_cast<size_t>(Kc) * 4) + (i >> 1)] = static_cast<uint8_t>(byte);
 }
 
-// 16 bytes of values a thread, stored past the caches: 16384 rows of 7168 in 42 us as bf16 and
-// 72 us as fp32 (7.1 and 7.4 TB/s); stores through them took 63 and 105.
+// 16 bytes of values a thread, stored past the caches: 16384 rows of 7168 in 42 us as bf16 (47
+// right behind their quantisation) and 73 us as fp32 (7.1 and 7.3 TB/s); stores through them took
+// 63 and 105.
 template <typename T>
 __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restrict__ q,
                                                          const uint8_t* __restrict__ s,

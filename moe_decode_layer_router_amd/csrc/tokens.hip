@@ -17,7 +17,8 @@ namespace {
 // chunks in front of its own. Within a run, a pick's rank among those of its
 // expert is a match over the bits of the expert's index (one ballot a bit). All
 // counts are integers, so no order of atomics shows. Latency bounds it: 512 picks 3.9 us in
-// one launch, 65536 picks 4.6 + 5.4 us.
+// one launch, 65536 picks 4.7 + 5.4 us, 524288 picks 11.7 us in all (256 experts held 13.8), 2^25 picks
+// 258 (762; 79 by the bytes): a wave then makes up to 128 rounds, one load of ids in flight.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
 constexpr int kMaxLocal = 256, kMaxChunks = 256;
 constexpr int kMinChunk = 2 * kSortThreads;  // picks
