@@ -561,7 +561,7 @@ def _t() -> _Torch:
     global _torch, _buf
     if _torch is None:
         _torch = _Torch()
-        _buf = _check_in_c(_buf)
+        _buf = _check_in_c(_python_buf)
     return _torch
 
 
@@ -595,6 +595,9 @@ def _buf(t, name: str, n: int, kinds, device: int):
     if t.numel() < n:
         raise ValueError(f"{name}: {t.numel()} elements, {n} are needed")
     return t.data_ptr()
+
+
+_python_buf = _buf  # _t() may put the check in C in _buf's place
 
 
 def _on(stream, T: _Torch, device: int) -> int:

@@ -98,3 +98,21 @@ for args, error in (((B(), "x", 1, None, 0), TypeError), ((torch.zeros(4), "x", 
     raise SystemExit(f"{args}: no {error}")
 """
     assert subprocess.run([sys.executable, "-c", code]).returncode == 0
+
+
+def test_two_first_calls():
+    """Two threads may both find the binding's state not yet there: the check in C still leaves
+    its rest to the one in Python, not to itself."""
+    code = """
+import moe_decode_layer_router_amd as mb
+class B:
+    get_device = lambda self: 0
+    is_contiguous = lambda self: True
+    numel = lambda self: 4
+    data_ptr = lambda self: 64
+for _ in range(2):
+    mb._torch = None
+    mb._t()
+raise SystemExit(0 if mb._buf(B(), "x", 4, None, 0) == 64 else 1)
+"""
+    assert subprocess.run([sys.executable, "-c", code], capture_output=True).returncode == 0
